@@ -38,6 +38,13 @@ QMV_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 MXFP4, CB2, CB3, CB4, MXFP8 = 0, 1, 2, 3, 4
 FORMATS = {"mxfp4": MXFP4, "cb2": CB2, "cb3": CB3, "cb4": CB4, "mxfp8": MXFP8}
+QMV_BF16, QMV_F16, QMV_F32 = 0, 1, 2
+TYPES = {"bf16": QMV_BF16, "f16": QMV_F16, "f32": QMV_F32,
+         torch.bfloat16: QMV_BF16, torch.float16: QMV_F16, torch.float32: QMV_F32}
+QMV_NORM_PLAIN, QMV_NORM_MXFP8, QMV_NORM_MXFP4, QMV_NORM_Q8 = 0, 1, 2, 3
+NORM_OUTS = {"plain": QMV_NORM_PLAIN, "mxfp8": QMV_NORM_MXFP8, "mxfp4": QMV_NORM_MXFP4, "q8": QMV_NORM_Q8}
+MAX_ROWS = 1 << 22
+MAX_SORT_EXPERTS = 1024
 MAX_NTOK = 16
 MAX_SLOTS = 128
 MAX_LAYER_SLOTS = 32
@@ -55,6 +62,10 @@ EXPORTS = (
     "qmv_device_status", "qmv_debug_wait_probe", "qmv_debug_chunk_rate", "qmv_debug_phase_entries",
     "qmv_debug_phase_probe",
     "qmv_debug_phase_read", "qmv_last_error", "qmv_version",
+    "qmv_act_mx_bytes", "qmv_act_mx_scale_offset", "qmv_act_mx_unpack", "qmv_quantize_act_mx", "qmv_rms_norm",
+    "qmv_mx_product", "qmv_mx_gate_up_swiglu", "qmv_moe_sort_workspace_bytes", "qmv_moe_sort", "qmv_moe_dispatch",
+    "qmv_moe_dispatch_mx", "qmv_moe_dispatch_grad", "qmv_moe_return", "qmv_moe_return_grad",
+    "qmv_moe_prefill_layer_workspace_bytes", "qmv_moe_prefill_layer",
 )
 
 
@@ -127,6 +138,22 @@ def _load() -> ctypes.CDLL:
         "qmv_debug_phase_entries": (SZ, []),
         "qmv_debug_phase_probe": (ctypes.c_int, [I32]),
         "qmv_debug_phase_read": (ctypes.c_int, [I32, P, SZ, I32]),
+        "qmv_act_mx_bytes": (SZ, [I32, I32, I32]),
+        "qmv_act_mx_scale_offset": (SZ, [I32, I32, I32]),
+        "qmv_act_mx_unpack": (ctypes.c_int, [I32, P, I32, I32, P, P]),
+        "qmv_quantize_act_mx": (ctypes.c_int, [I32, I32, P, I64, I32, I32, P, SZ, P]),
+        "qmv_rms_norm": (ctypes.c_int, [I32, P, I64, P, I64, P, I32, I32, ctypes.c_float, P, I32, P, SZ, P]),
+        "qmv_mx_product": (ctypes.c_int, [D, P, P, I32, P, I32, P, P]),
+        "qmv_mx_gate_up_swiglu": (ctypes.c_int, [D, P, P, I32, P, I32, P, SZ, P]),
+        "qmv_moe_sort_workspace_bytes": (SZ, [I32, I32, I32]),
+        "qmv_moe_sort": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P, SZ, P]),
+        "qmv_moe_dispatch": (ctypes.c_int, [I32, P, I64, I32, I32, I32, P, P, P]),
+        "qmv_moe_dispatch_mx": (ctypes.c_int, [I32, I32, P, I64, I32, I32, I32, P, P, SZ, P]),
+        "qmv_moe_dispatch_grad": (ctypes.c_int, [I32, P, I32, I32, I32, P, P, I64, P]),
+        "qmv_moe_return": (ctypes.c_int, [I32, P, P, I32, I32, I32, P, P, I64, P]),
+        "qmv_moe_return_grad": (ctypes.c_int, [I32, P, I64, P, P, I32, I32, I32, P, P, P, P]),
+        "qmv_moe_prefill_layer_workspace_bytes": (SZ, [D, D, I32, I32]),
+        "qmv_moe_prefill_layer": (ctypes.c_int, [D, P, D, P, I32, P, I64, P, P, I32, I32, P, SZ, P, P]),
         "qmv_last_error": (ctypes.c_char_p, []),
         "qmv_version": (ctypes.c_char_p, []),
     }
@@ -330,6 +357,109 @@ def qmv_moe_layer_combine(gate_up_desc: WDesc, w_gate_up, down_desc: WDesc, w_do
 
 def qmv_swiglu_bf16(g, u, h, n: int, stream=None) -> None:
     _check(lib.qmv_swiglu_bf16(_ptr(g), _ptr(u), _ptr(h), int(n), _stream(stream)))
+
+
+# --- many rows -------------------------------------------------------------------
+# dtype: "bf16", "f16", "f32", the torch dtype or the qmv_type value; strides
+# (ldx, ...) in elements; act buffers are uint8 tensors of qmv_act_mx_bytes.
+
+def _type(dtype) -> int:
+    return TYPES[dtype] if isinstance(dtype, (str, torch.dtype)) else int(dtype)
+
+
+def _fmt(fmt) -> int:
+    return FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+
+
+def qmv_act_mx_bytes(fmt, nrows: int, K: int) -> int:
+    return lib.qmv_act_mx_bytes(_fmt(fmt), nrows, K)
+
+
+def qmv_act_mx_scale_offset(fmt, nrows: int, K: int) -> int:
+    return lib.qmv_act_mx_scale_offset(_fmt(fmt), nrows, K)
+
+
+def qmv_act_mx_unpack(fmt, xq_host: np.ndarray, nrows: int, K: int):
+    """(codes [nrows][K * bits / 8], scales [nrows][K / 32]) of a host copy of an activation buffer."""
+    fmt = _fmt(fmt)
+    xq_host = np.ascontiguousarray(xq_host, dtype=np.uint8)
+    if xq_host.nbytes < qmv_act_mx_bytes(fmt, nrows, K):
+        raise ValueError("activation buffer is smaller than qmv_act_mx_bytes")
+    codes = np.empty((nrows, K * lib.qmv_code_bits(fmt) // 8), dtype=np.uint8)
+    scales = np.empty((nrows, K // 32), dtype=np.uint8)
+    _check(lib.qmv_act_mx_unpack(fmt, xq_host.ctypes.data, nrows, K, codes.ctypes.data, scales.ctypes.data))
+    return codes, scales
+
+
+def qmv_quantize_act_mx(fmt, dtype, x, ldx: int, nrows: int, K: int, xq, stream=None) -> None:
+    _check(lib.qmv_quantize_act_mx(_fmt(fmt), _type(dtype), _ptr(x), ldx, nrows, K, _ptr(xq), _nbytes(xq),
+                                   _stream(stream)))
+
+
+def qmv_rms_norm(dtype, x, ldx: int, residual, ldr: int, gain, nrows: int, K: int, eps: float, sum_out, out, y,
+                 stream=None) -> None:
+    """out: "plain", "mxfp8", "mxfp4" or "q8" (QMV_NORM_*); residual and sum_out may be None."""
+    _check(lib.qmv_rms_norm(_type(dtype), _ptr(x), ldx, _ptr(residual), ldr, _ptr(gain), nrows, K, eps, _ptr(sum_out),
+                            NORM_OUTS[out] if isinstance(out, str) else int(out), _ptr(y), _nbytes(y),
+                            _stream(stream)))
+
+
+def qmv_mx_product(desc: WDesc, w, xq, nrows: int, offsets, dtype, y, stream=None) -> None:
+    _check(lib.qmv_mx_product(ctypes.byref(desc), _ptr(w), _ptr(xq), nrows, _ptr(offsets), _type(dtype), _ptr(y),
+                              _stream(stream)))
+
+
+def qmv_mx_gate_up_swiglu(desc: WDesc, w_gate_up, xq, nrows: int, offsets, h_fmt, hq, stream=None) -> None:
+    _check(lib.qmv_mx_gate_up_swiglu(ctypes.byref(desc), _ptr(w_gate_up), _ptr(xq), nrows, _ptr(offsets), _fmt(h_fmt),
+                                     _ptr(hq), _nbytes(hq), _stream(stream)))
+
+
+def qmv_moe_sort_workspace_bytes(ntok: int, top_k: int, n_experts: int) -> int:
+    return lib.qmv_moe_sort_workspace_bytes(ntok, top_k, n_experts)
+
+
+def qmv_moe_sort(ids, ntok: int, top_k: int, n_experts: int, offsets, row_of_slot, slot_of_row, workspace=None,
+                 stream=None) -> None:
+    empty = workspace is None or _nbytes(workspace) == 0
+    _check(lib.qmv_moe_sort(_ptr(ids), ntok, top_k, n_experts, _ptr(offsets), _ptr(row_of_slot), _ptr(slot_of_row),
+                            None if empty else _ptr(workspace), 0 if empty else _nbytes(workspace), _stream(stream)))
+
+
+def qmv_moe_dispatch(dtype, x, ldx: int, ntok: int, top_k: int, K: int, row_of_slot, xs, stream=None) -> None:
+    _check(lib.qmv_moe_dispatch(_type(dtype), _ptr(x), ldx, ntok, top_k, K, _ptr(row_of_slot), _ptr(xs),
+                                _stream(stream)))
+
+
+def qmv_moe_dispatch_mx(fmt, dtype, x, ldx: int, ntok: int, top_k: int, K: int, row_of_slot, xq, stream=None) -> None:
+    _check(lib.qmv_moe_dispatch_mx(_fmt(fmt), _type(dtype), _ptr(x), ldx, ntok, top_k, K, _ptr(row_of_slot), _ptr(xq),
+                                   _nbytes(xq), _stream(stream)))
+
+
+def qmv_moe_dispatch_grad(dtype, dxs, ntok: int, top_k: int, K: int, row_of_slot, dx, ldx: int, stream=None) -> None:
+    _check(lib.qmv_moe_dispatch_grad(_type(dtype), _ptr(dxs), ntok, top_k, K, _ptr(row_of_slot), _ptr(dx), ldx,
+                                     _stream(stream)))
+
+
+def qmv_moe_return(dtype, ys, weights, ntok: int, top_k: int, N: int, row_of_slot, y, ldy: int, stream=None) -> None:
+    _check(lib.qmv_moe_return(_type(dtype), _ptr(ys), _ptr(weights), ntok, top_k, N, _ptr(row_of_slot), _ptr(y), ldy,
+                              _stream(stream)))
+
+
+def qmv_moe_return_grad(dtype, dy, ld_dy: int, ys, weights, ntok: int, top_k: int, N: int, row_of_slot, dys, dweights,
+                        stream=None) -> None:
+    _check(lib.qmv_moe_return_grad(_type(dtype), _ptr(dy), ld_dy, _ptr(ys), _ptr(weights), ntok, top_k, N,
+                                   _ptr(row_of_slot), _ptr(dys), _ptr(dweights), _stream(stream)))
+
+
+def qmv_moe_prefill_layer_workspace_bytes(gate_up_desc: WDesc, down_desc: WDesc, ntok: int, top_k: int) -> int:
+    return lib.qmv_moe_prefill_layer_workspace_bytes(ctypes.byref(gate_up_desc), ctypes.byref(down_desc), ntok, top_k)
+
+
+def qmv_moe_prefill_layer(gate_up_desc: WDesc, w_gate_up, down_desc: WDesc, w_down, dtype, x, ldx: int, ids, weights,
+                          ntok: int, top_k: int, workspace, y, stream=None) -> None:
+    _check(lib.qmv_moe_prefill_layer(ctypes.byref(gate_up_desc), _ptr(w_gate_up), ctypes.byref(down_desc),
+                                     _ptr(w_down), _type(dtype), _ptr(x), ldx, _ptr(ids), _ptr(weights), ntok, top_k,
+                                     _ptr(workspace), _nbytes(workspace), _ptr(y), _stream(stream)))
 
 
 def qmv_debug_block_sums(desc: WDesc, w, x, per_slot_x: int, ids, ntok: int, top_k: int, y, sums,

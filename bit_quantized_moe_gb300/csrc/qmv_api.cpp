@@ -119,9 +119,6 @@ int check_flags(int fmt, uint32_t flags, bool dbg, const char* name) {
   return QMV_OK;
 }
 
-// Rows of the gate/up-interleaved matrix of a projection with N rows.
-int gate_up_rows(int N) { return 2 * ((N + kRows / 2 - 1) / (kRows / 2) * (kRows / 2)); }
-
 // A gather of more than QMV_MAX_LAYER_SLOTS routed slots takes the sorted
 // tensor-core gather when its slots share experts: the tensor-core work item
 // decodes an expert's weights once for up to 16 of its slots, so it pays
@@ -300,6 +297,8 @@ int record_error(int code, const char* fmt, ...) {
   g_last_error = buf;
   return code;
 }
+
+int check_weight_desc(const qmv_wdesc* d) { return check_desc(d); }
 
 int device_sm_count() {
   const DevInfo* di = dev_info();
@@ -672,8 +671,8 @@ int qmv_debug_dequant(const qmv_wdesc* desc, const void* w, int32_t expert, floa
 int qmv_device_status(uint32_t* flags, int32_t clear) {
   if (!flags) return fail(QMV_EINVAL, "qmv_device_status: NULL pointer");
   uint32_t v = 0;
-  const uint32_t parts[7] = {status_mxfp4(clear), status_cb2(clear),   status_cb3(clear),   status_cb4(clear),
-                             status_mxfp8(clear), status_verify(clear), status_act(clear)};
+  const uint32_t parts[8] = {status_mxfp4(clear), status_cb2(clear),    status_cb3(clear), status_cb4(clear),
+                             status_mxfp8(clear), status_verify(clear), status_act(clear), status_mx_gemm(clear)};
   for (uint32_t p : parts) {
     if (p == 0xffffffffu) return cuda_fail(cudaGetLastError(), "qmv_device_status");
     v |= p;

@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "../../include/qmv.h"
 #include "qmv_layout.h"
 
 namespace qmv {
@@ -72,6 +73,108 @@ cudaError_t launch_combine(int dtype, const void* ys, const float* w, const int3
 cudaError_t launch_dequant(int fmt, int N, int K, const void* w, const uint32_t lut[4], float* out,
                            cudaStream_t s);
 
+// Output kinds of the norm (qmv_norm_out).
+enum : int { kNormPlain = 0, kNormMxfp8 = 1, kNormMxfp4 = 2, kNormQ8 = 3 };
+
+struct NormArgs {
+  int type = 0;                 // qmv_type of x, res, gain, sum and a plain y
+  const void* x = nullptr;
+  int64_t ldx = 0;              // elements between rows of x
+  const void* res = nullptr;    // null: no residual
+  int64_t ldr = 0;              // elements between rows of res and of sum
+  const void* gain = nullptr;
+  int64_t nrows = 0;
+  int K = 0;
+  float eps = 0.0f;
+  void* sum = nullptr;          // null: the sum is not stored
+  int out = 0;                  // kNorm*
+  void* y = nullptr;
+  uint64_t scale_offset = 0;    // MX outputs
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_rms_norm(const NormArgs& a);
+
+struct QuantArgs {
+  int fmt = 0, type = 0;
+  const void* x = nullptr;
+  int64_t ldx = 0;
+  int64_t ntok = 0;             // rows of x
+  int top_k = 1;
+  int K = 0;
+  const int32_t* row_of_slot = nullptr;   // null: row t of x is row t of xq
+  void* xq = nullptr;
+  int64_t nrows = 0;            // rows of xq
+  uint64_t scale_offset = 0;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_quantize_mx(const QuantArgs& a);
+
+struct SortArgs {
+  const int32_t* ids = nullptr;
+  int64_t nslots = 0;
+  int n_experts = 0;
+  int32_t *offsets = nullptr, *row_of_slot = nullptr, *slot_of_row = nullptr;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_moe_sort(const SortArgs& a);
+
+// Rows between the tokens' and the experts' order (qmv_route.cu).
+struct RouteArgs {
+  int type = 0;
+  int64_t ntok = 0;
+  int top_k = 1;
+  int K = 0;                    // columns
+  const int32_t* row_of_slot = nullptr;
+  const void* tok = nullptr;    // token-major rows read (x, dy)
+  int64_t ld_tok = 0;
+  const void* rows = nullptr;   // expert-major rows read (ys, dxs)
+  const float* weights = nullptr;   // null: every weight is 1
+  void* out_tok = nullptr;      // token-major rows written (y, dx)
+  int64_t ld_out = 0;
+  void* out_rows = nullptr;     // expert-major rows written (xs, dys)
+  float* dweights = nullptr;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_dispatch(const RouteArgs& a);      // out_rows[row] = tok[t]
+cudaError_t launch_return(const RouteArgs& a);        // out_tok[t] = sum_j weights * rows[row]
+cudaError_t launch_return_grad(const RouteArgs& a);   // out_rows[row] = weights * tok[t]; dweights = <rows[row], tok[t]>
+
+// Product of microscaled activations and weights on the tensor cores.
+struct MxGemmArgs {
+  int fmt = 0;
+  int N = 0, K = 0;             // of the packed matrix (gate/up interleaved: both projections' rows)
+  int n_experts = 1;
+  const void* w = nullptr;
+  const void* xq = nullptr;     // mx_act buffer of nrows rows
+  int64_t nrows = 0;
+  const int32_t* offsets = nullptr;   // [n_experts + 1] first row of each expert; null: every row, expert 0
+  int out_n = 0;                // output columns
+  int out_type = 0;             // qmv_type (plain outputs)
+  void* y = nullptr;            // [nrows][out_n], or the mx_act buffer of h (glu)
+  bool glu = false;             // store silu(gate) * up, quantized to h_fmt
+  int h_fmt = 0;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_mx_gemm(const MxGemmArgs& a);
+uint32_t status_mx_gemm(int clear);
+
+// Launch with programmatic stream serialization (the kernel begins with
+// griddepcontrol.wait); the legacy default stream has no such edges.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = s != nullptr ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 cudaError_t launch_wait_probe(unsigned long long limit_ns, cudaStream_t s);
 
 // Phase probe (build variant -DQMV_PHASE_PROBE, never the product build):
@@ -115,6 +218,9 @@ uint32_t status_verify(int clear);
 
 // Sets the calling thread's qmv_last_error() message and returns `code`.
 int record_error(int code, const char* fmt, ...);
+
+// QMV_OK, or the error code of an invalid weight descriptor (message recorded).
+int check_weight_desc(const qmv_wdesc* d);
 
 // Per-device cached properties.
 int device_sm_count();

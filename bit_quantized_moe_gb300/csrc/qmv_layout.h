@@ -183,4 +183,21 @@ QMV_HD inline uint64_t q8_vec_bytes(int K) {
   return (b + 15) / 16 * 16;
 }
 
+// Rows of the gate/up-interleaved matrix of a projection with N rows.
+QMV_HD inline int gate_up_rows(int N) { return 2 * ((N + kRows / 2 - 1) / (kRows / 2) * (kRows / 2)); }
+
+// Microscaled activations of nrows rows x K columns in an MX format: the codes
+// row after row (K * bits / 8 bytes, a multiple of 16), then the E8M0 scales as
+// 32-bit words [ceil(K / 128)][nrows]: byte b of word (w, r) is the scale of
+// columns [128 w + 32 b, + 32) of row r, 0 past K. A product tile's scales of
+// 128 columns are then consecutive words whatever row the tile starts at.
+QMV_HD inline uint64_t mx_row_bytes(int f, int K) { return (uint64_t)K * fmt_bits(f) / 8; }
+QMV_HD inline int mx_scale_words(int K) { return (K + 127) / 128; }
+QMV_HD inline uint64_t mx_scale_offset(int f, int64_t nrows, int K) {
+  return ((uint64_t)nrows * mx_row_bytes(f, K) + 127) / 128 * 128;
+}
+QMV_HD inline uint64_t mx_act_bytes(int f, int64_t nrows, int K) {
+  return mx_scale_offset(f, nrows, K) + ((uint64_t)nrows * mx_scale_words(K) * 4 + 15) / 16 * 16;
+}
+
 }  // namespace qmv

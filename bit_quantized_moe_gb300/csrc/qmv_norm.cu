@@ -1,0 +1,311 @@
+// qmv_norm.cu -- root-mean-square norm with the residual's addition and a
+// quantized output, and the microscaled quantizer of activation rows.
+#include "qmv_internal.h"
+#include "qmv_rows.cuh"
+
+namespace qmv {
+
+// ---------------------------------------------------------------------------
+// y = s * rsqrt(mean(s^2) + eps) * gain, s = x + r.
+//
+// One pass: a row's s stays in the registers of its TPR threads (V vectors of
+// 8 columns each), its squares are summed in fp32, and the same registers give
+// the output. s is rounded only where it is stored: the norm takes the fp32
+// sum. Bound by memory: 2 + 2 bytes in, 2 + 1 + 1/32 out per element for bf16
+// and MXFP8.
+//
+// VEC: every row starts on a 16-byte boundary and the width is a multiple of
+// 8. Otherwise (plain output only needs no group of 32) a thread's elements
+// are TPR apart, so that a warp still reads consecutive ones.
+// ---------------------------------------------------------------------------
+template <typename T, int OUT, int TPR, int V, bool VEC>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+rms_norm_kernel(NormArgs a) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  constexpr int kRowsPerCta = kThreads / TPR;
+  constexpr int kWarps = TPR / 32;
+  constexpr bool kCols = VEC || OUT != kNormPlain;   // a thread owns 8 consecutive columns
+  __shared__ float part[kThreads / 32];
+  const int tid = threadIdx.x % TPR;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / TPR;
+  const bool live = row < a.nrows;
+  const int K = a.K;
+  pdl_wait();
+  const T* x = static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
+  const T* res = a.res != nullptr ? static_cast<const T*>(a.res) + (live ? row : 0) * a.ldr : nullptr;
+  T* sum = a.sum != nullptr ? static_cast<T*>(a.sum) + (live ? row : 0) * a.ldr : nullptr;
+  const T* gain = static_cast<const T*>(a.gain);
+
+  float s[V][8];
+  float sq = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if constexpr (kCols) {
+      const int c = (j * TPR + tid) * 8;
+      const bool in = live && c < K;
+      if (in) {
+        load8<T, VEC>(x + c, s[j]);
+      } else {
+#pragma unroll
+        for (float& v : s[j]) v = 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (j * 8 + i) * TPR + tid;
+        s[j][i] = live && c < K ? to_f32(x[c]) : 0.0f;
+      }
+    }
+  }
+  if (res != nullptr) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if constexpr (kCols) {
+        const int c = (j * TPR + tid) * 8;
+        if (live && c < K) {
+          float r[8];
+          load8<T, VEC>(res + c, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[j][i] += r[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = (j * 8 + i) * TPR + tid;
+          if (live && c < K) s[j][i] += to_f32(res[c]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float p = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p = fmaf(s[j][i], s[j][i], p);
+    sq += p;
+  }
+  if (sum != nullptr) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if constexpr (kCols) {
+        const int c = (j * TPR + tid) * 8;
+        if (live && c < K) store8<T, VEC>(sum + c, s[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = (j * 8 + i) * TPR + tid;
+          if (live && c < K) sum[c] = from_f32<T>(s[j][i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+  if constexpr (kWarps > 1) {
+    if (lane == 0) part[threadIdx.x / 32] = sq;
+    __syncthreads();
+    const int w0 = (threadIdx.x / TPR) * kWarps;
+    sq = lane < kWarps ? part[w0 + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+  }
+  const float rs = 1.0f / sqrtf(sq / (float)K + a.eps);
+
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if constexpr (kCols) {
+      const int c = (j * TPR + tid) * 8;
+      const bool in = live && c < K;
+      float y[8];
+      if (in) {
+        float g[8];
+        load8<T, VEC>(gain + c, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = s[j][i] * rs * g[i];
+      } else {
+#pragma unroll
+        for (float& v : y) v = 0.0f;
+      }
+      if constexpr (OUT == kNormPlain) {
+        if (in) store8<T, VEC>(static_cast<T*>(a.y) + row * K + c, y);
+      } else {
+        uint32_t m = amax_bits8(y);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));   // four lanes: one group of 32
+        if constexpr (OUT == kNormQ8) {
+          // as quantize_q8_kernel: d = amax / 127, q = x / d rounded half away from zero
+          const float amax = __uint_as_float(m);
+          const float d = __fdiv_rn(amax, 127.0f);
+          const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+          if (in) {
+            uint8_t* out = static_cast<uint8_t*>(a.y) + row * q8_vec_bytes(K);
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float r = fminf(fmaxf(roundf(__fmul_rn(y[i], id)), -127.0f), 127.0f);
+              w[i >> 2] |= (uint32_t)(uint8_t)(int8_t)(int)r << (8 * (i & 3));
+            }
+            *reinterpret_cast<uint2*>(out + c) = make_uint2(w[0], w[1]);
+            if ((tid & 3) == 0) reinterpret_cast<__half*>(out + K)[c / 32] = __float2half_rn(d);
+          }
+        } else {
+          constexpr int FMT = OUT == kNormMxfp8 ? MXFP8 : MXFP4;
+          const uint32_t e = group_e8m0<FMT>(m);
+          uint32_t w[FMT == MXFP4 ? 1 : 2];
+          mx_codes8<FMT>(y, e, w);
+          uint8_t* out = static_cast<uint8_t*>(a.y);
+          if (in) store_codes8<FMT>(out + row * mx_row_bytes(FMT, K), c, w);
+          const uint32_t word = scale_word16(e, lane);
+          if ((lane & 15) == 0 && in) {
+            reinterpret_cast<uint32_t*>(out + a.scale_offset)[(int64_t)(c / 128) * a.nrows + row] = word;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (j * 8 + i) * TPR + tid;
+        if (live && c < K) static_cast<T*>(a.y)[row * K + c] = from_f32<T>(s[j][i] * rs * to_f32(gain[c]));
+      }
+    }
+  }
+  pdl_launch_dependents();
+}
+
+namespace {
+
+template <typename T, int OUT, int TPR, int V, bool VEC>
+cudaError_t norm_go(const NormArgs& a) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  constexpr int kRowsPerCta = kThreads / TPR;
+  return launch_pdl(rms_norm_kernel<T, OUT, TPR, V, VEC>, dim3((unsigned)((a.nrows + kRowsPerCta - 1) / kRowsPerCta)),
+                    dim3(kThreads), 0, a.stream, a);
+}
+
+// Threads of a row: as few as keep its columns in registers at up to 4 vectors
+// of 8 a thread, 8 vectors for the widest rows.
+template <typename T, int OUT, bool VEC>
+cudaError_t norm_width(const NormArgs& a) {
+  if (a.K <= 256) return norm_go<T, OUT, 32, 1, VEC>(a);
+  if (a.K <= 1024) return norm_go<T, OUT, 32, 4, VEC>(a);
+  if (a.K <= 4096) return norm_go<T, OUT, 256, 2, VEC>(a);
+  if (a.K <= 8192) return norm_go<T, OUT, 256, 4, VEC>(a);
+  if (a.K <= 32768) return norm_go<T, OUT, 1024, 4, VEC>(a);
+  return norm_go<T, OUT, 1024, 8, VEC>(a);
+}
+
+template <typename T, int OUT>
+cudaError_t norm_vec(const NormArgs& a) {
+  const int64_t unit = 16 / (int)sizeof(T);
+  const bool vec = a.K % 8 == 0 && a.ldx % unit == 0 && (a.ldr % unit == 0 || (a.res == nullptr && a.sum == nullptr));
+  return vec ? norm_width<T, OUT, true>(a) : norm_width<T, OUT, false>(a);
+}
+
+template <typename T>
+cudaError_t norm_out(const NormArgs& a) {
+  switch (a.out) {
+    case kNormMxfp8: return norm_vec<T, kNormMxfp8>(a);
+    case kNormMxfp4: return norm_vec<T, kNormMxfp4>(a);
+    case kNormQ8: return norm_vec<T, kNormQ8>(a);
+    default: return norm_vec<T, kNormPlain>(a);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormArgs& a) {
+  switch (a.type) {
+    case QMV_BF16: return norm_out<__nv_bfloat16>(a);
+    case QMV_F16: return norm_out<__half>(a);
+    default: return norm_out<float>(a);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Microscaled quantization of rows (and, with row_of_slot, their dispatch to
+// the experts' order). Sixteen lanes take 128 columns of one row: 16 bytes in
+// per lane (bf16), a group's maximum by two shuffles, codes and one scale word
+// out. A routed token is read and quantized once and written to its top_k
+// rows; a dropped slot's row (~row in row_of_slot) is written as zeros.
+// Bound by memory: 2 bytes in, 0.53 (E2M1) or 1.03 (E4M3) out per row.
+// ---------------------------------------------------------------------------
+template <typename T, int FMT, bool ROUTED, bool VEC>
+__global__ void __launch_bounds__(256)
+quantize_mx_kernel(QuantArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int words = mx_scale_words(a.K);
+  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const int64_t total = (int64_t)a.ntok * words;
+  const bool live = unit < total;
+  const int t = live ? (int)(unit / words) : 0;
+  const int kb = live ? (int)(unit - (int64_t)t * words) : 0;
+  const int c = kb * 128 + (lane & 15) * 8;
+  const bool in = live && c < a.K;
+  pdl_wait();
+  float v[8];
+  if (in) {
+    load8<T, VEC>(static_cast<const T*>(a.x) + (int64_t)t * a.ldx + c, v);
+  } else {
+#pragma unroll
+    for (float& f : v) f = 0.0f;
+  }
+  uint32_t m = amax_bits8(v);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t e = group_e8m0<FMT>(m);
+  uint32_t w[FMT == MXFP4 ? 1 : 2];
+  mx_codes8<FMT>(v, e, w);
+  const uint32_t word = scale_word16(e, lane);
+  uint8_t* out = static_cast<uint8_t*>(a.xq);
+  uint32_t* scales = reinterpret_cast<uint32_t*>(out + a.scale_offset) + (int64_t)kb * a.nrows;
+  const uint64_t row_bytes = mx_row_bytes(FMT, a.K);
+  if constexpr (!ROUTED) {
+    if (in) store_codes8<FMT>(out + (uint64_t)t * row_bytes, c, w);
+    if (live && (lane & 15) == 0) scales[t] = word;
+  } else if (live) {
+    for (int j = 0; j < a.top_k; ++j) {
+      const int r = __ldg(a.row_of_slot + (int64_t)t * a.top_k + j);
+      const bool keep = r >= 0;
+      const int row = keep ? r : ~r;
+      uint32_t z[FMT == MXFP4 ? 1 : 2];
+#pragma unroll
+      for (int i = 0; i < (FMT == MXFP4 ? 1 : 2); ++i) z[i] = keep ? w[i] : 0u;
+      if (in) store_codes8<FMT>(out + (uint64_t)row * row_bytes, c, z);
+      if ((lane & 15) == 0) scales[row] = keep ? word : 0u;
+    }
+  }
+  pdl_launch_dependents();
+}
+
+namespace {
+
+template <typename T, int FMT>
+cudaError_t quant_go(const QuantArgs& a) {
+  const int64_t units = (int64_t)a.ntok * mx_scale_words(a.K);
+  const dim3 grid((unsigned)((units + 15) / 16)), block(256);
+  const bool vec = a.ldx % (16 / (int)sizeof(T)) == 0;
+  if (a.row_of_slot != nullptr) {
+    return vec ? launch_pdl(quantize_mx_kernel<T, FMT, true, true>, grid, block, 0, a.stream, a)
+               : launch_pdl(quantize_mx_kernel<T, FMT, true, false>, grid, block, 0, a.stream, a);
+  }
+  return vec ? launch_pdl(quantize_mx_kernel<T, FMT, false, true>, grid, block, 0, a.stream, a)
+             : launch_pdl(quantize_mx_kernel<T, FMT, false, false>, grid, block, 0, a.stream, a);
+}
+
+template <typename T>
+cudaError_t quant_fmt(const QuantArgs& a) {
+  return a.fmt == MXFP4 ? quant_go<T, MXFP4>(a) : quant_go<T, MXFP8>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_mx(const QuantArgs& a) {
+  switch (a.type) {
+    case QMV_BF16: return quant_fmt<__nv_bfloat16>(a);
+    case QMV_F16: return quant_fmt<__half>(a);
+    default: return quant_fmt<float>(a);
+  }
+}
+
+}  // namespace qmv

@@ -122,6 +122,8 @@ typedef enum { QMV_MXFP4 = 0, QMV_CB2 = 1, QMV_CB3 = 2, QMV_CB4 = 3, QMV_MXFP8 =
 #define QMV_MAX_LAYER_SLOTS 32  /* routed slots per launch of the CUDA-core gather and gate/up fusion */
 #define QMV_MAX_N (1 << 20)
 #define QMV_MAX_K (1 << 16)
+#define QMV_MAX_ROWS (1 << 22)  /* rows, and routed slots, of the many-row calls below */
+#define QMV_MAX_SORT_EXPERTS 1024   /* experts of the many-row calls */
 
 /*
  * Weight descriptor. `lut` holds the codebook value of code c in lut[c] for
@@ -414,6 +416,170 @@ int qmv_moe_layer_noalloc(const qmv_wdesc* gate_up_desc, const void* w_gate_up_d
                           int32_t top_k, void* y_dev, uint32_t flags, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Many rows: what the same model needs on a prompt, a large batch or a
+ * training step over frozen experts, next to the decode calls above and on
+ * the same packed weights. Rows and slots up to QMV_MAX_ROWS; a call with no
+ * rows (or no tokens) is valid and writes nothing (qmv_moe_sort: offsets of
+ * zero). Rows of a strided operand are `ld` elements apart (ld >= the row's
+ * width); the others are contiguous.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element type of activations, gradients and outputs. */
+typedef enum { QMV_BF16 = 0, QMV_F16 = 1, QMV_F32 = 2 } qmv_type;
+
+/*
+ * Microscaled activations (the MX formats' own form): per row and group of 32
+ * columns one E8M0 scale and 32 E2M1 (QMV_MXFP4) or E4M3 (QMV_MXFP8) codes.
+ * For a group with largest magnitude m > 0 the scale is
+ * 2^(floor(log2 m) - emax), emax = 2 (E2M1) or 8 (E4M3), at least 2^-127;
+ * the codes are the scaled values rounded to nearest even, saturating at 6 or
+ * 448. A group of zeros has scale byte 0; a group with an infinity or a NaN
+ * has scale byte 255 (NaN) and codes 0, so that its products are NaN.
+ *
+ * Buffer: the codes, row after row (K * bits / 8 bytes each; E2M1 element k in
+ * byte k/2, low nibble first); at qmv_act_mx_scale_offset bytes the scales, as
+ * 32-bit words [ceil(K / 128)][nrows], byte b of word (w, r) the scale of
+ * columns [128 w + 32 b, + 32) of row r, zero past K.
+ * The size functions return 0 for an invalid format or shape.
+ */
+size_t qmv_act_mx_bytes(int32_t fmt, int32_t nrows, int32_t K);
+size_t qmv_act_mx_scale_offset(int32_t fmt, int32_t nrows, int32_t K);
+
+/* Host helper: split such a buffer (host copy) into canonical codes
+ * [nrows][K * bits / 8] and scales [nrows][K / 32]. */
+int qmv_act_mx_unpack(int32_t fmt, const void* xq_host, int32_t nrows, int32_t K, uint8_t* codes_host,
+                      uint8_t* scales_host);
+
+/*
+ * Quantize activations x_dev [nrows][K] (type: qmv_type, rows ldx apart) to
+ * such a buffer. K a multiple of 32.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+int qmv_quantize_act_mx(int32_t fmt, int32_t type, const void* x_dev, int64_t ldx, int32_t nrows, int32_t K,
+                        void* xq_dev, size_t xq_bytes, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and a choice of output:
+ *   s[r] = x[r] + residual[r]     (fp32; x[r] where residual_dev is NULL)
+ *   y[r] = s[r] / sqrt(mean(s[r]^2) + eps) * gain
+ * x, residual, gain [K] and sum have element type `type`; x rows are ldx
+ * elements apart, residual and sum rows ldr. sum_dev (may be NULL, may be
+ * residual_dev or x_dev itself where the strides agree) receives s rounded to
+ * `type`, the next layer's residual; the norm is taken of the unrounded sum.
+ * out selects y (y_bytes: its size):
+ *   QMV_NORM_PLAIN   `type` [nrows][K], any K
+ *   QMV_NORM_MXFP8   an MXFP8 activation buffer (qmv_act_mx_bytes), K % 32 == 0
+ *   QMV_NORM_MXFP4   an MXFP4 activation buffer
+ *   QMV_NORM_Q8      q8_1 vectors as qmv_quantize_act_q8 makes of an fp32 y
+ * The squares are summed in fp32 in an order that depends on K alone.
+ * Errors: QMV_EINVAL (also eps < 0 or NaN), QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+typedef enum { QMV_NORM_PLAIN = 0, QMV_NORM_MXFP8 = 1, QMV_NORM_MXFP4 = 2, QMV_NORM_Q8 = 3 } qmv_norm_out;
+int qmv_rms_norm(int32_t type, const void* x_dev, int64_t ldx, const void* residual_dev, int64_t ldr,
+                 const void* gain_dev, int32_t nrows, int32_t K, float eps, void* sum_dev, int32_t out, void* y_dev,
+                 size_t y_bytes, void* stream);
+
+/*
+ * Product of microscaled activations and weights on the tensor cores:
+ *   y[r] = W . x[r],   products of codes and scales exact, sums in fp32.
+ * desc: an MX format; w_dev the packed weights (qmv_pack_weights), xq_dev an
+ * activation buffer of the same format, of nrows rows. y_dev: out_type
+ * [nrows][N].
+ * offsets_dev == NULL: a dense product (n_experts 1). Otherwise a product
+ * grouped by expert: int32 [n_experts + 1], rows offsets[e] .. offsets[e + 1]
+ * of x (as qmv_moe_sort orders them) are multiplied by expert e's matrix; rows
+ * of no expert are not written. Offsets are read on the device; they must
+ * ascend, and are taken into [0, nrows].
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ECUDA.
+ */
+int qmv_mx_product(const qmv_wdesc* desc, const void* w_dev, const void* xq_dev, int32_t nrows,
+                   const int32_t* offsets_dev, int32_t out_type, void* y_dev, void* stream);
+
+/*
+ * Gate and up projections with the SwiGLU between them, over rows:
+ *   h[r] = silu(W_gate . x[r]) * (W_up . x[r])
+ * with the gate and up sums in fp32 and h quantized, without another rounding,
+ * to the activation buffer hq_dev (h_fmt: an MX format; nrows rows of N
+ * columns, N a multiple of 32), the down projection's input. desc describes one
+ * projection, w_gate_up_dev is packed by qmv_pack_gate_up; xq, nrows and
+ * offsets as qmv_mx_product.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+int qmv_mx_gate_up_swiglu(const qmv_wdesc* desc, const void* w_gate_up_dev, const void* xq_dev, int32_t nrows,
+                          const int32_t* offsets_dev, int32_t h_fmt, void* hq_dev, size_t hq_bytes, void* stream);
+
+/*
+ * Routed slots sorted by expert. Slot s = t * top_k + j goes to expert
+ * ids[s]; slots of an expert keep their order, and slots whose id is outside
+ * [0, n_experts) (dropped slots) come after all others.
+ *   offsets [n_experts + 1]: first row of each expert; offsets[n_experts] is
+ *       the number of slots that are not dropped
+ *   row_of_slot [ntok * top_k]: the slot's row; ~row (negative) for a dropped
+ *       slot, whose row the calls below write as zeros and read as nothing
+ *   slot_of_row [ntok * top_k]: the inverse
+ * workspace: qmv_moe_sort_workspace_bytes(...) bytes of device scratch, which
+ * may be 0 (workspace_dev may then be NULL). One launch; the same result every run.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+size_t qmv_moe_sort_workspace_bytes(int32_t ntok, int32_t top_k, int32_t n_experts);
+int qmv_moe_sort(const int32_t* ids_dev, int32_t ntok, int32_t top_k, int32_t n_experts, int32_t* offsets_dev,
+                 int32_t* row_of_slot_dev, int32_t* slot_of_row_dev, void* workspace_dev, size_t workspace_bytes,
+                 void* stream);
+
+/*
+ * Tokens to the experts' order, and its gradient:
+ *   qmv_moe_dispatch       xs[row_of_slot[t][j]] = x[t]     (type [ntok * top_k][K])
+ *   qmv_moe_dispatch_mx    the same rows quantized, as qmv_quantize_act_mx, to
+ *                          an activation buffer of ntok * top_k rows
+ *   qmv_moe_dispatch_grad  dx[t] = sum_j dxs[row_of_slot[t][j]]   (dx rows ldx apart)
+ * Sums are fp32 in slot order over the slots that are not dropped.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+int qmv_moe_dispatch(int32_t type, const void* x_dev, int64_t ldx, int32_t ntok, int32_t top_k, int32_t K,
+                     const int32_t* row_of_slot_dev, void* xs_dev, void* stream);
+int qmv_moe_dispatch_mx(int32_t fmt, int32_t type, const void* x_dev, int64_t ldx, int32_t ntok, int32_t top_k,
+                        int32_t K, const int32_t* row_of_slot_dev, void* xq_dev, size_t xq_bytes, void* stream);
+int qmv_moe_dispatch_grad(int32_t type, const void* dxs_dev, int32_t ntok, int32_t top_k, int32_t K,
+                          const int32_t* row_of_slot_dev, void* dx_dev, int64_t ldx, void* stream);
+
+/*
+ * The experts' rows back to their tokens, with the router's weights (fp32
+ * [ntok][top_k]) applied, and its gradients:
+ *   qmv_moe_return       y[t] = sum_j weights[t][j] * ys[row_of_slot[t][j]]   (y rows ldy apart)
+ *   qmv_moe_return_grad  dys[row_of_slot[t][j]] = weights[t][j] * dy[t],
+ *                        dweights[t][j] = <ys[row_of_slot[t][j]], dy[t]>      (fp32; dy rows ld_dy apart)
+ * over the slots that are not dropped; a dropped slot's row of dys and its
+ * weight's gradient are zero.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ECUDA.
+ */
+int qmv_moe_return(int32_t type, const void* ys_dev, const float* weights_dev, int32_t ntok, int32_t top_k, int32_t N,
+                   const int32_t* row_of_slot_dev, void* y_dev, int64_t ldy, void* stream);
+int qmv_moe_return_grad(int32_t type, const void* dy_dev, int64_t ld_dy, const void* ys_dev,
+                        const float* weights_dev, int32_t ntok, int32_t top_k, int32_t N,
+                        const int32_t* row_of_slot_dev, void* dys_dev, float* dweights_dev, void* stream);
+
+/*
+ * A MoE layer's expert FFN over many tokens, with microscaled activations:
+ * sort, dispatch with quantization, gate/up with SwiGLU and quantization,
+ * down, weighted return:
+ *   y[t] = sum_j weights[t][j] * W_down[e] . Q(silu(W_gate[e] . Q(x[t])) * (W_up[e] . Q(x[t]))),  e = ids[t][j],
+ * Q the quantization to the projection's MX format; MXFP4 and MXFP8 may be
+ * mixed as in qmv_moe_layer. The experts' rows are rounded to `type` before
+ * they are weighted. Descriptors and packed weights as qmv_moe_layer; x
+ * [ntok][K] of `type` (bf16 or fp16), rows ldx apart; y `type` [ntok][N_down].
+ * Five launches. workspace: as qmv_moe_layer.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+size_t qmv_moe_prefill_layer_workspace_bytes(const qmv_wdesc* gate_up_desc, const qmv_wdesc* down_desc, int32_t ntok,
+                                             int32_t top_k);
+int qmv_moe_prefill_layer(const qmv_wdesc* gate_up_desc, const void* w_gate_up_dev, const qmv_wdesc* down_desc,
+                          const void* w_down_dev, int32_t type, const void* x_dev, int64_t ldx,
+                          const int32_t* ids_dev, const float* weights_dev, int32_t ntok, int32_t top_k,
+                          void* workspace_dev, size_t workspace_bytes, void* y_dev, void* stream);
+
+/*
  * SwiGLU between the gate/up and down gathers of a gpt-oss-style MoE layer:
  * h[i] = silu(g[i]) * u[i], silu(z) = z / (1 + exp(-z)), bf16 in and out,
  * fp32 arithmetic, n elements ("perf(rocm): add an mxfp4 arm ...", "Problem /
@@ -476,7 +642,7 @@ int qmv_debug_dequant(const qmv_wdesc* desc, const void* w_dev, int32_t expert, 
 
 /*
  * Device-side status: bit flags set by kernels whose bounded waits gave up:
- * 1 (not used), 2 weight tile copy, 4 copy still in flight when giving
+ * 1 (not used), 2 weight tile copy (or another wait of a product over many rows), 4 copy still in flight when giving
  * up, 8 the wait probe; and 16: a CTA of a per-slot gather needed more
  * staged activation vectors than the launch planned for (a library bug; the
  * outputs of that call are wrong). No kernel here waits on another kernel, so
