@@ -17,15 +17,20 @@
 // chunk has a map of its own. The scales of a row tile lie lane by lane
 // ([lane][row]); a scale warp transposes them while the codes are in flight.
 //
-// One CTA per SM takes output tiles of 128 rows x 192 columns in turn. Warps:
-//   0      issues the TMA copies of codes, kStages steps of 128 bytes deep
+// One CTA per SM, or a pair of CTAs on two, takes output tiles of 128 rows (a
+// pair: 256) x 192 columns in turn. Warps:
+//   0      issues the TMA copies of codes, 128 bytes of every row a step.
+//          (Asking for the weights of 16 later steps in L2, by boxes or by
+//          whole tiles, was slower at every size measured: 132 rows of 32
+//          experts 57 -> 79 us.)
 //   1      copies a step's scales into tensor memory (tcgen05.cp) and issues
 //          its MMAs; two accumulators, so that the next tile's products run
 //          while a tile is stored
-//   4..7   the epilogue: a thread has a row's columns in order, so SwiGLU, a
-//          group's maximum and its quantization need no other thread
-//   8..11  read the scales of one step in four each, a step ahead, and write
-//          them as tcgen05.cp wants them
+//   4..11  the epilogue, one warpgroup an accumulator: a thread has a row's
+//          columns in order, so SwiGLU, a group's maximum and its quantization
+//          need no other thread
+//   2, 3, 12..15  read the scales of one step in six each, a turn ahead, and
+//          write them as tcgen05.cp wants them
 // Tiles of an expert follow one another along its rows, so that its weights
 // are read from memory once and again from L2.
 #include <cuda.h>
@@ -35,29 +40,38 @@
 
 namespace qmv {
 
-constexpr int kTileM = 128;        // rows of activations
+constexpr int kTileM = 128;        // rows of activations of one CTA
 constexpr int kTileN = 192;        // rows of weights: the output's columns
-constexpr int kGemmThreads = 384;
-constexpr int kStages = 5;
-constexpr int kScaleWarps = 4;
+constexpr int kGemmThreads = 512;
+constexpr int kScaleWarps = 6;      // warps 2, 3 and 12..15
+// Columns of 16-bit outputs that a thread parks in shared memory before its
+// warp stores them row by row, and the pitch of a row there (an odd number of
+// 16 bytes: no bank conflicts between rows).
+constexpr int kParkCols = 64;
+constexpr int kParkPitch = kParkCols * 2 + 16;
 
-template <int FMT>
+template <int FMT, bool PAIR>
 struct GemmFmt {
   static constexpr int step_k = FMT == MXFP4 ? 256 : 128;   // columns in 128 bytes of codes
   static constexpr int mma_k = FMT == MXFP4 ? 64 : 32;      // columns of one MMA
   static constexpr int atoms = step_k / 128;                // scale words of a row per step
   static constexpr int steps_per_chunk = kChunkK / step_k;
   static constexpr uint32_t a_bytes = kTileM * 128;
-  static constexpr uint32_t b_bytes = kTileN * 128;
+  static constexpr int b_rows = PAIR ? kTileN / 2 : kTileN;   // a pair's CTAs hold half of the weights each
+  static constexpr uint32_t b_bytes = b_rows * 128;
   // scales: 512 bytes hold the words of 128 rows, [row % 32][row / 32]
   static constexpr uint32_t sfa_bytes = atoms * 512;
   static constexpr uint32_t sfb_bytes = atoms * 1024;
-  static constexpr uint32_t stage_bytes = (a_bytes + b_bytes + sfa_bytes + sfb_bytes + 1023) / 1024 * 1024;
+  static constexpr uint32_t stage_bytes = a_bytes + b_bytes;
+  static constexpr uint32_t sf_bytes = sfa_bytes + sfb_bytes;
   static constexpr uint32_t sf_cols = atoms * 12;           // tensor memory columns of a stage's scales
+  static constexpr int stages = PAIR ? 5 : 4;
+  static constexpr int sf_stages = PAIR ? 10 : 6;           // steps that the scales may be ahead
+  static constexpr uint32_t park_bytes = 2 * kTileM * kParkPitch;
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol0 = 2 * kTileN;   // scales follow the two accumulators
-static_assert(kSfCol0 + kStages * GemmFmt<MXFP4>::sf_cols <= kTmemCols, "tensor memory");
+static_assert(kSfCol0 + GemmFmt<MXFP4, true>::stages * GemmFmt<MXFP4, true>::sf_cols <= kTmemCols, "tensor memory");
 
 struct GemmParams {
   const uint8_t* w;
@@ -72,15 +86,31 @@ struct GemmParams {
   int K, n_experts, out_n, out_type, n_tiles;
 };
 
+// PAIR: `bar` is the leader's barrier, as an address of the cluster.
+template <bool PAIR>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-               :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+  }
 }
+template <bool PAIR>
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int r, int t, int c, int e,
                                             uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-      :: "r"(dst), "l"(map), "r"(x), "r"(r), "r"(t), "r"(c), "r"(e), "r"(bar) : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        :: "r"(dst), "l"(map), "r"(x), "r"(r), "r"(t), "r"(c), "r"(e), "r"(bar) : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        :: "r"(dst), "l"(map), "r"(x), "r"(r), "r"(t), "r"(c), "r"(e), "r"(bar) : "memory");
+  }
 }
 
 // K-major operand in shared memory, rows of 128 bytes with the 128-byte
@@ -97,33 +127,103 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 // Instruction descriptor of the block-scaled kinds: element types (E2M1 is 1 in
 // kind::mxf4; E4M3 is 0 in kind::mxf8f6f4), N / 8, E8M0 scales (bit 23), M / 128,
 // and which byte of the scale words the instruction's first group uses.
-template <int FMT>
+template <int FMT, bool PAIR>
 __device__ __forceinline__ uint32_t block_idesc(uint32_t sf_byte) {
   constexpr uint32_t elem = FMT == MXFP4 ? 1u : 0u;
   constexpr uint32_t base = (elem << 7) | (elem << 10) | ((uint32_t)(kTileN >> 3) << 17) | (1u << 23) |
-                            ((uint32_t)(kTileM >> 7) << 27);
+                            ((uint32_t)((PAIR ? 2 * kTileM : kTileM) >> 7) << 27);
   return base | (sf_byte << 4) | (sf_byte << 29);
 }
 
-template <int FMT>
+#define QMV_BLOCK_MMA(GROUP, KIND)                                                              \
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n tcgen05.mma.cta_group::" GROUP       \
+               ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d), "l"(a), "l"(b),   \
+               "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                                   \
+               : "memory")
+
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_block_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                                  uint32_t sfb, uint32_t accumulate) {
   if constexpr (FMT == MXFP4) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    if constexpr (PAIR) QMV_BLOCK_MMA("2", "mxf4.block_scale.scale_vec::2X");
+    else QMV_BLOCK_MMA("1", "mxf4.block_scale.scale_vec::2X");
   } else {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    if constexpr (PAIR) QMV_BLOCK_MMA("2", "mxf8f6f4.block_scale.scale_vec::1X");
+    else QMV_BLOCK_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
   }
 }
+#undef QMV_BLOCK_MMA
 
+// PAIR: each CTA's tensor memory from the same place in its own shared memory.
+template <bool PAIR>
 __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
+  if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
 }
+// Arrives when this thread's earlier MMAs and copies are complete; PAIR: at the
+// same barrier of both CTAs.
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit_to(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(bar), "h"((uint16_t)3) : "memory");
+  } else {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+  }
+}
+// The address of `addr` in the cluster's CTA 0.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// As mbar_wait_bounded, for a barrier that the other CTA arrives at.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+  unsigned long long t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+    if (ok != 0) return true;
+    const unsigned long long now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) return false;
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+  if constexpr (PAIR) return mbar_wait_cluster(bar, parity, kWaitLimitNs);
+  else return mbar_wait_bounded(bar, parity, kWaitLimitNs);
+}
+// Whether a phase is already complete; does not wait.
+template <bool PAIR>
+__device__ __forceinline__ bool peek(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  }
+  return ok != 0;
 }
 __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
@@ -179,17 +279,18 @@ __device__ __forceinline__ float swiglu_fast(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-// Where one output tile lies.
+// Where a CTA's part of one output tile lies.
 struct Tile {
   int expert;
-  int row0;    // first row, and rows of the expert from there on
+  int row0;    // first row, and rows of the expert from there on (none: 0 or less)
   int rows;
   int n;       // column tile
 };
 
 // Output tile t: experts in order, the column tiles of an expert in order, the
 // row tiles of a column tile in order. first_tile[e]: tiles before expert e.
-__device__ __forceinline__ Tile tile_at(int t, const int* first_tile, const int* first_row, int n_experts) {
+template <bool PAIR>
+__device__ __forceinline__ Tile tile_at(int t, const int* first_tile, const int* first_row, int n_experts, int rank) {
   int lo = 0, hi = n_experts - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -197,14 +298,15 @@ __device__ __forceinline__ Tile tile_at(int t, const int* first_tile, const int*
     else hi = mid - 1;
   }
   const int rows = first_row[lo + 1] - first_row[lo];
-  const int mt = (rows + kTileM - 1) / kTileM;
+  constexpr int unit = PAIR ? 2 * kTileM : kTileM;
+  const int mt = (rows + unit - 1) / unit;
   const int i = t - first_tile[lo];
   Tile r;
   r.expert = lo;
   r.n = i / mt;
   const int m = i - r.n * mt;
-  r.row0 = first_row[lo] + m * kTileM;
-  r.rows = rows - m * kTileM;
+  r.row0 = first_row[lo] + m * unit + rank * kTileM;
+  r.rows = rows - m * unit - rank * kTileM;
   return r;
 }
 
@@ -213,13 +315,13 @@ __device__ __forceinline__ Tile tile_at(int t, const int* first_tile, const int*
 // of one or two row tiles of weights.
 template <int FMT>
 struct StepScales {
-  static constexpr int kItems = kTileN / 8 * GemmFmt<FMT>::atoms;   // (row tile, 128 columns) pairs
+  using F = GemmFmt<FMT, false>;
+  static constexpr int kItems = kTileN / 8 * F::atoms;   // (row tile, 128 columns) pairs
   static constexpr int kRounds = (kItems + 31) / 32;
-  uint32_t a[GemmFmt<FMT>::atoms][4];
+  uint32_t a[F::atoms][4];
   uint4 b[kRounds][2];
 
   __device__ __forceinline__ void load(const GemmParams& p, const Tile& t, int step, int lane) {
-    using F = GemmFmt<FMT>;
     const int words = mx_scale_words(p.K);
 #pragma unroll
     for (int k = 0; k < F::atoms; ++k) {
@@ -249,7 +351,6 @@ struct StepScales {
   }
 
   __device__ __forceinline__ void store(uint8_t* sfa, uint8_t* sfb, int lane) const {
-    using F = GemmFmt<FMT>;
 #pragma unroll
     for (int k = 0; k < F::atoms; ++k) {
       *reinterpret_cast<uint4*>(sfa + k * 512 + lane * 16) = make_uint4(a[k][0], a[k][1], a[k][2], a[k][3]);
@@ -263,10 +364,24 @@ struct StepScales {
         uint32_t w[8];
         transpose4(lo, *reinterpret_cast<uint32_t(*)[4]>(w));
         transpose4(hi, *reinterpret_cast<uint32_t(*)[4]>(w + 4));
-        const int row0 = item / F::atoms * 8;
-        uint8_t* atom = sfb + (item % F::atoms) * 1024 + (row0 / 128) * 512 + (row0 % 128) / 32 * 4;
+        // Row r of every item lies in the same eighth of the banks, so lanes take the rows in orders of their own:
+        // w[r] becomes the word of row r ^ x, x different in lanes whose items otherwise share banks.
+        const int x = F::atoms == 2 ? lane & 7 : (lane & 3) | (lane >> 4 & 1) << 2;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) *reinterpret_cast<uint32_t*>(atom + ((row0 + r) % 32) * 16) = w[r];
+        for (int bit = 1; bit < 8; bit <<= 1) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            if ((r & bit) == 0) {
+              const uint32_t u = w[r], v = w[r | bit];
+              w[r] = (x & bit) ? v : u;
+              w[r | bit] = (x & bit) ? u : v;
+            }
+          }
+        }
+        const int row0 = item / F::atoms * 8;
+        uint8_t* atom = sfb + (item % F::atoms) * 1024 + (row0 / 128) * 512 + (row0 % 32) * 16 + (row0 % 128) / 32 * 4;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) *reinterpret_cast<uint32_t*>(atom + (r ^ x) * 16) = w[r];
       }
     }
   }
@@ -292,40 +407,70 @@ __device__ __forceinline__ void store_columns(T* out, const uint32_t (&r)[32], i
   }
 }
 
+template <typename T>
+__device__ __forceinline__ void park_columns(uint8_t* at, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 v;
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = from_f32<T>(__uint_as_float(r[i * 8 + k]));
+    reinterpret_cast<uint4*>(at)[i] = v;
+  }
+}
+
 // HFMT < 0: y as out_type. Otherwise the columns are gate and up rows by fours
 // and silu(gate) * up is stored, quantized to HFMT.
-template <int FMT, int HFMT>
+// PAIR: two CTAs (a cluster) share a tile of 256 rows; the first, the leader,
+// issues the MMAs of both.
+template <int FMT, int HFMT, bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                const __grid_constant__ CUtensorMap map_last, const __grid_constant__ GemmParams p) {
-  using F = GemmFmt<FMT>;
+  using F = GemmFmt<FMT, PAIR>;
+  constexpr int kStages = F::stages;
+  constexpr int kCtas = PAIR ? 2 : 1;
   extern __shared__ uint8_t dyn[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
-  int* first_tile = reinterpret_cast<int*>(stages + kStages * F::stage_bytes);   // [n_experts + 1]
-  int* first_row = first_tile + p.n_experts + 1;                                 // [n_experts + 1]
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], done;
+  uint8_t* scales = stages + kStages * F::stage_bytes;   // [sf_stages][sf_bytes]
+  uint8_t* park = scales + F::sf_stages * F::sf_bytes;
+  int* first_tile = reinterpret_cast<int*>(park + F::park_bytes);   // [n_experts + 1]
+  int* first_row = first_tile + p.n_experts + 1;                    // [n_experts + 1]
+  // Barriers of a step: its codes and its scales have arrived, its MMAs are complete. The scales run up to 2 kStages
+  // steps ahead, the codes kStages; both wait for the MMAs of the step whose place they take.
+  __shared__ __align__(8) uint64_t full[F::stages], sf_full[F::sf_stages], used[F::sf_stages];
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done;
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&full[i]), 2);   // the copies' thread and the step's scale warp
-      mbar_init(smem_addr(&empty[i]), 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_addr(&full[i]), 1);
+    for (int i = 0; i < F::sf_stages; ++i) {
+      mbar_init(smem_addr(&sf_full[i]), kCtas);   // every CTA's scale warp
+      mbar_init(smem_addr(&used[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&acc_full[i]), 1);
-      mbar_init(smem_addr(&acc_empty[i]), 4);
+      mbar_init(smem_addr(&acc_empty[i]), 4 * kCtas);
     }
     mbar_init(smem_addr(&done), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(&tmem_base)),
-                 "r"(kTmemCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(&tmem_base)),
+                   "r"(kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(&tmem_base)),
+                   "r"(kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   pdl_wait();
   if (warp == 0) {
+    constexpr int unit = kCtas * kTileM;
     int tiles = 0;
     for (int e0 = 0; e0 < p.n_experts; e0 += 32) {
       const int e = e0 + lane;
@@ -339,7 +484,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         first_row[e] = lo;
         if (e == p.n_experts - 1) first_row[e + 1] = hi;
       }
-      int inc = (hi - lo + kTileM - 1) / kTileM * p.n_tiles;
+      int inc = (hi - lo + unit - 1) / unit * p.n_tiles;
       const int own = inc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -353,146 +498,229 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
   }
   tc_before_sync();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();   // both CTAs' barriers exist
   tc_after_sync();
   const uint32_t tmem = tmem_base;
   const int tiles = first_tile[p.n_experts];
   const int steps = p.chunks_full * F::steps_per_chunk + (p.last_lanes * 32 + F::step_k - 1) / F::step_k;
+  const int t0 = (int)blockIdx.x / kCtas, dt = (int)gridDim.x / kCtas;
+  const auto tile_of = [&](int t) { return tile_at<PAIR>(t, first_tile, first_row, p.n_experts, rank); };
   bool ok = true;
+
+  // Waits until the MMAs of step `it` - AHEAD are complete.
+  const auto wait_used = [&](int it, int ahead) {
+    const int j = it - ahead;
+    return j < 0 || wait_for<false>(smem_addr(&used[j % F::sf_stages]), (j / F::sf_stages) & 1);
+  };
 
   if (warp == 0) {
     // ---- copies of codes
     int it = 0;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile tile = tile_at(t, first_tile, first_row, p.n_experts);
-      for (int s = 0; s < steps; ++s, ++it) {
-        const int st = it % kStages;
-        if (!mbar_wait_bounded(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-        if (elect_one()) {
-          const uint32_t bar = smem_addr(&full[st]);
+    if (elect_one()) {
+      for (int t = t0; t < tiles && ok; t += dt) {
+        const Tile tile = tile_of(t);
+        const int rt = tile.n * (kTileN / 8) + rank * (F::b_rows / 8);
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int st = it % kStages;
+          if (!wait_used(it, kStages)) { ok = false; break; }
+          uint32_t bar = smem_addr(&full[st]);
           const uint32_t dst = smem_addr(stages + (uint32_t)st * F::stage_bytes);
-          mbar_arrive_expect_tx(bar, F::a_bytes + F::b_bytes);
-          tma_load_2d(dst, &map_x, s * 128, tile.row0, bar);
+          if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * (F::a_bytes + F::b_bytes));
+          if constexpr (PAIR) bar = leader_addr(bar);
+          tma_load_2d<PAIR>(dst, &map_x, s * 128, tile.row0, bar);
           const int chunk = s / F::steps_per_chunk;
           const int x = (s % F::steps_per_chunk) * 128;
           if (chunk < p.chunks_full) {
-            tma_load_5d(dst + F::a_bytes, &map_w, x, 0, tile.n * (kTileN / 8), chunk, tile.expert, bar);
+            tma_load_5d<PAIR>(dst + F::a_bytes, &map_w, x, 0, rt, chunk, tile.expert, bar);
           } else {
-            tma_load_5d(dst + F::a_bytes, &map_last, x, 0, tile.n * (kTileN / 8), 0, tile.expert, bar);
+            tma_load_5d<PAIR>(dst + F::a_bytes, &map_last, x, 0, rt, 0, tile.expert, bar);
           }
         }
-        __syncwarp();
       }
     }
+    __syncwarp();
+    it = __reduce_max_sync(0xffffffffu, it);
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) {   // leave no copy in flight
-      for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
-        if (!mbar_wait_bounded(smem_addr(&full[i % kStages]), (i / kStages) & 1, kDrainLimitNs) && lane == 0) {
-          set_status(kStatusDrain);
+      if constexpr (PAIR) {
+        const unsigned long long from = global_timer_ns();   // the copies report to the leader: give them their time
+        while (global_timer_ns() - from < kDrainLimitNs) {}
+      } else {
+        for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
+          if (!mbar_wait_bounded(smem_addr(&full[i % kStages]), (i / kStages) & 1, kDrainLimitNs) && lane == 0) {
+            set_status(kStatusDrain);
+          }
         }
       }
     }
   } else if (warp == 1) {
-    // ---- products
-    int it = 0, n = 0;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
-      const int acc = n & 1;
-      if (!mbar_wait_bounded(smem_addr(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-      tc_after_sync();
-      const uint32_t d = tmem + (uint32_t)(acc * kTileN);
-      for (int s = 0; s < steps; ++s, ++it) {
-        const int st = it % kStages;
-        if (!mbar_wait_bounded(smem_addr(&full[st]), (it / kStages) & 1, kWaitLimitNs)) { ok = false; break; }
+    // ---- products. Everything here is the same in all lanes, and the compiler knows it (counts come by shuffle,
+    // conditions by vote): addresses and descriptors stay in uniform registers, and one lane issues.
+    if (rank == 0) {
+      const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t code0 = smem_addr(stages), scale0 = smem_addr(scales);
+      int st = 0, ss = 0;                   // places of the step's codes and scales,
+      uint32_t st_phase = 0, ss_phase = 0;  // and their barriers' phases
+      // a step's barriers are looked at before the step before it is issued: the look's latency is then hidden
+      bool ready = false;
+      for (int n = 0; n < my_tiles && ok; ++n) {
+        const int acc = n & 1;
+        if (!__all_sync(0xffffffffu, wait_for<PAIR>(smem_addr(&acc_empty[acc]), ((n >> 1) & 1) ^ 1))) { ok = false; break; }
         tc_after_sync();
-        if (elect_one()) {
-          const uint32_t a0 = smem_addr(stages + (uint32_t)st * F::stage_bytes);
-          const uint32_t b0 = a0 + F::a_bytes, sfa = b0 + F::b_bytes, sfb = sfa + F::sfa_bytes;
-          const uint32_t sf = tmem + kSfCol0 + (uint32_t)st * F::sf_cols;
-#pragma unroll
-          for (int k = 0; k < F::atoms; ++k) {
-            scales_to_tmem(sf + (uint32_t)k * 12, scale_desc(sfa + (uint32_t)k * 512));
-            scales_to_tmem(sf + (uint32_t)k * 12 + 4, scale_desc(sfb + (uint32_t)k * 1024));
-            scales_to_tmem(sf + (uint32_t)k * 12 + 8, scale_desc(sfb + (uint32_t)k * 1024 + 512));
+        const uint32_t d = tm + (uint32_t)(acc * kTileN);
+        int left = p.K;
+        for (int s = 0; s < steps; ++s, left -= F::step_k) {
+          if (!ready && !__all_sync(0xffffffffu, wait_for<PAIR>(smem_addr(&sf_full[ss]), ss_phase) &&
+                                                     wait_for<false>(smem_addr(&full[st]), st_phase))) {
+            ok = false;
+            break;
           }
-          const int left = p.K - s * F::step_k;
+          tc_after_sync();
+          const uint32_t a0 = code0 + (uint32_t)st * F::stage_bytes, b0 = a0 + F::a_bytes;
+          const uint32_t sfa = scale0 + (uint32_t)ss * F::sf_bytes, sfb = sfa + F::sfa_bytes;
+          const uint32_t sf = tm + kSfCol0 + (uint32_t)st * F::sf_cols;
+          const uint32_t used_bar = smem_addr(&used[ss]);
+          if (++st == kStages) { st = 0; st_phase ^= 1; }
+          if (++ss == F::sf_stages) { ss = 0; ss_phase ^= 1; }
+          ready = __all_sync(0xffffffffu, peek<PAIR>(smem_addr(&sf_full[ss]), ss_phase) &
+                                              peek<false>(smem_addr(&full[st]), st_phase));
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < F::step_k / F::mma_k; ++j) {
-            if (j * F::mma_k < left) {
+            for (int k = 0; k < F::atoms; ++k) {
+              scales_to_tmem<PAIR>(sf + (uint32_t)k * 12, scale_desc(sfa + (uint32_t)k * 512));
+              scales_to_tmem<PAIR>(sf + (uint32_t)k * 12 + 4, scale_desc(sfb + (uint32_t)k * 1024));
+              scales_to_tmem<PAIR>(sf + (uint32_t)k * 12 + 8, scale_desc(sfb + (uint32_t)k * 1024 + 512));
+            }
+            const auto mma = [&](int j, uint32_t accumulate) {
               constexpr int per_atom = 128 / F::mma_k;
               const uint32_t col = sf + (uint32_t)(j / per_atom) * 12;
-              mma_block_scaled<FMT>(d, operand_desc(a0 + (uint32_t)j * 32), operand_desc(b0 + (uint32_t)j * 32),
-                                    block_idesc<FMT>((uint32_t)(j % per_atom) * (F::mma_k / 32)), col, col + 4,
-                                    (s > 0 || j > 0) ? 1u : 0u);
+              mma_block_scaled<FMT, PAIR>(d, operand_desc(a0 + (uint32_t)j * 32), operand_desc(b0 + (uint32_t)j * 32),
+                                          block_idesc<FMT, PAIR>((uint32_t)(j % per_atom) * (F::mma_k / 32)), col,
+                                          col + 4, accumulate);
+            };
+            mma(0, s > 0 ? 1u : 0u);
+            if (left >= F::step_k) {
+#pragma unroll
+              for (int j = 1; j < F::step_k / F::mma_k; ++j) mma(j, 1u);
+            } else {   // the ragged end of K
+#pragma unroll
+              for (int j = 1; j < F::step_k / F::mma_k; ++j) {
+                if (j * F::mma_k < left) mma(j, 1u);
+              }
             }
+            mma_commit_to<PAIR>(used_bar);
+            if (s == steps - 1) mma_commit_to<PAIR>(smem_addr(&acc_full[acc]));
           }
-          mma_commit_to(smem_addr(&empty[st]));
-          if (s == steps - 1) mma_commit_to(smem_addr(&acc_full[acc]));
         }
-        __syncwarp();
       }
+      if (elect_one()) mma_commit_to<PAIR>(smem_addr(&done));
+      __syncwarp();
+      if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
     }
-    if (elect_one()) mma_commit_to(smem_addr(&done));
-    __syncwarp();
-    if (!mbar_wait_bounded(smem_addr(&done), 0, kWaitLimitNs)) ok = false;
-  } else if (warp >= 8) {
-    // ---- scales: every fourth step, loaded one turn ahead of its slot in the ring
-    const int mine = warp - 8;
+  } else if (warp < 4 || warp >= 12) {
+    // ---- scales: every sixth step, loaded one turn ahead of its slot in the ring
     StepScales<FMT> cur;
-    int it = 0, t = blockIdx.x, s = mine;
+    int it = warp < 4 ? warp - 2 : warp - 10;
+    int t = t0, s = it;
     Tile tile{};
-    // step `mine`, `mine` + 4, ... of this CTA's steps, tile after tile
-    while (t < tiles && s >= steps) { s -= steps; t += gridDim.x; }
+    while (t < tiles && s >= steps) { s -= steps; t += dt; }
     if (t < tiles) {
-      tile = tile_at(t, first_tile, first_row, p.n_experts);
+      tile = tile_of(t);
       cur.load(p, tile, s, lane);
     }
-    it = mine;
     while (t < tiles) {
       int t2 = t, s2 = s + kScaleWarps;
-      while (t2 < tiles && s2 >= steps) { s2 -= steps; t2 += gridDim.x; }
+      while (t2 < tiles && s2 >= steps) { s2 -= steps; t2 += dt; }
       StepScales<FMT> next = cur;
       if (t2 < tiles) {
-        if (t2 != t) tile = tile_at(t2, first_tile, first_row, p.n_experts);
+        if (t2 != t) tile = tile_of(t2);
         next.load(p, tile, s2, lane);
       }
-      const int st = it % kStages;
-      if (!mbar_wait_bounded(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-      uint8_t* sfa = stages + (uint32_t)st * F::stage_bytes + F::a_bytes + F::b_bytes;
+      const int ss = it % F::sf_stages;
+      if (!wait_used(it, F::sf_stages)) { ok = false; break; }
+      uint8_t* sfa = scales + (uint32_t)ss * F::sf_bytes;
       cur.store(sfa, sfa + F::sfa_bytes, lane);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_one(smem_addr(&full[st]));
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(leader_addr(smem_addr(&sf_full[ss])));
+        else mbar_arrive_one(smem_addr(&sf_full[ss]));
+      }
       cur = next;
       t = t2;
       s = s2;
       it += kScaleWarps;
     }
-  } else if (warp >= 4) {
-    // ---- epilogue: thread = row 32 (warp - 4) + lane of the tile
-    const int quad = warp - 4;
-    int n = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
-      const int acc = n & 1;
-      const Tile tile = tile_at(t, first_tile, first_row, p.n_experts);
-      if (!mbar_wait_bounded(smem_addr(&acc_full[acc]), (n >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
+  } else {
+    // ---- epilogue: warps 4..7 take the first, third, ... tile, warps 8..11 the others, each its own accumulator;
+    // thread = row 32 (warp % 4) + lane of this CTA's part of the tile
+    const int quad = warp % 4, group = warp / 4 - 1;
+    uint8_t* warp_park = park + (uint32_t)(group * kTileM + quad * 32) * kParkPitch;
+    uint8_t* my_park = warp_park + lane * kParkPitch;
+    const int acc = group;
+    uint32_t phase = 0;
+    for (int t = t0 + group * dt; t < tiles; t += 2 * dt, phase ^= 1) {
+      const Tile tile = tile_of(t);
+      if (!wait_for<false>(smem_addr(&acc_full[acc]), phase)) { ok = false; break; }
       tc_after_sync();
       const int r = quad * 32 + lane;
       const bool live = r < tile.rows;
       const int64_t row = (int64_t)tile.row0 + r;
       const uint32_t d = tmem + (uint32_t)(acc * kTileN) + ((uint32_t)(quad * 32) << 16);
+      const auto release = [&] {   // the accumulator has been read
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR) mbar_arrive_cluster(leader_addr(smem_addr(&acc_empty[acc])));
+          else mbar_arrive_one(smem_addr(&acc_empty[acc]));
+        }
+      };
       if constexpr (HFMT < 0) {
-        const int size = p.out_type == QMV_F32 ? 4 : 2;
-        const bool vec = ((int64_t)p.out_n * size) % 16 == 0;
+        if (p.out_type != QMV_F32 && p.out_n % 8 == 0) {
+          // rows of whole 16 bytes: a warp parks its 32 rows and stores them row by row
+          uint8_t* out = static_cast<uint8_t*>(p.y) + ((int64_t)tile.row0 + quad * 32) * p.out_n * 2;
+          const int rows = min(32, tile.rows - quad * 32);
 #pragma unroll 1
-        for (int c = 0; c < kTileN; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(d + (uint32_t)c, v);
-          tmem_ld_wait(v);
-          const int n0 = tile.n * kTileN + c;
-          if (live && n0 < p.out_n) {
-            const int64_t at = row * p.out_n + n0;
-            if (p.out_type == QMV_BF16) store_columns(static_cast<__nv_bfloat16*>(p.y) + at, v, p.out_n - n0, vec);
-            else if (p.out_type == QMV_F16) store_columns(static_cast<__half*>(p.y) + at, v, p.out_n - n0, vec);
-            else store_columns(static_cast<float*>(p.y) + at, v, p.out_n - n0, vec);
+          for (int c = 0; c < kTileN; c += kParkCols) {
+#pragma unroll
+            for (int i = 0; i < kParkCols; i += 32) {
+              uint32_t v[32];
+              tmem_ld32(d + (uint32_t)(c + i), v);
+              tmem_ld_wait(v);
+              if (p.out_type == QMV_BF16) park_columns<__nv_bfloat16>(my_park + i * 2, v);
+              else park_columns<__half>(my_park + i * 2, v);
+            }
+            if (c + kParkCols == kTileN) release();
+            __syncwarp();
+            const int n0 = tile.n * kTileN + c;
+            const int vecs = min(kParkCols, p.out_n - n0) / 8;   // 16 bytes each
+#pragma unroll 4
+            for (int i = lane; i < 32 * (kParkCols / 8); i += 32) {
+              const int r = i / (kParkCols / 8), v = i % (kParkCols / 8);
+              if (r < rows && v < vecs) {
+                *reinterpret_cast<uint4*>(out + ((int64_t)r * p.out_n + n0) * 2 + v * 16) =
+                    *reinterpret_cast<const uint4*>(warp_park + r * kParkPitch + v * 16);
+              }
+            }
+            __syncwarp();
           }
+        } else {
+          const bool vec = p.out_type == QMV_F32 && p.out_n % 4 == 0;
+#pragma unroll 1
+          for (int c = 0; c < kTileN; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(d + (uint32_t)c, v);
+            tmem_ld_wait(v);
+            const int n0 = tile.n * kTileN + c;
+            if (live && n0 < p.out_n) {
+              const int64_t at = row * p.out_n + n0;
+              if (p.out_type == QMV_BF16) store_columns(static_cast<__nv_bfloat16*>(p.y) + at, v, p.out_n - n0, false);
+              else if (p.out_type == QMV_F16) store_columns(static_cast<__half*>(p.y) + at, v, p.out_n - n0, false);
+              else store_columns(static_cast<float*>(p.y) + at, v, p.out_n - n0, vec);
+            }
+          }
+          release();
         }
       } else {
         const uint64_t h_bytes = mx_row_bytes(HFMT, p.out_n);
@@ -503,6 +731,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
           tmem_ld32(d + (uint32_t)c + 32, v[1]);
           tmem_ld_wait(v[0]);
           tmem_ld_wait(v[1]);
+          if (c + 64 == kTileN) release();
           const int n0 = (tile.n * kTileN + c) / 2;   // a group of 32 columns of h
           if (live && n0 < p.out_n) {
             float h[4][8];
@@ -535,18 +764,20 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
           }
         }
       }
-      tc_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_one(smem_addr(&acc_empty[acc]));
     }
+    // the leader's last arrival has reached this CTA before it may exit
+    if (PAIR && ok && !wait_for<false>(smem_addr(&done), 0)) ok = false;
   }
   if (!ok && lane == 0) set_status(kStatusWaitTile);
   __syncwarp();
   pdl_launch_dependents();
+  tc_before_sync();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();   // neither CTA's memory is in use by the other any more
   if (warp == 1) {
     tc_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
   }
 }
 
@@ -580,9 +811,9 @@ bool encode(CUtensorMap* map, int rank, const void* base, const cuuint64_t* dims
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int HFMT>
+template <int FMT, int HFMT, bool PAIR>
 cudaError_t go(const MxGemmArgs& a) {
-  using F = GemmFmt<FMT>;
+  using F = GemmFmt<FMT, PAIR>;
   const Geometry g = make_geometry(FMT, a.N, a.K);
   const int lane_bytes = lane_code_bytes(FMT);
   GemmParams p = {};
@@ -615,7 +846,7 @@ cudaError_t go(const MxGemmArgs& a) {
     const cuuint32_t box[2] = {128, kTileM};
     if (!encode(&mx, 2, a.xq, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const cuuint32_t box[5] = {128, kRows, kTileN / kRows, 1, 1};
+  const cuuint32_t box[5] = {128, kRows, F::b_rows / kRows, 1, 1};
   // lanes of the map's chunks, chunks, first byte
   const auto weights = [&](CUtensorMap* m, int lanes, int chunks, uint64_t at) {
     const cuuint64_t row = (cuuint64_t)lanes * lane_bytes;
@@ -628,26 +859,51 @@ cudaError_t go(const MxGemmArgs& a) {
   if (p.chunks_full == 0) mw = ml;
   if (p.last_lanes == 0) ml = mw;
 
-  const size_t smem = 1024 + (size_t)kStages * F::stage_bytes + 2 * ((size_t)a.n_experts + 1) * sizeof(int);
+  const size_t smem =
+      1024 + (size_t)F::stages * F::stage_bytes + F::sf_stages * F::sf_bytes + F::park_bytes + 2 * ((size_t)a.n_experts + 1) * sizeof(int);
   g_launch_stage = "cudaFuncSetAttribute";
-  cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e =
+      cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // no more CTAs than tiles there can be: every expert has at most one partial row tile
-  const int64_t row_tiles = a.nrows / kTileM + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);
+  constexpr int ctas = PAIR ? 2 : 1;
+  const int64_t row_tiles = a.nrows / (ctas * kTileM) + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);
   int64_t grid = row_tiles * p.n_tiles;
-  if (grid > device_sm_count()) grid = device_sm_count();
+  if (grid > device_sm_count() / ctas) grid = device_sm_count() / ctas;
   g_launch_stage = "launch";
-  return launch_pdl(mx_gemm_kernel<FMT, HFMT>, dim3((unsigned)grid), dim3(kGemmThreads), smem, a.stream, mx, mw, ml, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(grid * ctas));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.stream != nullptr ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, HFMT, PAIR>, mx, mw, ml, p);
+}
+
+// Pairs of CTAs where an expert has more rows than one CTA's tile on average.
+bool use_pairs(const MxGemmArgs& a) { return a.nrows > (int64_t)kTileM * a.n_experts; }
+
+template <int FMT, bool PAIR>
+cudaError_t by_h(const MxGemmArgs& a) {
+  if (!a.glu) return go<FMT, -1, PAIR>(a);
+  return a.h_fmt == MXFP4 ? go<FMT, MXFP4, PAIR>(a) : go<FMT, MXFP8, PAIR>(a);
 }
 
 template <int FMT>
-cudaError_t by_h(const MxGemmArgs& a) {
-  if (!a.glu) return go<FMT, -1>(a);
-  return a.h_fmt == MXFP4 ? go<FMT, MXFP4>(a) : go<FMT, MXFP8>(a);
+cudaError_t by_pair(const MxGemmArgs& a) {
+  return use_pairs(a) ? by_h<FMT, true>(a) : by_h<FMT, false>(a);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_gemm(const MxGemmArgs& a) { return a.fmt == MXFP4 ? by_h<MXFP4>(a) : by_h<MXFP8>(a); }
+cudaError_t launch_mx_gemm(const MxGemmArgs& a) { return a.fmt == MXFP4 ? by_pair<MXFP4>(a) : by_pair<MXFP8>(a); }
 
 }  // namespace qmv

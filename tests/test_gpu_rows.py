@@ -272,7 +272,8 @@ def test_product_scale_range(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
-@pytest.mark.parametrize("counts", [[1], [0, 3, 0], [128, 0, 129, 1], [5, 300, 2, 0, 0, 77, 128], [0, 0], [1] * 40])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0], [128, 0, 129, 1], [5, 300, 2, 0, 0, 77, 128], [0, 0], [1] * 40,
+                                    [300, 0, 513, 129], [256, 1, 1000], [700]])
 def test_grouped_product(fmt, counts):
     """Rows of each expert by its own matrix; rows of no expert stay as they are."""
     E, N, K, tail = len(counts), 200, 1184, 5
@@ -293,7 +294,8 @@ def test_grouped_product(fmt, counts):
 
 
 @pytest.mark.parametrize("fmt,h_fmt", [("mxfp4", "mxfp4"), ("mxfp4", "mxfp8"), ("mxfp8", "mxfp4"), ("mxfp8", "mxfp8")])
-@pytest.mark.parametrize("counts,N,K", [([1], 32, 32), ([0, 130, 3], 96, 96), ([129, 7], 224, 1056), ([257], 2880, 288)])
+@pytest.mark.parametrize("counts,N,K", [([1], 32, 32), ([0, 130, 3], 96, 96), ([129, 7], 224, 1056), ([257], 2880, 288),
+                                        ([0, 400, 5, 200], 96, 1056)])
 def test_gate_up_swiglu(fmt, h_fmt, counts, N, K):
     """Gate and up sums are exact here, so h is known within the special functions' error."""
     E, rows = len(counts), sum(counts)
