@@ -39,37 +39,38 @@ rms_norm_kernel(NormArgs a) {
 
   float s[V][8];
   float sq = 0.0f;
+  if constexpr (kCols) {
+    // every load of the row is under way before the first is used
+    Raw8<T> rx[V], rr[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if constexpr (kCols) {
+    for (int j = 0; j < V; ++j) {
       const int c = (j * TPR + tid) * 8;
-      const bool in = live && c < K;
-      if (in) {
-        load8<T, VEC>(x + c, s[j]);
-      } else {
+      if (live && c < K) load_raw8<T, VEC>(x + c, rx[j]);
+      else clear_raw8(rx[j]);
+    }
 #pragma unroll
-        for (float& v : s[j]) v = 0.0f;
-      }
-    } else {
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * TPR + tid) * 8;
+      if (res != nullptr && live && c < K) load_raw8<T, VEC>(res + c, rr[j]);
+      else clear_raw8(rr[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j][i] = to_f32(rx[j].e[i]) + to_f32(rr[j].e[i]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = (j * 8 + i) * TPR + tid;
         s[j][i] = live && c < K ? to_f32(x[c]) : 0.0f;
       }
     }
-  }
-  if (res != nullptr) {
+    if (res != nullptr) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if constexpr (kCols) {
-        const int c = (j * TPR + tid) * 8;
-        if (live && c < K) {
-          float r[8];
-          load8<T, VEC>(res + c, r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[j][i] += r[i];
-        }
-      } else {
+      for (int j = 0; j < V; ++j) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int c = (j * 8 + i) * TPR + tid;
@@ -156,7 +157,7 @@ rms_norm_kernel(NormArgs a) {
           mx_codes8<FMT>(y, e, w);
           uint8_t* out = static_cast<uint8_t*>(a.y);
           if (in) store_codes8<FMT>(out + row * mx_row_bytes(FMT, K), c, w);
-          const uint32_t word = scale_word16(e, lane);
+          const uint32_t word = scale_word16(e);
           if ((lane & 15) == 0 && in) {
             reinterpret_cast<uint32_t*>(out + a.scale_offset)[(int64_t)(c / 128) * a.nrows + row] = word;
           }
@@ -230,49 +231,57 @@ cudaError_t launch_rms_norm(const NormArgs& a) {
 // rows; a dropped slot's row (~row in row_of_slot) is written as zeros.
 // Bound by memory: 2 bytes in, 0.53 (E2M1) or 1.03 (E4M3) out per row.
 // ---------------------------------------------------------------------------
-template <typename T, int FMT, bool ROUTED, bool VEC>
+template <typename T, int FMT, bool ROUTED, bool VEC, int U>
 __global__ void __launch_bounds__(256)
 quantize_mx_kernel(QuantArgs a) {
   const int lane = threadIdx.x & 31;
-  const int words = mx_scale_words(a.K);
-  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
-  const int64_t total = (int64_t)a.ntok * words;
-  const bool live = unit < total;
-  const int t = live ? (int)(unit / words) : 0;
-  const int kb = live ? (int)(unit - (int64_t)t * words) : 0;
-  const int c = kb * 128 + (lane & 15) * 8;
-  const bool in = live && c < a.K;
+  const unsigned words = (unsigned)mx_scale_words(a.K);
+  const unsigned total = (unsigned)a.ntok * words;   // at most 2^22 rows of 2^9 words
+  const unsigned unit0 = blockIdx.x * (16u * U) + threadIdx.x / 16u;   // U units of 128 columns, 16 apart
+  Raw8<T> raw[U];
+  unsigned t[U], kb[U];
   pdl_wait();
-  float v[8];
-  if (in) {
-    load8<T, VEC>(static_cast<const T*>(a.x) + (int64_t)t * a.ldx + c, v);
-  } else {
 #pragma unroll
-    for (float& f : v) f = 0.0f;
+  for (int i = 0; i < U; ++i) {
+    const unsigned unit = unit0 + 16u * i;
+    t[i] = unit < total ? unit / words : 0u;
+    kb[i] = unit - t[i] * words;
+    const int c = (int)(kb[i] * 128u) + (lane & 15) * 8;
+    if (unit < total && c < a.K) load_raw8<T, VEC>(static_cast<const T*>(a.x) + (int64_t)t[i] * a.ldx + c, raw[i]);
+    else clear_raw8(raw[i]);
   }
-  uint32_t m = amax_bits8(v);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const uint32_t e = group_e8m0<FMT>(m);
-  uint32_t w[FMT == MXFP4 ? 1 : 2];
-  mx_codes8<FMT>(v, e, w);
-  const uint32_t word = scale_word16(e, lane);
   uint8_t* out = static_cast<uint8_t*>(a.xq);
-  uint32_t* scales = reinterpret_cast<uint32_t*>(out + a.scale_offset) + (int64_t)kb * a.nrows;
   const uint64_t row_bytes = mx_row_bytes(FMT, a.K);
-  if constexpr (!ROUTED) {
-    if (in) store_codes8<FMT>(out + (uint64_t)t * row_bytes, c, w);
-    if (live && (lane & 15) == 0) scales[t] = word;
-  } else if (live) {
-    for (int j = 0; j < a.top_k; ++j) {
-      const int r = __ldg(a.row_of_slot + (int64_t)t * a.top_k + j);
-      const bool keep = r >= 0;
-      const int row = keep ? r : ~r;
-      uint32_t z[FMT == MXFP4 ? 1 : 2];
 #pragma unroll
-      for (int i = 0; i < (FMT == MXFP4 ? 1 : 2); ++i) z[i] = keep ? w[i] : 0u;
-      if (in) store_codes8<FMT>(out + (uint64_t)row * row_bytes, c, z);
-      if ((lane & 15) == 0) scales[row] = keep ? word : 0u;
+  for (int i = 0; i < U; ++i) {
+    const bool live = unit0 + 16u * i < total;
+    const int c = (int)(kb[i] * 128u) + (lane & 15) * 8;
+    const bool in = live && c < a.K;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = to_f32(raw[i].e[k]);
+    uint32_t m = amax_bits8(raw[i]);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t e = group_e8m0<FMT>(m);
+    uint32_t w[FMT == MXFP4 ? 1 : 2];
+    mx_codes8<FMT>(v, e, w);
+    const uint32_t word = scale_word16(e);
+    uint32_t* scales = reinterpret_cast<uint32_t*>(out + a.scale_offset) + (int64_t)kb[i] * a.nrows;
+    if constexpr (!ROUTED) {
+      if (in) store_codes8<FMT>(out + t[i] * row_bytes, c, w);
+      if (live && (lane & 15) == 0) scales[t[i]] = word;
+    } else if (live) {
+      for (int j = 0; j < a.top_k; ++j) {
+        const int r = __ldg(a.row_of_slot + (int64_t)t[i] * a.top_k + j);
+        const bool keep = r >= 0;
+        const int row = keep ? r : ~r;
+        uint32_t z[FMT == MXFP4 ? 1 : 2];
+#pragma unroll
+        for (int k = 0; k < (FMT == MXFP4 ? 1 : 2); ++k) z[k] = keep ? w[k] : 0u;
+        if (in) store_codes8<FMT>(out + (uint64_t)row * row_bytes, c, z);
+        if ((lane & 15) == 0) scales[row] = keep ? word : 0u;
+      }
     }
   }
   pdl_launch_dependents();
@@ -280,17 +289,25 @@ quantize_mx_kernel(QuantArgs a) {
 
 namespace {
 
+template <typename T, int FMT, bool ROUTED, bool VEC>
+cudaError_t quant_launch(const QuantArgs& a) {
+  // Two units in flight a thread once that still gives every SM threads enough
+  // (8192 x 7168 to MXFP4: 29.6 us; one unit 33.5, four 31.1, eight 43.8).
+  const int64_t units = a.ntok * mx_scale_words(a.K);
+  constexpr int U = 2;
+  if (units >= (int64_t)device_sm_count() * 16 * 8 * U) {
+    return launch_pdl(quantize_mx_kernel<T, FMT, ROUTED, VEC, U>, dim3((unsigned)((units + 16 * U - 1) / (16 * U))),
+                      dim3(256), 0, a.stream, a);
+  }
+  return launch_pdl(quantize_mx_kernel<T, FMT, ROUTED, VEC, 1>, dim3((unsigned)((units + 15) / 16)), dim3(256), 0,
+                    a.stream, a);
+}
+
 template <typename T, int FMT>
 cudaError_t quant_go(const QuantArgs& a) {
-  const int64_t units = (int64_t)a.ntok * mx_scale_words(a.K);
-  const dim3 grid((unsigned)((units + 15) / 16)), block(256);
   const bool vec = a.ldx % (16 / (int)sizeof(T)) == 0;
-  if (a.row_of_slot != nullptr) {
-    return vec ? launch_pdl(quantize_mx_kernel<T, FMT, true, true>, grid, block, 0, a.stream, a)
-               : launch_pdl(quantize_mx_kernel<T, FMT, true, false>, grid, block, 0, a.stream, a);
-  }
-  return vec ? launch_pdl(quantize_mx_kernel<T, FMT, false, true>, grid, block, 0, a.stream, a)
-             : launch_pdl(quantize_mx_kernel<T, FMT, false, false>, grid, block, 0, a.stream, a);
+  if (a.row_of_slot != nullptr) return vec ? quant_launch<T, FMT, true, true>(a) : quant_launch<T, FMT, true, false>(a);
+  return vec ? quant_launch<T, FMT, false, true>(a) : quant_launch<T, FMT, false, false>(a);
 }
 
 template <typename T>

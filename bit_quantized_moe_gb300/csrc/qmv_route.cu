@@ -26,7 +26,9 @@ constexpr int kSortWarps = 32;
 constexpr int kSortThreads = kSortWarps * 32;
 constexpr int kSortMaxCtas = 8;
 // Slots that one CTA sorts alone; more CTAs share larger calls.
-constexpr int64_t kSortSlotsPerCta = 4096;
+constexpr int64_t kSortSlotsPerCta = 1024;
+constexpr int kSortKept = 8;
+constexpr uint32_t kNoSlot = 0xffffu;
 
 __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t smem[];
@@ -39,13 +41,15 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs a) {
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
 
-  for (int i = threadIdx.x; i < kSortWarps * E1; i += kSortThreads) hist[i] = 0;
+  // this warp's slots [s0, s1), and the warps that have any
+  const int64_t parts = (int64_t)ctas * kSortWarps;
+  const int64_t per = (a.nslots + parts * 32 - 1) / (parts * 32) * 32;
+  const int used_warps = ctas > 1 ? kSortWarps : (int)((a.nslots + 31) / 32 < kSortWarps ? (a.nslots + 31) / 32 : kSortWarps);
+  const int hist_rows = used_warps <= 4 ? used_warps : kSortWarps;
+  for (int i = threadIdx.x; i < hist_rows * E1; i += kSortThreads) hist[i] = 0;
   __syncthreads();
   pdl_wait();
 
-  // this warp's slots [s0, s1)
-  const int64_t parts = (int64_t)ctas * kSortWarps;
-  const int64_t per = (a.nslots + parts * 32 - 1) / (parts * 32) * 32;
   const int64_t s0 = min(((int64_t)rank * kSortWarps + warp) * per, a.nslots);
   const int64_t s1 = min(s0 + per, a.nslots);
   uint32_t* mine = hist + warp * E1;
@@ -54,22 +58,50 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs a) {
     const int e = __ldg(a.ids + s);
     return e >= 0 && e < a.n_experts ? e : a.n_experts;
   };
-  for (int64_t s = s0; s < s1; s += 32) {
-    const int e = expert_of(s + lane);
+  // Counts 32 slots of a warp; the lane's own place among its warp's slots of its expert.
+  auto count = [&](int e) -> uint32_t {
     const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    const uint32_t before = e >= 0 ? mine[e] : 0u;
     __syncwarp();
+    if (e >= 0 && lane == __ffs(same) - 1) mine[e] = before + __popc(same);
+    __syncwarp();
+    return before + __popc(same & ((1u << lane) - 1u));
+  };
+  // A warp with at most 32 kSortKept slots keeps their experts and places; longer walks are made again.
+  uint32_t kept[kSortKept];   // expert (kNoSlot: none) | place << 16
+  const bool keep = per <= 32 * kSortKept;
+  if (keep) {
+#pragma unroll
+    for (int i = 0; i < kSortKept; ++i) kept[i] = (uint32_t)expert_of(s0 + 32 * i + lane) & kNoSlot;
+#pragma unroll
+    for (int i = 0; i < kSortKept; ++i) {
+      if (s0 + 32 * i < s1) kept[i] |= count(kept[i] == kNoSlot ? -1 : (int)kept[i]) << 16;
+    }
+  } else {
+    for (int64_t s = s0; s < s1; s += 32) count(expert_of(s + lane));
   }
   __syncthreads();
-  // counts of this CTA, and each warp's first place within them
-  for (int e = threadIdx.x; e < E1; e += kSortThreads) {
-    uint32_t n = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t c = hist[w * E1 + e];
-      hist[w * E1 + e] = n;
-      n += c;
+  // counts of this CTA, and each warp's first place within them: one warp an expert, lane = warp
+  if (used_warps <= 4) {   // few: a thread an expert
+    for (int e = threadIdx.x; e < E1; e += kSortThreads) {
+      uint32_t n = 0;
+      for (int w = 0; w < used_warps; ++w) {
+        const uint32_t c = hist[w * E1 + e];
+        hist[w * E1 + e] = n;
+        n += c;
+      }
+      total[e] = n;
     }
-    total[e] = n;
+  } else for (int e = warp; e < E1; e += kSortWarps) {
+    const uint32_t c = hist[lane * E1 + e];
+    uint32_t inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      inc += lane >= o ? v : 0u;
+    }
+    hist[lane * E1 + e] = inc - c;
+    if (lane == 31) total[e] = inc;
   }
   cluster.sync();
   // rows before each expert: an exclusive sum over experts of the cluster's counts
@@ -107,18 +139,25 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs a) {
     carry += __shfl_sync(0xffffffffu, ws, 31);
     __syncthreads();
   }
-  // ranks: the expert's first row, its slots in earlier CTAs and warps, and in this warp before this lane
-  for (int64_t s = s0; s < s1; s += 32) {
-    const int e = expert_of(s + lane);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0) {
-      const uint32_t row = start[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
-      a.row_of_slot[s + lane] = e < a.n_experts ? (int32_t)row : ~(int32_t)row;
-      a.slot_of_row[row] = (int32_t)(s + lane);
+  // a slot's row: its expert's first row, then the expert's slots in earlier CTAs, in earlier warps, in this warp
+  auto place = [&](int64_t s, int e, uint32_t row) {
+    if (e < 0) return;
+    a.row_of_slot[s] = e < a.n_experts ? (int32_t)row : ~(int32_t)row;
+    a.slot_of_row[row] = (int32_t)s;
+  };
+  if (keep) {
+#pragma unroll
+    for (int i = 0; i < kSortKept; ++i) {
+      const uint32_t e = kept[i] & kNoSlot;
+      if (e != kNoSlot) place(s0 + 32 * i + lane, (int)e, start[e] + mine[e] + (kept[i] >> 16));
     }
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  } else {
+    // `mine` goes on from the warp's first place
+    for (int64_t s = s0; s < s1; s += 32) {
+      const int e = expert_of(s + lane);
+      const uint32_t at = count(e);
+      place(s + lane, e, e >= 0 ? start[e] + at : 0u);
+    }
   }
   pdl_launch_dependents();
   cluster.sync();   // the others may still read this CTA's counts
@@ -169,125 +208,148 @@ struct Bytes<2> { using type = uint16_t; };
 // Slot values beyond the call's top_k are never used.
 constexpr int kTopK = QMV_MAX_TOPK;
 
+// Slots of a token whose rows are asked for together.
+constexpr int kSlotGroup = 4;
+static_assert(kTopK % kSlotGroup == 0, "part[] of the gradient");
+
+constexpr int kMoveThreads = 384;   // most threads of a mover's CTA
+
+// Arguments of the movers beside RouteArgs: accesses of a row, and between
+// rows of the token-major side; tokens of one pass of the grid.
+struct MoveShape {
+  int vecs;
+  int tokens;
+  int64_t ld;
+};
+
 template <int VB>
-__global__ void __launch_bounds__(512) dispatch_kernel(RouteArgs a, int64_t vecs, int64_t ld, int64_t grid_tokens) {
+__global__ void __launch_bounds__(kMoveThreads, 4) dispatch_kernel(RouteArgs a, MoveShape m) {
   using U = typename Bytes<VB>::type;
+  const int ntok = (int)a.ntok, top_k = a.top_k;
   pdl_wait();
-  for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.ntok; t += grid_tokens) {
-    int row[kTopK];
-#pragma unroll
-    for (int j = 0; j < kTopK; ++j) row[j] = j < a.top_k ? __ldg(a.row_of_slot + t * a.top_k + j) : 0;
-    const U* in = static_cast<const U*>(a.tok) + t * ld;
-    for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
+  for (int t = blockIdx.x * blockDim.y + threadIdx.y; t < ntok; t += m.tokens) {
+    const int32_t* rows = a.row_of_slot + (int64_t)t * top_k;
+    const U* in = static_cast<const U*>(a.tok) + t * m.ld;
+    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < m.vecs; v += gridDim.y * blockDim.x) {
       const U x = __ldg(in + v);
-#pragma unroll
-      for (int j = 0; j < kTopK; ++j) {
-        if (j < a.top_k) {
-          const int r = row[j];
-          static_cast<U*>(a.out_rows)[(int64_t)(r >= 0 ? r : ~r) * vecs + v] = r >= 0 ? x : U{};
-        }
+#pragma unroll 4
+      for (int j = 0; j < top_k; ++j) {
+        const int r = __ldg(rows + j);
+        static_cast<U*>(a.out_rows)[(int64_t)(r >= 0 ? r : ~r) * m.vecs + v] = r >= 0 ? x : U{};
       }
     }
   }
   pdl_launch_dependents();
 }
 
-template <typename T, int VB>
-__global__ void __launch_bounds__(512) return_kernel(RouteArgs a, int64_t vecs, int64_t ld, int64_t grid_tokens) {
+// SPLIT: blockIdx.y takes a part of the columns. Without it the kernel fits 40
+// registers and four CTAs an SM (8191 tokens x 4 slots of 2880: 41 us against 47).
+template <typename T, int VB, bool SPLIT>
+__global__ void __launch_bounds__(kMoveThreads, SPLIT ? 3 : 4) return_kernel(RouteArgs a, MoveShape m) {
   using U = typename Bytes<VB>::type;
   constexpr int EV = VB / (int)sizeof(T);
+  const int ntok = (int)a.ntok, top_k = a.top_k;
   pdl_wait();
-  for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.ntok; t += grid_tokens) {
-    int row[kTopK];
-    float w[kTopK];
-#pragma unroll
-    for (int j = 0; j < kTopK; ++j) {
-      row[j] = j < a.top_k ? __ldg(a.row_of_slot + t * a.top_k + j) : -1;
-      w[j] = j < a.top_k && a.weights != nullptr ? __ldg(a.weights + t * a.top_k + j) : 1.0f;
-    }
-    for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
-      U x[kTopK];
-#pragma unroll
-      for (int j = 0; j < kTopK; ++j) {
-        x[j] = row[j] >= 0 ? __ldg(static_cast<const U*>(a.rows) + (int64_t)row[j] * vecs + v) : U{};
-      }
+  for (int t = blockIdx.x * blockDim.y + threadIdx.y; t < ntok; t += m.tokens) {
+    const int32_t* rows = a.row_of_slot + (int64_t)t * top_k;
+    for (int v = (SPLIT ? blockIdx.y * blockDim.x : 0u) + threadIdx.x; v < m.vecs;
+         v += (SPLIT ? gridDim.y : 1u) * blockDim.x) {
+      const U* in = static_cast<const U*>(a.rows) + v;
       float acc[EV];
 #pragma unroll
       for (int i = 0; i < EV; ++i) acc[i] = 0.0f;
+      for (int j0 = 0; j0 < top_k; j0 += kSlotGroup) {
+        U x[kSlotGroup];
+        uint32_t live = 0;
 #pragma unroll
-      for (int j = 0; j < kTopK; ++j) {
-        if (row[j] >= 0) {
-          const T* e = reinterpret_cast<const T*>(&x[j]);
+        for (int j = 0; j < kSlotGroup; ++j) {
+          const int r = j0 + j < top_k ? __ldg(rows + j0 + j) : -1;
+          if (r >= 0) {
+            x[j] = __ldg(in + (int64_t)r * m.vecs);
+            live |= 1u << j;
+          }
+        }
 #pragma unroll
-          for (int i = 0; i < EV; ++i) acc[i] = fmaf(w[j], to_f32(e[i]), acc[i]);
+        for (int j = 0; j < kSlotGroup; ++j) {
+          if (live >> j & 1u) {
+            const float w = a.weights != nullptr ? __ldg(a.weights + (int64_t)t * top_k + j0 + j) : 1.0f;
+            const T* e = reinterpret_cast<const T*>(&x[j]);
+#pragma unroll
+            for (int i = 0; i < EV; ++i) acc[i] = fmaf(w, to_f32(e[i]), acc[i]);
+          }
         }
       }
       U out;
       T* o = reinterpret_cast<T*>(&out);
 #pragma unroll
       for (int i = 0; i < EV; ++i) o[i] = from_f32<T>(acc[i]);
-      static_cast<U*>(a.out_tok)[t * ld + v] = out;
+      static_cast<U*>(a.out_tok)[t * m.ld + v] = out;
     }
   }
   pdl_launch_dependents();
 }
 
-// dys[row] = w dy[t] and dw = <ys[row], dy[t]>: one CTA per token (blockDim.y
-// = 1), each thread's part of the top_k dot products reduced over the CTA in
+// dys[row] = w dy[t] and dw = <ys[row], dy[t]>: one CTA per token (or, of few
+// tokens, per token and group of slots), its slots in groups, each thread's part of a group's dot products reduced over the CTA in
 // a fixed order. A dropped slot's row of dys and its weight's gradient are 0.
 template <typename T, int VB>
-__global__ void __launch_bounds__(512) return_grad_kernel(RouteArgs a, int64_t vecs, int64_t ld, int64_t grid_tokens) {
+__global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs a, MoveShape m) {
   using U = typename Bytes<VB>::type;
   constexpr int EV = VB / (int)sizeof(T);
   __shared__ float part[kTopK][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int ntok = (int)a.ntok, top_k = a.top_k;
   pdl_wait();
-  for (int64_t t = blockIdx.x; t < a.ntok; t += grid_tokens) {
-    int row[kTopK];
-    float w[kTopK], dot[kTopK];
+  for (int t = blockIdx.x; t < ntok; t += m.tokens) {
+    const int32_t* rows = a.row_of_slot + (int64_t)t * top_k;
+    const float* weights = a.weights + (int64_t)t * top_k;
+    const U* grad = static_cast<const U*>(a.tok) + t * m.ld;
+    const int first = blockIdx.y * kSlotGroup, step = gridDim.y * kSlotGroup;
+    for (int j0 = first; j0 < top_k; j0 += step) {
+      float dot[kSlotGroup];
 #pragma unroll
-    for (int j = 0; j < kTopK; ++j) {
-      row[j] = j < a.top_k ? __ldg(a.row_of_slot + t * a.top_k + j) : 0;
-      w[j] = j < a.top_k ? __ldg(a.weights + t * a.top_k + j) : 0.0f;
-      dot[j] = 0.0f;
-    }
-    for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
-      const U g = __ldg(static_cast<const U*>(a.tok) + t * ld + v);
-      const T* ge = reinterpret_cast<const T*>(&g);
+      for (int j = 0; j < kSlotGroup; ++j) dot[j] = 0.0f;
+      for (int v = threadIdx.x; v < m.vecs; v += blockDim.x) {
+        const U g = __ldg(grad + v);
+        U y[kSlotGroup];
+        int row[kSlotGroup];
 #pragma unroll
-      for (int j = 0; j < kTopK; ++j) {
-        if (j < a.top_k) {
-          U out{};
-          const int64_t at = (int64_t)(row[j] >= 0 ? row[j] : ~row[j]) * vecs + v;
-          if (row[j] >= 0) {
-            const U y = __ldg(static_cast<const U*>(a.rows) + at);
-            const T* ye = reinterpret_cast<const T*>(&y);
-            T* oe = reinterpret_cast<T*>(&out);
+        for (int j = 0; j < kSlotGroup; ++j) {
+          row[j] = j0 + j < top_k ? __ldg(rows + j0 + j) : -1;
+          if (row[j] >= 0) y[j] = __ldg(static_cast<const U*>(a.rows) + (int64_t)row[j] * m.vecs + v);
+        }
+        const T* ge = reinterpret_cast<const T*>(&g);
 #pragma unroll
-            for (int i = 0; i < EV; ++i) {
-              const float d = to_f32(ge[i]);
-              dot[j] = fmaf(to_f32(ye[i]), d, dot[j]);
-              oe[i] = from_f32<T>(w[j] * d);
+        for (int j = 0; j < kSlotGroup; ++j) {
+          if (j0 + j < top_k) {
+            U out{};
+            if (row[j] >= 0) {
+              const float w = __ldg(weights + j0 + j);
+              const T* ye = reinterpret_cast<const T*>(&y[j]);
+              T* oe = reinterpret_cast<T*>(&out);
+#pragma unroll
+              for (int i = 0; i < EV; ++i) {
+                const float d = to_f32(ge[i]);
+                dot[j] = fmaf(to_f32(ye[i]), d, dot[j]);
+                oe[i] = from_f32<T>(w * d);
+              }
             }
+            static_cast<U*>(a.out_rows)[(int64_t)(row[j] >= 0 ? row[j] : ~row[j]) * m.vecs + v] = out;
           }
-          static_cast<U*>(a.out_rows)[at] = out;
         }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kTopK; ++j) {
-      if (j < a.top_k) {
+      for (int j = 0; j < kSlotGroup; ++j) {
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-        if (lane == 0) part[j][warp] = dot[j];
+        if (lane == 0) part[j0 + j][warp] = dot[j];
       }
     }
     __syncthreads();
-    if ((int)threadIdx.x < a.top_k) {
-      const int r = __ldg(a.row_of_slot + t * a.top_k + threadIdx.x);
+    if ((int)threadIdx.x < top_k && (int)threadIdx.x / kSlotGroup % gridDim.y == blockIdx.y) {
       float d = 0.0f;
       for (int i = 0; i < (int)blockDim.x / 32; ++i) d += part[threadIdx.x][i];
-      a.dweights[t * a.top_k + threadIdx.x] = r >= 0 ? d : 0.0f;
+      a.dweights[(int64_t)t * top_k + threadIdx.x] = __ldg(rows + threadIdx.x) >= 0 ? d : 0.0f;
     }
     __syncthreads();
   }
@@ -298,29 +360,37 @@ namespace {
 
 struct RowShape {
   int vb;            // bytes of an access
-  int64_t vecs, ld;  // accesses of a row, and between rows of the token-major side
+  MoveShape move;
   dim3 grid, block;
-  int64_t tokens;    // tokens of one pass of the grid
 };
 
 // Accesses as wide as the row's bytes and stride allow; a CTA's threads cover
-// a row in as few, evenly filled rounds as 512 threads need.
+// a row in as few, evenly filled rounds as kMoveThreads threads need. Where that makes
+// fewer CTAs than SMs, a row's columns (or, for one_token, its slots) are
+// spread over several (16 tokens x 8 slots of 7168: return 4.8 -> 3.2 us).
 RowShape row_shape(const RouteArgs& a, int64_t ld_elems, bool one_token) {
   const int size = a.type == QMV_F32 ? 4 : 2;
   const int64_t bytes = (int64_t)a.K * size, stride = ld_elems * size;
   RowShape s;
   s.vb = 16;
   while (s.vb > size && (bytes % s.vb != 0 || stride % s.vb != 0)) s.vb /= 2;
-  s.vecs = bytes / s.vb;
-  s.ld = stride / s.vb;
-  const int64_t rounds = (s.vecs + 511) / 512;
-  const int64_t x = ((s.vecs + rounds - 1) / rounds + 31) / 32 * 32;
+  const int64_t vecs = bytes / s.vb;   // at most 2^17
+  const int64_t rounds = (vecs + kMoveThreads - 1) / kMoveThreads;
+  int64_t x = ((vecs + rounds - 1) / rounds + 31) / 32 * 32;
   const int64_t y = one_token || x >= 256 ? 1 : 256 / x;
-  s.block = dim3((unsigned)x, (unsigned)y);
-  int64_t grid = (a.ntok + y - 1) / y;
+  int64_t grid = (a.ntok + y - 1) / y, split = 1;
+  if (grid < device_sm_count()) {
+    if (one_token) {
+      split = (a.top_k + kSlotGroup - 1) / kSlotGroup;
+    } else if (y == 1) {
+      x = 128;
+      split = (vecs + x - 1) / x;
+    }
+  }
   if (grid > (1 << 20)) grid = 1 << 20;
-  s.grid = dim3((unsigned)grid);
-  s.tokens = grid * y;
+  s.block = dim3((unsigned)x, (unsigned)y);
+  s.grid = dim3((unsigned)grid, (unsigned)split);
+  s.move = {(int)vecs, (int)(grid * y), stride / s.vb};
   return s;
 }
 
@@ -348,13 +418,14 @@ cudaError_t by_type(const RouteArgs& a, const RowShape& s) {
 template <typename T, int VB>
 struct Return {
   static cudaError_t go(const RouteArgs& a, const RowShape& s) {
-    return launch_pdl(return_kernel<T, VB>, s.grid, s.block, 0, a.stream, a, s.vecs, s.ld, s.tokens);
+    return s.grid.y > 1 ? launch_pdl(return_kernel<T, VB, true>, s.grid, s.block, 0, a.stream, a, s.move)
+                        : launch_pdl(return_kernel<T, VB, false>, s.grid, s.block, 0, a.stream, a, s.move);
   }
 };
 template <typename T, int VB>
 struct ReturnGrad {
   static cudaError_t go(const RouteArgs& a, const RowShape& s) {
-    return launch_pdl(return_grad_kernel<T, VB>, s.grid, s.block, 0, a.stream, a, s.vecs, s.ld, s.tokens);
+    return launch_pdl(return_grad_kernel<T, VB>, s.grid, s.block, 0, a.stream, a, s.move);
   }
 };
 
@@ -363,10 +434,10 @@ struct ReturnGrad {
 cudaError_t launch_dispatch(const RouteArgs& a) {
   const RowShape s = row_shape(a, a.ld_tok, false);
   switch (s.vb) {
-    case 16: return launch_pdl(dispatch_kernel<16>, s.grid, s.block, 0, a.stream, a, s.vecs, s.ld, s.tokens);
-    case 8: return launch_pdl(dispatch_kernel<8>, s.grid, s.block, 0, a.stream, a, s.vecs, s.ld, s.tokens);
-    case 4: return launch_pdl(dispatch_kernel<4>, s.grid, s.block, 0, a.stream, a, s.vecs, s.ld, s.tokens);
-    default: return launch_pdl(dispatch_kernel<2>, s.grid, s.block, 0, a.stream, a, s.vecs, s.ld, s.tokens);
+    case 16: return launch_pdl(dispatch_kernel<16>, s.grid, s.block, 0, a.stream, a, s.move);
+    case 8: return launch_pdl(dispatch_kernel<8>, s.grid, s.block, 0, a.stream, a, s.move);
+    case 4: return launch_pdl(dispatch_kernel<4>, s.grid, s.block, 0, a.stream, a, s.move);
+    default: return launch_pdl(dispatch_kernel<2>, s.grid, s.block, 0, a.stream, a, s.move);
   }
 }
 

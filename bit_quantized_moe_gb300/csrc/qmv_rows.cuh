@@ -23,22 +23,40 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Eight consecutive elements as fp32. VEC: the address is 16-byte aligned.
+// Eight consecutive elements as they lie in memory, so that several can be
+// asked for before the first is used.
+template <typename T>
+struct alignas(16) Raw8 {
+  T e[8];
+};
+
+// VEC: the address is 16-byte aligned.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_raw8(const T* __restrict__ p, Raw8<T>& r) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(r) / 16; ++i) {
+      reinterpret_cast<uint4*>(r.e)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.e[i] = p[i];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void clear_raw8(Raw8<T>& r) {
+#pragma unroll
+  for (T& e : r.e) e = from_f32<T>(0.0f);
+}
+
+// Eight consecutive elements as fp32.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* __restrict__ p, float (&v)[8]) {
-  if constexpr (!VEC) {
+  Raw8<T> r;
+  load_raw8<T, VEC>(p, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const T* e = reinterpret_cast<const T*>(&a);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
-  }
+  for (int i = 0; i < 8; ++i) v[i] = to_f32(r.e[i]);
 }
 
 template <typename T, bool VEC>
@@ -65,6 +83,33 @@ __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
   return m;
+}
+
+// The same of elements as loaded. 16-bit types compare two at a time; the
+// NaN-propagating maximum keeps a NaN above everything.
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<float>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(r.e[i]) & 0x7fffffffu);
+  return m;
+}
+template <typename T, typename T2>
+__device__ __forceinline__ T2 amax_pair8(const Raw8<T>& r) {
+  T2 p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(r.e)[i] & 0x7fff7fffu;
+    p[i] = *reinterpret_cast<const T2*>(&w);
+  }
+  return __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+}
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<__nv_bfloat16>& r) {
+  const __nv_bfloat162 m = amax_pair8<__nv_bfloat16, __nv_bfloat162>(r);
+  return __float_as_uint(__bfloat162float(__hmax_nan(m.x, m.y)));
+}
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<__half>& r) {
+  const __half2 m = amax_pair8<__half, __half2>(r);
+  return __float_as_uint(__half2float(__hmax_nan(m.x, m.y)));
 }
 
 // E8M0 byte of a group whose largest |v| has these bits: the exponent of the
@@ -120,14 +165,11 @@ __device__ __forceinline__ void store_codes8(uint8_t* row, int c, const uint32_t
   }
 }
 
-// The four scale bytes of 128 columns from 16 lanes of eight columns each
-// (lane l of the 16 holds its group's byte): the word, in every lane of the 16.
-__device__ __forceinline__ uint32_t scale_word16(uint32_t e, int lane) {
-  const int base = lane & 16;
-  uint32_t w = 0;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) w |= __shfl_sync(0xffffffffu, e, base + 4 * b) << (8 * b);
-  return w;
+// The four scale bytes of 128 columns from 16 lanes of eight columns each (a
+// lane of the 16 holds its group's byte): the word, in the first lane of the 16.
+__device__ __forceinline__ uint32_t scale_word16(uint32_t e) {
+  const uint32_t two = e | __shfl_down_sync(0xffffffffu, e, 4) << 8;
+  return two | __shfl_down_sync(0xffffffffu, two, 8) << 16;
 }
 
 }  // namespace qmv
