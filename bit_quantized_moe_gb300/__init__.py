@@ -183,9 +183,16 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# The current stream's handle as torch's own generated code asks for it (0.2 us
+# instead of 2.9 for a Stream object on a Grace core); None: not in this torch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -29,10 +29,12 @@
 //   4..11  the epilogue, one warpgroup an accumulator: a thread has a row's
 //          columns in order, so SwiGLU, a group's maximum and its quantization
 //          need no other thread
-//   2, 3, 12..15  read the scales of one step in six each, a turn ahead, and
+//   2, 3, 12..19  read the scales of one step in ten each, a turn ahead, and
 //          write them as tcgen05.cp wants them
 // Tiles of an expert follow one another along its rows, so that its weights
 // are read from memory once and again from L2.
+#include <atomic>
+
 #include <cuda.h>
 
 #include "qmv_internal.h"
@@ -42,12 +44,12 @@ namespace qmv {
 
 constexpr int kTileM = 128;        // rows of activations of one CTA
 constexpr int kTileN = 192;        // rows of weights: the output's columns
-constexpr int kGemmThreads = 512;
-constexpr int kScaleWarps = 6;      // warps 2, 3 and 12..15
+constexpr int kGemmThreads = 640;
+constexpr int kScaleWarps = 10;     // warps 2, 3 and 12..19 (six: 8192 x 7168 x 7168 MXFP4 152 us, ten: 143)
 // Columns of 16-bit outputs that a thread parks in shared memory before its
 // warp stores them row by row, and the pitch of a row there (an odd number of
 // 16 bytes: no bank conflicts between rows).
-constexpr int kParkCols = 64;
+constexpr int kParkCols = 32;
 constexpr int kParkPitch = kParkCols * 2 + 16;
 
 template <int FMT, bool PAIR>
@@ -66,7 +68,10 @@ struct GemmFmt {
   static constexpr uint32_t sf_bytes = sfa_bytes + sfb_bytes;
   static constexpr uint32_t sf_cols = atoms * 12;           // tensor memory columns of a stage's scales
   static constexpr int stages = PAIR ? 5 : 4;
-  static constexpr int sf_stages = PAIR ? 10 : 6;           // steps that the scales may be ahead
+  // Steps that the scales may be ahead. At least the scale warps: a warp may then not be two uses of a place ahead of
+  // the MMAs, which its barrier's phase bit could not tell from none.
+  static constexpr int sf_stages = 10;
+  static_assert(kScaleWarps <= sf_stages && stages <= sf_stages, "phases of the barriers");
   static constexpr uint32_t park_bytes = 2 * kTileM * kParkPitch;
 };
 constexpr uint32_t kTmemCols = 512;
@@ -619,7 +624,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
       if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
     }
   } else if (warp < 4 || warp >= 12) {
-    // ---- scales: every sixth step, loaded one turn ahead of its slot in the ring
+    // ---- scales: every tenth step, loaded one turn ahead of its slot in the ring
     StepScales<FMT> cur;
     int it = warp < 4 ? warp - 2 : warp - 10;
     int t = t0, s = it;
@@ -869,10 +874,7 @@ cudaError_t go(const MxGemmArgs& a) {
   constexpr int ctas = PAIR ? 2 : 1;
   const int64_t row_tiles = a.nrows / (ctas * kTileM) + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);
   int64_t grid = row_tiles * p.n_tiles;
-  if (grid > device_sm_count() / ctas) grid = device_sm_count() / ctas;
-  g_launch_stage = "launch";
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(grid * ctas));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
@@ -884,6 +886,25 @@ cudaError_t go(const MxGemmArgs& a) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // No more pairs than run at once: the device may not place one on every two SMs, and one that starts when another
+  // ends would have its share of the tiles still before it.
+  int most = device_sm_count();
+  if constexpr (PAIR) {
+    static std::atomic<int> pairs{0};   // per kernel: the same on every device this library is built for
+    most = pairs.load(std::memory_order_relaxed);
+    if (most == 0) {
+      g_launch_stage = "cudaOccupancyMaxActiveClusters";
+      cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2));
+      e = cudaOccupancyMaxActiveClusters(&most, mx_gemm_kernel<FMT, HFMT, PAIR>, &cfg);
+      if (e != cudaSuccess) return e;
+      if (most < 1) return cudaErrorInvalidConfiguration;
+      pairs.store(most, std::memory_order_relaxed);
+    }
+  }
+  if (grid > most) grid = most;
+  g_launch_stage = "launch";
+  cfg.gridDim = dim3((unsigned)(grid * ctas));
   cfg.numAttrs = a.stream != nullptr ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, HFMT, PAIR>, mx, mw, ml, p);
 }
