@@ -17,8 +17,8 @@
 // chunk has a map of its own. The scales of a row tile lie lane by lane
 // ([lane][row]); a scale warp transposes them while the codes are in flight.
 //
-// One CTA per SM, or a pair of CTAs on two, takes output tiles of 128 rows (a
-// pair: 256) x 192 columns in turn. Warps:
+// One CTA per SM takes output tiles of 128 rows x 128 or 64 columns in turn, or
+// a pair of CTAs on two SMs tiles of 256 x 192 (pick_tile). Warps:
 //   0      issues the TMA copies of codes, 128 bytes of every row a step.
 //          (Asking for the weights of 16 later steps in L2, by boxes or by
 //          whole tiles, was slower at every size measured: 132 rows of 32
@@ -34,6 +34,7 @@
 // Tiles of an expert follow one another along its rows, so that its weights
 // are read from memory once and again from L2.
 #include <atomic>
+#include <cmath>
 
 #include <cuda.h>
 
@@ -43,7 +44,6 @@
 namespace qmv {
 
 constexpr int kTileM = 128;        // rows of activations of one CTA
-constexpr int kTileN = 192;        // rows of weights: the output's columns
 constexpr int kGemmThreads = 640;
 constexpr int kScaleWarps = 10;     // warps 2, 3 and 12..19 (six: 8192 x 7168 x 7168 MXFP4 152 us, ten: 143)
 // Columns of 16-bit outputs that a thread parks in shared memory before its
@@ -52,31 +52,36 @@ constexpr int kScaleWarps = 10;     // warps 2, 3 and 12..19 (six: 8192 x 7168 x
 constexpr int kParkCols = 32;
 constexpr int kParkPitch = kParkCols * 2 + 16;
 
-template <int FMT, bool PAIR>
+template <int FMT, int TN, bool PAIR>
 struct GemmFmt {
   static constexpr int step_k = FMT == MXFP4 ? 256 : 128;   // columns in 128 bytes of codes
   static constexpr int mma_k = FMT == MXFP4 ? 64 : 32;      // columns of one MMA
   static constexpr int atoms = step_k / 128;                // scale words of a row per step
   static constexpr int steps_per_chunk = kChunkK / step_k;
   static constexpr uint32_t a_bytes = kTileM * 128;
-  static constexpr int b_rows = PAIR ? kTileN / 2 : kTileN;   // a pair's CTAs hold half of the weights each
+  // Rows of one copy of activations. Single CTAs' tiles often have few rows, and copies of rows that are not there are
+  // not free (17 rows: boxes of 128 rows took longer than 128 rows did): they copy 32 at a time, as many as live ones.
+  static constexpr int x_rows = PAIR ? kTileM : 32;
+  static constexpr int b_rows = PAIR ? TN / 2 : TN;         // a pair's CTAs hold half of the weights each
   static constexpr uint32_t b_bytes = b_rows * 128;
-  // scales: 512 bytes hold the words of 128 rows, [row % 32][row / 32]
-  static constexpr uint32_t sfa_bytes = atoms * 512;
-  static constexpr uint32_t sfb_bytes = atoms * 1024;
   static constexpr uint32_t stage_bytes = a_bytes + b_bytes;
+  // scales: 512 bytes, and four columns of tensor memory, hold the words of 128 rows, [row % 32][row / 32]
+  static constexpr int b_blocks = (TN + 127) / 128;
+  static constexpr uint32_t sfa_bytes = atoms * 512;
+  static constexpr uint32_t sfb_bytes = atoms * b_blocks * 512;
   static constexpr uint32_t sf_bytes = sfa_bytes + sfb_bytes;
-  static constexpr uint32_t sf_cols = atoms * 12;           // tensor memory columns of a stage's scales
-  static constexpr int stages = PAIR ? 5 : 4;
+  static constexpr uint32_t atom_cols = 4 + 4 * b_blocks;   // tensor memory columns of 128 columns' scales
+  static constexpr uint32_t sf_cols = atoms * atom_cols;
+  static constexpr int stages = PAIR ? 5 : (TN == 128 ? 5 : 7);
   // Steps that the scales may be ahead. At least the scale warps: a warp may then not be two uses of a place ahead of
   // the MMAs, which its barrier's phase bit could not tell from none.
   static constexpr int sf_stages = 10;
   static_assert(kScaleWarps <= sf_stages && stages <= sf_stages, "phases of the barriers");
   static constexpr uint32_t park_bytes = 2 * kTileM * kParkPitch;
+  static constexpr uint32_t sf_col0 = 2 * TN;               // scales follow the two accumulators
+  static constexpr uint32_t tmem_cols = sf_col0 + stages * sf_cols <= 256 ? 256 : 512;
+  static_assert(sf_col0 + stages * sf_cols <= tmem_cols, "tensor memory");
 };
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol0 = 2 * kTileN;   // scales follow the two accumulators
-static_assert(kSfCol0 + GemmFmt<MXFP4, true>::stages * GemmFmt<MXFP4, true>::sf_cols <= kTmemCols, "tensor memory");
 
 struct GemmParams {
   const uint8_t* w;
@@ -132,10 +137,10 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 // Instruction descriptor of the block-scaled kinds: element types (E2M1 is 1 in
 // kind::mxf4; E4M3 is 0 in kind::mxf8f6f4), N / 8, E8M0 scales (bit 23), M / 128,
 // and which byte of the scale words the instruction's first group uses.
-template <int FMT, bool PAIR>
+template <int FMT, int TN, bool PAIR>
 __device__ __forceinline__ uint32_t block_idesc(uint32_t sf_byte) {
   constexpr uint32_t elem = FMT == MXFP4 ? 1u : 0u;
-  constexpr uint32_t base = (elem << 7) | (elem << 10) | ((uint32_t)(kTileN >> 3) << 17) | (1u << 23) |
+  constexpr uint32_t base = (elem << 7) | (elem << 10) | ((uint32_t)(TN >> 3) << 17) | (1u << 23) |
                             ((uint32_t)((PAIR ? 2 * kTileM : kTileM) >> 7) << 27);
   return base | (sf_byte << 4) | (sf_byte << 29);
 }
@@ -318,10 +323,10 @@ __device__ __forceinline__ Tile tile_at(int t, const int* first_tile, const int*
 // The scales of one step as a scale warp's lane reads them: the words of four
 // rows of activations per 128 columns, and 32 bytes ([lane][row], four lanes)
 // of one or two row tiles of weights.
-template <int FMT>
+template <int FMT, int TN>
 struct StepScales {
-  using F = GemmFmt<FMT, false>;
-  static constexpr int kItems = kTileN / 8 * F::atoms;   // (row tile, 128 columns) pairs
+  using F = GemmFmt<FMT, TN, (TN > 128)>;   // the scales of a tile are the same for one CTA and a pair
+  static constexpr int kItems = TN / 8 * F::atoms;   // (row tile, 128 columns) pairs
   static constexpr int kRounds = (kItems + 31) / 32;
   uint32_t a[F::atoms][4];
   uint4 b[kRounds][2];
@@ -345,7 +350,7 @@ struct StepScales {
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
       const int item = lane + 32 * i;
-      const int rt = t.n * (kTileN / 8) + item / F::atoms;
+      const int rt = t.n * (TN / 8) + item / F::atoms;
       const int l = l0 + 4 * (item % F::atoms);
       const uint4* src = reinterpret_cast<const uint4*>(base + (uint64_t)rt * p.rowtile + (uint64_t)l * kRows);
       const bool in = item < kItems && rt < p.row_tiles;
@@ -384,7 +389,7 @@ struct StepScales {
           }
         }
         const int row0 = item / F::atoms * 8;
-        uint8_t* atom = sfb + (item % F::atoms) * 1024 + (row0 / 128) * 512 + (row0 % 32) * 16 + (row0 % 128) / 32 * 4;
+        uint8_t* atom = sfb + ((item % F::atoms) * F::b_blocks + row0 / 128) * 512 + (row0 % 32) * 16 + (row0 % 128) / 32 * 4;
 #pragma unroll
         for (int r = 0; r < 8; ++r) *reinterpret_cast<uint32_t*>(atom + (r ^ x) * 16) = w[r];
       }
@@ -428,11 +433,11 @@ __device__ __forceinline__ void park_columns(uint8_t* at, const uint32_t (&r)[32
 // and silu(gate) * up is stored, quantized to HFMT.
 // PAIR: two CTAs (a cluster) share a tile of 256 rows; the first, the leader,
 // issues the MMAs of both.
-template <int FMT, int HFMT, bool PAIR>
+template <int FMT, int HFMT, int TN, bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                const __grid_constant__ CUtensorMap map_last, const __grid_constant__ GemmParams p) {
-  using F = GemmFmt<FMT, PAIR>;
+  using F = GemmFmt<FMT, TN, PAIR>;
   constexpr int kStages = F::stages;
   constexpr int kCtas = PAIR ? 2 : 1;
   extern __shared__ uint8_t dyn[];
@@ -465,11 +470,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
   if (warp == 1) {
     if constexpr (PAIR) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(&tmem_base)),
-                   "r"(kTmemCols) : "memory");
+                   "r"(F::tmem_cols) : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     } else {
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(&tmem_base)),
-                   "r"(kTmemCols) : "memory");
+                   "r"(F::tmem_cols) : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
   }
@@ -524,15 +529,23 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     if (elect_one()) {
       for (int t = t0; t < tiles && ok; t += dt) {
         const Tile tile = tile_of(t);
-        const int rt = tile.n * (kTileN / 8) + rank * (F::b_rows / 8);
+        const int rt = tile.n * (TN / 8) + rank * (F::b_rows / 8);
+        const int copies = (min(tile.rows, kTileM) + F::x_rows - 1) / F::x_rows;
         for (int s = 0; s < steps; ++s, ++it) {
           const int st = it % kStages;
           if (!wait_used(it, kStages)) { ok = false; break; }
           uint32_t bar = smem_addr(&full[st]);
           const uint32_t dst = smem_addr(stages + (uint32_t)st * F::stage_bytes);
-          if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * (F::a_bytes + F::b_bytes));
-          if constexpr (PAIR) bar = leader_addr(bar);
-          tma_load_2d<PAIR>(dst, &map_x, s * 128, tile.row0, bar);
+          if constexpr (PAIR) {
+            if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * (F::a_bytes + F::b_bytes));
+            bar = leader_addr(bar);
+            tma_load_2d<PAIR>(dst, &map_x, s * 128, tile.row0, bar);
+          } else {   // rows past the last live copy keep what the stage held: their products are not stored
+            mbar_arrive_expect_tx(bar, (uint32_t)copies * F::x_rows * 128 + F::b_bytes);
+            for (int i = 0; i < copies; ++i) {
+              tma_load_2d<PAIR>(dst + (uint32_t)i * F::x_rows * 128, &map_x, s * 128, tile.row0 + i * F::x_rows, bar);
+            }
+          }
           const int chunk = s / F::steps_per_chunk;
           const int x = (s % F::steps_per_chunk) * 128;
           if (chunk < p.chunks_full) {
@@ -573,7 +586,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         const int acc = n & 1;
         if (!__all_sync(0xffffffffu, wait_for<PAIR>(smem_addr(&acc_empty[acc]), ((n >> 1) & 1) ^ 1))) { ok = false; break; }
         tc_after_sync();
-        const uint32_t d = tm + (uint32_t)(acc * kTileN);
+        const uint32_t d = tm + (uint32_t)(acc * TN);
         int left = p.K;
         for (int s = 0; s < steps; ++s, left -= F::step_k) {
           if (!ready && !__all_sync(0xffffffffu, wait_for<PAIR>(smem_addr(&sf_full[ss]), ss_phase) &&
@@ -584,7 +597,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
           tc_after_sync();
           const uint32_t a0 = code0 + (uint32_t)st * F::stage_bytes, b0 = a0 + F::a_bytes;
           const uint32_t sfa = scale0 + (uint32_t)ss * F::sf_bytes, sfb = sfa + F::sfa_bytes;
-          const uint32_t sf = tm + kSfCol0 + (uint32_t)st * F::sf_cols;
+          const uint32_t sf = tm + F::sf_col0 + (uint32_t)st * F::sf_cols;
           const uint32_t used_bar = smem_addr(&used[ss]);
           if (++st == kStages) { st = 0; st_phase ^= 1; }
           if (++ss == F::sf_stages) { ss = 0; ss_phase ^= 1; }
@@ -593,15 +606,18 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < F::atoms; ++k) {
-              scales_to_tmem<PAIR>(sf + (uint32_t)k * 12, scale_desc(sfa + (uint32_t)k * 512));
-              scales_to_tmem<PAIR>(sf + (uint32_t)k * 12 + 4, scale_desc(sfb + (uint32_t)k * 1024));
-              scales_to_tmem<PAIR>(sf + (uint32_t)k * 12 + 8, scale_desc(sfb + (uint32_t)k * 1024 + 512));
+              const uint32_t col = sf + (uint32_t)k * F::atom_cols;
+              scales_to_tmem<PAIR>(col, scale_desc(sfa + (uint32_t)k * 512));
+#pragma unroll
+              for (int i = 0; i < F::b_blocks; ++i) {
+                scales_to_tmem<PAIR>(col + 4 + 4 * i, scale_desc(sfb + (uint32_t)(k * F::b_blocks + i) * 512));
+              }
             }
             const auto mma = [&](int j, uint32_t accumulate) {
               constexpr int per_atom = 128 / F::mma_k;
-              const uint32_t col = sf + (uint32_t)(j / per_atom) * 12;
+              const uint32_t col = sf + (uint32_t)(j / per_atom) * F::atom_cols;
               mma_block_scaled<FMT, PAIR>(d, operand_desc(a0 + (uint32_t)j * 32), operand_desc(b0 + (uint32_t)j * 32),
-                                          block_idesc<FMT, PAIR>((uint32_t)(j % per_atom) * (F::mma_k / 32)), col,
+                                          block_idesc<FMT, TN, PAIR>((uint32_t)(j % per_atom) * (F::mma_k / 32)), col,
                                           col + 4, accumulate);
             };
             mma(0, s > 0 ? 1u : 0u);
@@ -625,7 +641,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     }
   } else if (warp < 4 || warp >= 12) {
     // ---- scales: every tenth step, loaded one turn ahead of its slot in the ring
-    StepScales<FMT> cur;
+    StepScales<FMT, TN> cur;
     int it = warp < 4 ? warp - 2 : warp - 10;
     int t = t0, s = it;
     Tile tile{};
@@ -637,7 +653,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     while (t < tiles) {
       int t2 = t, s2 = s + kScaleWarps;
       while (t2 < tiles && s2 >= steps) { s2 -= steps; t2 += dt; }
-      StepScales<FMT> next = cur;
+      StepScales<FMT, TN> next = cur;
       if (t2 < tiles) {
         if (t2 != t) tile = tile_of(t2);
         next.load(p, tile, s2, lane);
@@ -672,7 +688,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
       const int r = quad * 32 + lane;
       const bool live = r < tile.rows;
       const int64_t row = (int64_t)tile.row0 + r;
-      const uint32_t d = tmem + (uint32_t)(acc * kTileN) + ((uint32_t)(quad * 32) << 16);
+      const uint32_t d = tmem + (uint32_t)(acc * TN) + ((uint32_t)(quad * 32) << 16);
       const auto release = [&] {   // the accumulator has been read
         tc_before_sync();
         __syncwarp();
@@ -687,7 +703,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
           uint8_t* out = static_cast<uint8_t*>(p.y) + ((int64_t)tile.row0 + quad * 32) * p.out_n * 2;
           const int rows = min(32, tile.rows - quad * 32);
 #pragma unroll 1
-          for (int c = 0; c < kTileN; c += kParkCols) {
+          for (int c = 0; c < TN; c += kParkCols) {
 #pragma unroll
             for (int i = 0; i < kParkCols; i += 32) {
               uint32_t v[32];
@@ -696,9 +712,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
               if (p.out_type == QMV_BF16) park_columns<__nv_bfloat16>(my_park + i * 2, v);
               else park_columns<__half>(my_park + i * 2, v);
             }
-            if (c + kParkCols == kTileN) release();
+            if (c + kParkCols == TN) release();
             __syncwarp();
-            const int n0 = tile.n * kTileN + c;
+            const int n0 = tile.n * TN + c;
             const int vecs = min(kParkCols, p.out_n - n0) / 8;   // 16 bytes each
 #pragma unroll 4
             for (int i = lane; i < 32 * (kParkCols / 8); i += 32) {
@@ -713,11 +729,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         } else {
           const bool vec = p.out_type == QMV_F32 && p.out_n % 4 == 0;
 #pragma unroll 1
-          for (int c = 0; c < kTileN; c += 32) {
+          for (int c = 0; c < TN; c += 32) {
             uint32_t v[32];
             tmem_ld32(d + (uint32_t)c, v);
             tmem_ld_wait(v);
-            const int n0 = tile.n * kTileN + c;
+            const int n0 = tile.n * TN + c;
             if (live && n0 < p.out_n) {
               const int64_t at = row * p.out_n + n0;
               if (p.out_type == QMV_BF16) store_columns(static_cast<__nv_bfloat16*>(p.y) + at, v, p.out_n - n0, false);
@@ -730,14 +746,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
       } else {
         const uint64_t h_bytes = mx_row_bytes(HFMT, p.out_n);
 #pragma unroll 1
-        for (int c = 0; c < kTileN; c += 64) {
+        for (int c = 0; c < TN; c += 64) {
           uint32_t v[2][32];
           tmem_ld32(d + (uint32_t)c, v[0]);
           tmem_ld32(d + (uint32_t)c + 32, v[1]);
           tmem_ld_wait(v[0]);
           tmem_ld_wait(v[1]);
-          if (c + 64 == kTileN) release();
-          const int n0 = (tile.n * kTileN + c) / 2;   // a group of 32 columns of h
+          if (c + 64 == TN) release();
+          const int n0 = (tile.n * TN + c) / 2;   // a group of 32 columns of h
           if (live && n0 < p.out_n) {
             float h[4][8];
             uint32_t m = 0;
@@ -781,8 +797,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
   if constexpr (PAIR) cluster_sync_all();   // neither CTA's memory is in use by the other any more
   if (warp == 1) {
     tc_after_sync();
-    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
-    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(F::tmem_cols));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(F::tmem_cols));
   }
 }
 
@@ -816,9 +832,9 @@ bool encode(CUtensorMap* map, int rank, const void* base, const cuuint64_t* dims
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int HFMT, bool PAIR>
+template <int FMT, int HFMT, int TN, bool PAIR>
 cudaError_t go(const MxGemmArgs& a) {
-  using F = GemmFmt<FMT, PAIR>;
+  using F = GemmFmt<FMT, TN, PAIR>;
   const Geometry g = make_geometry(FMT, a.N, a.K);
   const int lane_bytes = lane_code_bytes(FMT);
   GemmParams p = {};
@@ -840,7 +856,7 @@ cudaError_t go(const MxGemmArgs& a) {
   p.n_experts = a.n_experts;
   p.out_n = a.out_n;
   p.out_type = a.out_type;
-  p.n_tiles = (g.row_tiles * kRows + kTileN - 1) / kTileN;
+  p.n_tiles = (g.row_tiles * kRows + TN - 1) / TN;
 
   g_launch_stage = "cuTensorMapEncodeTiled";
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
@@ -848,7 +864,7 @@ cudaError_t go(const MxGemmArgs& a) {
   {
     const cuuint64_t row = mx_row_bytes(FMT, a.K);
     const cuuint64_t dims[2] = {row, (cuuint64_t)a.nrows}, strides[1] = {row};
-    const cuuint32_t box[2] = {128, kTileM};
+    const cuuint32_t box[2] = {128, F::x_rows};
     if (!encode(&mx, 2, a.xq, dims, strides, box)) return cudaErrorInvalidValue;
   }
   const cuuint32_t box[5] = {128, kRows, F::b_rows / kRows, 1, 1};
@@ -868,7 +884,7 @@ cudaError_t go(const MxGemmArgs& a) {
       1024 + (size_t)F::stages * F::stage_bytes + F::sf_stages * F::sf_bytes + F::park_bytes + 2 * ((size_t)a.n_experts + 1) * sizeof(int);
   g_launch_stage = "cudaFuncSetAttribute";
   cudaError_t e =
-      cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT, TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // no more CTAs than tiles there can be: every expert has at most one partial row tile
   constexpr int ctas = PAIR ? 2 : 1;
@@ -896,7 +912,7 @@ cudaError_t go(const MxGemmArgs& a) {
     if (most == 0) {
       g_launch_stage = "cudaOccupancyMaxActiveClusters";
       cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2));
-      e = cudaOccupancyMaxActiveClusters(&most, mx_gemm_kernel<FMT, HFMT, PAIR>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&most, mx_gemm_kernel<FMT, HFMT, TN, PAIR>, &cfg);
       if (e != cudaSuccess) return e;
       if (most < 1) return cudaErrorInvalidConfiguration;
       pairs.store(most, std::memory_order_relaxed);
@@ -906,25 +922,62 @@ cudaError_t go(const MxGemmArgs& a) {
   g_launch_stage = "launch";
   cfg.gridDim = dim3((unsigned)(grid * ctas));
   cfg.numAttrs = a.stream != nullptr ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, HFMT, PAIR>, mx, mw, ml, p);
+  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, HFMT, TN, PAIR>, mx, mw, ml, p);
 }
 
-// Pairs of CTAs where an expert has more rows than one CTA's tile on average.
-bool use_pairs(const MxGemmArgs& a) { return a.nrows > (int64_t)kTileM * a.n_experts; }
-
-template <int FMT, bool PAIR>
+template <int FMT, int TN, bool PAIR>
 cudaError_t by_h(const MxGemmArgs& a) {
-  if (!a.glu) return go<FMT, -1, PAIR>(a);
-  return a.h_fmt == MXFP4 ? go<FMT, MXFP4, PAIR>(a) : go<FMT, MXFP8, PAIR>(a);
+  if (!a.glu) return go<FMT, -1, TN, PAIR>(a);
+  return a.h_fmt == MXFP4 ? go<FMT, MXFP4, TN, PAIR>(a) : go<FMT, MXFP8, TN, PAIR>(a);
+}
+
+// The tile of a call: a pair's 256 x 192, or one CTA's 128 x 128 or 128 x 64.
+// Every CTA (pair) takes ceil(tiles / CTAs) tiles one after another, whose time
+// is their steps of 128 bytes; the row tiles of a grouped product are those of
+// equally full experts, each with half a tile more. A step and a launch took,
+// fitted to both formats on GB300: pair 0.33 us and 7 us, 128 x 128 0.36 and
+// 4.5, 128 x 64 0.27 and 4.5. Measured (pair / 128 x 128 / 128 x 64, us):
+//   17 x 7168 x 7168 MXFP4       16.8 / 13.2 / 11.6
+//   200 x 7168 x 7168 MXFP4      17.0 / 14.0 / 19.2
+//   300 x 7168 x 7168 MXFP4      17.3 / 21.8 / 26.0
+//   1001 x 7168 x 2048 MXFP8     17.9 / 19.2 / 28.9
+//   132 rows of 32 experts, gate/up 2880 MXFP4    68 / 54 / 71
+//   16000 rows of them                           150 / 191 / 287
+int pick_tile(const MxGemmArgs& a) {
+  struct Shape {
+    int m, n;
+    double step_us, launch_us;
+  };
+  const Shape shapes[3] = {{2 * kTileM, 192, 0.33, 7.0}, {kTileM, 128, 0.36, 4.5}, {kTileM, 64, 0.27, 4.5}};
+  const int steps = (int)((mx_row_bytes(a.fmt, a.K) + 127) / 128);
+  int best = 0;
+  double best_us = 0.0;
+  for (int i = 0; i < 3; ++i) {
+    const Shape& s = shapes[i];
+    const double hit = a.nrows < a.n_experts ? (double)a.nrows : (double)a.n_experts;
+    const double each = a.nrows / hit / s.m;
+    const double row_tiles = a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
+    const int slots = device_sm_count() / (s.m / kTileM);
+    const double us = s.launch_us + ceil(row_tiles * ((a.N + s.n - 1) / s.n) / slots) * steps * s.step_us;
+    if (i == 0 || us < best_us) {
+      best = i;
+      best_us = us;
+    }
+  }
+  return best;
 }
 
 template <int FMT>
-cudaError_t by_pair(const MxGemmArgs& a) {
-  return use_pairs(a) ? by_h<FMT, true>(a) : by_h<FMT, false>(a);
+cudaError_t by_tile(const MxGemmArgs& a) {
+  switch (pick_tile(a)) {
+    case 0: return by_h<FMT, 192, true>(a);
+    case 1: return by_h<FMT, 128, false>(a);
+    default: return by_h<FMT, 64, false>(a);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_mx_gemm(const MxGemmArgs& a) { return a.fmt == MXFP4 ? by_pair<MXFP4>(a) : by_pair<MXFP8>(a); }
+cudaError_t launch_mx_gemm(const MxGemmArgs& a) { return a.fmt == MXFP4 ? by_tile<MXFP4>(a) : by_tile<MXFP8>(a); }
 
 }  // namespace qmv
