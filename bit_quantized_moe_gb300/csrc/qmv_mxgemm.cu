@@ -770,11 +770,16 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             }
             const uint32_t e = group_e8m0<HFMT>(m);
             uint8_t* out = static_cast<uint8_t*>(p.y) + (uint64_t)row * h_bytes;
+            constexpr int kWords = HFMT == MXFP4 ? 4 : 8;   // of the group's codes
+            uint32_t w[kWords];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t w[HFMT == MXFP4 ? 1 : 2];
-              mx_codes8<HFMT>(h[i], e, w);
-              store_codes8<HFMT>(out, n0 + 8 * i, w);
+              mx_codes8<HFMT>(h[i], e, *reinterpret_cast<uint32_t(*)[kWords / 4]>(w + i * (kWords / 4)));
+            }
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+              reinterpret_cast<uint4*>(out + n0 * fmt_bits(HFMT) / 8)[i] =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             }
             uint8_t* sc = reinterpret_cast<uint8_t*>(p.h_scales + (int64_t)(n0 / 128) * p.nrows + row);
             const int b = n0 / 32 % 4;
