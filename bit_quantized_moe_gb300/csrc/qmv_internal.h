@@ -128,6 +128,7 @@ struct RouteArgs {
   const void* tok = nullptr;    // token-major rows read (x, dy)
   int64_t ld_tok = 0;
   const void* rows = nullptr;   // expert-major rows read (ys, dxs)
+  bool rows_f32 = false;        // launch_return: rows are fp32 whatever `type`
   const float* weights = nullptr;   // null: every weight is 1
   void* out_tok = nullptr;      // token-major rows written (y, dx)
   int64_t ld_out = 0;

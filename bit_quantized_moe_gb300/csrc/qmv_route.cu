@@ -242,10 +242,25 @@ __global__ void __launch_bounds__(kMoveThreads, 4) dispatch_kernel(RouteArgs a, 
   pdl_launch_dependents();
 }
 
-// SPLIT: blockIdx.y takes a part of the columns. Without it the kernel fits 40
-// registers and four CTAs an SM (8191 tokens x 4 slots of 2880: 41 us against 47).
-template <typename T, int VB, bool SPLIT>
-__global__ void __launch_bounds__(kMoveThreads, SPLIT ? 3 : 4) return_kernel(RouteArgs a, MoveShape m) {
+// EV elements of a row, read in accesses of up to 16 bytes.
+template <typename R, int EV>
+struct RowVec {
+  static constexpr int bytes = EV * (int)sizeof(R), access = bytes < 16 ? bytes : 16, count = bytes / access;
+  typename Bytes<access>::type u[count];
+  __device__ __forceinline__ void load(const void* rows, int64_t at) {
+    const auto* p = static_cast<const typename Bytes<access>::type*>(rows) + at * count;
+#pragma unroll
+    for (int i = 0; i < count; ++i) u[i] = __ldg(p + i);
+  }
+  __device__ __forceinline__ float operator[](int i) const { return to_f32(reinterpret_cast<const R*>(u)[i]); }
+};
+
+// R: the element type of the experts' rows. SPLIT: blockIdx.y takes a part of
+// the columns. Without it the kernel fits 40 registers and four CTAs an SM
+// (8191 tokens x 4 slots of 2880: 41 us against 47).
+template <typename R, typename T, int VB, bool SPLIT>
+__global__ void __launch_bounds__(kMoveThreads, SPLIT || sizeof(R) > sizeof(T) ? 3 : 4)
+return_kernel(RouteArgs a, MoveShape m) {
   using U = typename Bytes<VB>::type;
   constexpr int EV = VB / (int)sizeof(T);
   const int ntok = (int)a.ntok, top_k = a.top_k;
@@ -254,18 +269,17 @@ __global__ void __launch_bounds__(kMoveThreads, SPLIT ? 3 : 4) return_kernel(Rou
     const int32_t* rows = a.row_of_slot + (int64_t)t * top_k;
     for (int v = (SPLIT ? blockIdx.y * blockDim.x : 0u) + threadIdx.x; v < m.vecs;
          v += (SPLIT ? gridDim.y : 1u) * blockDim.x) {
-      const U* in = static_cast<const U*>(a.rows) + v;
       float acc[EV];
 #pragma unroll
       for (int i = 0; i < EV; ++i) acc[i] = 0.0f;
       for (int j0 = 0; j0 < top_k; j0 += kSlotGroup) {
-        U x[kSlotGroup];
+        RowVec<R, EV> x[kSlotGroup];
         uint32_t live = 0;
 #pragma unroll
         for (int j = 0; j < kSlotGroup; ++j) {
           const int r = j0 + j < top_k ? __ldg(rows + j0 + j) : -1;
           if (r >= 0) {
-            x[j] = __ldg(in + (int64_t)r * m.vecs);
+            x[j].load(a.rows, (int64_t)r * m.vecs + v);
             live |= 1u << j;
           }
         }
@@ -273,9 +287,8 @@ __global__ void __launch_bounds__(kMoveThreads, SPLIT ? 3 : 4) return_kernel(Rou
         for (int j = 0; j < kSlotGroup; ++j) {
           if (live >> j & 1u) {
             const float w = a.weights != nullptr ? __ldg(a.weights + (int64_t)t * top_k + j0 + j) : 1.0f;
-            const T* e = reinterpret_cast<const T*>(&x[j]);
 #pragma unroll
-            for (int i = 0; i < EV; ++i) acc[i] = fmaf(w, to_f32(e[i]), acc[i]);
+            for (int i = 0; i < EV; ++i) acc[i] = fmaf(w, x[j][i], acc[i]);
           }
         }
       }
@@ -415,11 +428,15 @@ cudaError_t by_type(const RouteArgs& a, const RowShape& s) {
   }
 }
 
+template <typename R, typename T, int VB>
+cudaError_t go_return(const RouteArgs& a, const RowShape& s) {
+  return s.grid.y > 1 ? launch_pdl(return_kernel<R, T, VB, true>, s.grid, s.block, 0, a.stream, a, s.move)
+                      : launch_pdl(return_kernel<R, T, VB, false>, s.grid, s.block, 0, a.stream, a, s.move);
+}
 template <typename T, int VB>
 struct Return {
   static cudaError_t go(const RouteArgs& a, const RowShape& s) {
-    return s.grid.y > 1 ? launch_pdl(return_kernel<T, VB, true>, s.grid, s.block, 0, a.stream, a, s.move)
-                        : launch_pdl(return_kernel<T, VB, false>, s.grid, s.block, 0, a.stream, a, s.move);
+    return a.rows_f32 ? go_return<float, T, VB>(a, s) : go_return<T, T, VB>(a, s);
   }
 };
 template <typename T, int VB>

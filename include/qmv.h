@@ -566,8 +566,9 @@ int qmv_moe_return_grad(int32_t type, const void* dy_dev, int64_t ld_dy, const v
  * down, weighted return:
  *   y[t] = sum_j weights[t][j] * W_down[e] . Q(silu(W_gate[e] . Q(x[t])) * (W_up[e] . Q(x[t]))),  e = ids[t][j],
  * Q the quantization to the projection's MX format; MXFP4 and MXFP8 may be
- * mixed as in qmv_moe_layer. The experts' rows are rounded to `type` before
- * they are weighted. Descriptors and packed weights as qmv_moe_layer; x
+ * mixed as in qmv_moe_layer. The experts' rows stay in fp32 until they are
+ * weighted and summed where they take at most 32 MB so; larger calls round them
+ * to `type` first. Descriptors and packed weights as qmv_moe_layer; x
  * [ntok][K] of `type` (bf16 or fp16), rows ldx apart; y `type` [ntok][N_down].
  * Five launches. workspace: as qmv_moe_layer.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.

@@ -479,29 +479,32 @@ def layer_case(gu_fmt, dn_fmt, dtype, ntok, top_k, E, K, N, N_down, drop, seed=0
     return gu, w_gu, dn, w_dn, x, ids, dev(weights), (gc, gs, uc, us, dc, ds)
 
 
+def split_layer(gu, w_gu, dn, w_dn, dtype, x, ids, weights, E, K, N, N_down, ys_type):
+    """The layer's calls one by one: (h buffer, the experts' rows, row_of_slot)."""
+    (ntok, top_k), n = ids.shape, ids.size
+    offsets, row, _ = sorted_on_gpu(ids, E)
+    xq, hq = buf(qmv.qmv_act_mx_bytes(gu.fmt, n, K)), buf(qmv.qmv_act_mx_bytes(dn.fmt, n, N))
+    ys = torch.zeros(n, N_down, dtype=TORCH[ys_type], device=DEV)
+    qmv.qmv_moe_dispatch_mx(gu.fmt, dtype, x, K, ntok, top_k, K, row, xq)
+    qmv.qmv_mx_gate_up_swiglu(gu, w_gu, xq, n, offsets, dn.fmt, hq)
+    qmv.qmv_mx_product(dn, w_dn, hq, n, offsets, ys_type, ys)
+    return hq, ys, row
+
+
 @pytest.mark.parametrize("gu_fmt,dn_fmt,dtype,ntok,top_k,E,K,N,N_down,drop", [
     ("mxfp4", "mxfp4", "bf16", 1, 1, 1, 32, 32, 1, 0), ("mxfp4", "mxfp8", "bf16", 5, 2, 4, 96, 160, 40, 0.3),
     ("mxfp8", "mxfp8", "f16", 140, 2, 3, 288, 96, 200, 0), ("mxfp8", "mxfp4", "bf16", 33, 4, 32, 1056, 224, 264, 0.1),
     ("mxfp4", "mxfp4", "f16", 3, 2, 4, 64, 64, 64, 1.0)])
-def test_prefill_layer_is_its_parts(gu_fmt, dn_fmt, dtype, ntok, top_k, E, K, N, N_down, drop):
-    """The layer equals its five calls bit for bit, and the definition within the h codes' freedom: the products
-    of the h that the gate/up call stored, weighted, within the bounds of the product and the return."""
+def test_prefill_layer(gu_fmt, dn_fmt, dtype, ntok, top_k, E, K, N, N_down, drop):
+    """The layer against the definition, within the h codes' freedom: h as the gate/up call quantizes it, then its
+    products, weighted, within the bounds of the product and of an fp32 sum."""
     gu, w_gu, dn, w_dn, x, ids, weights, (gc, gs, uc, us, dc, ds) = layer_case(gu_fmt, dn_fmt, dtype, ntok, top_k, E, K, N,
                                                                                N_down, drop)
     n = ntok * top_k
     ws = buf(qmv.qmv_moe_prefill_layer_workspace_bytes(gu, dn, ntok, top_k))
     y = torch.full((ntok, N_down), 7.0, dtype=TORCH[dtype], device=DEV)
     qmv.qmv_moe_prefill_layer(gu, w_gu, dn, w_dn, dtype, x, K, dev(ids), weights, ntok, top_k, ws, y)
-
-    offsets, row, _ = sorted_on_gpu(ids, E)
-    xq, hq = buf(qmv.qmv_act_mx_bytes(gu_fmt, n, K)), buf(qmv.qmv_act_mx_bytes(dn_fmt, n, N))
-    ys = torch.zeros(n, N_down, dtype=TORCH[dtype], device=DEV)
-    y2 = torch.empty_like(y)
-    qmv.qmv_moe_dispatch_mx(gu_fmt, dtype, x, K, ntok, top_k, K, row, xq)
-    qmv.qmv_mx_gate_up_swiglu(gu, w_gu, xq, n, offsets, dn_fmt, hq)
-    qmv.qmv_mx_product(dn, w_dn, hq, n, offsets, dtype, ys)
-    qmv.qmv_moe_return(dtype, ys, weights, ntok, top_k, N_down, row, y2, N_down)
-    assert torch.equal(y, y2)
+    hq, _, _ = split_layer(gu, w_gu, dn, w_dn, dtype, x, ids, weights, E, K, N, N_down, "f32")
 
     off, r, slot = ref.sort_slots(ids, E)
     hc, hs = unpacked(dn_fmt, hq, n, N)
@@ -521,10 +524,32 @@ def test_prefill_layer_is_its_parts(gu_fmt, dn_fmt, dtype, ntok, top_k, E, K, N,
         hv = ref.decode(hc[a:b], hs[a:b], dn_fmt)
         prod, absum = hv @ wd.T, np.abs(hv) @ np.abs(wd).T
         wt = host(weights).reshape(-1)[slot[a:b], None]
-        half = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
         np.add.at(want, tok, wt * prod)
-        np.add.at(bound, tok, wt * (1e-3 * absum + half * (np.abs(prod) + 1e-3 * absum) + 2.0 ** -24) * (1 + top_k * 2.0 ** -23))
+        np.add.at(bound, tok, wt * (1e-3 * absum + top_k * 2.0 ** -23 * np.abs(prod)))
     assert_within(host(y), want, bound, dtype, "layer")
+    assert status_clean()
+
+
+@pytest.mark.parametrize("gu_fmt,dn_fmt,dtype,ntok,top_k,E,K,N,N_down,drop,ys_type", [
+    ("mxfp4", "mxfp8", "bf16", 130, 4, 8, 288, 160, 264, 0.1, "f32"),
+    ("mxfp8", "mxfp4", "f16", 1100, 2, 4, 96, 64, 4000, 0.05, "f16"), ("mxfp4", "mxfp4", "bf16", 4200, 2, 16, 64, 96, 1024, 0, "bf16")])
+def test_prefill_layer_is_its_parts(gu_fmt, dn_fmt, dtype, ntok, top_k, E, K, N, N_down, drop, ys_type):
+    """The layer equals its calls made one by one, bit for bit: with the experts' rows in fp32 up to 32 MB of them, in the
+    output's type above. fp32 rows are weighted here in float64 and compared as a sum of fp32 terms."""
+    gu, w_gu, dn, w_dn, x, ids, weights, _ = layer_case(gu_fmt, dn_fmt, dtype, ntok, top_k, E, K, N, N_down, drop)
+    assert (ntok * top_k * N_down * 4 <= 32 << 20) == (ys_type == "f32")
+    ws = buf(qmv.qmv_moe_prefill_layer_workspace_bytes(gu, dn, ntok, top_k))
+    y = torch.full((ntok, N_down), 7.0, dtype=TORCH[dtype], device=DEV)
+    qmv.qmv_moe_prefill_layer(gu, w_gu, dn, w_dn, dtype, x, K, dev(ids), weights, ntok, top_k, ws, y)
+    _, ys, row = split_layer(gu, w_gu, dn, w_dn, dtype, x, ids, weights, E, K, N, N_down, ys_type)
+    if ys_type != "f32":
+        y2 = torch.empty_like(y)
+        qmv.qmv_moe_return(dtype, ys, weights, ntok, top_k, N_down, row, y2, N_down)
+        assert torch.equal(y, y2)
+    else:
+        r = row.cpu().numpy().reshape(ntok, top_k)
+        terms = np.where((r >= 0)[..., None], host(ys)[np.where(r >= 0, r, ~r)], 0) * host(weights)[..., None]
+        assert_within(host(y), terms.sum(1), (top_k + 1) * 2.0 ** -24 * np.abs(terms).sum(1), dtype, "layer")
     assert status_clean()
 
 
