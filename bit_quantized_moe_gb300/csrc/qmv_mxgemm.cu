@@ -59,9 +59,9 @@ struct GemmFmt {
   static constexpr int atoms = step_k / 128;                // scale words of a row per step
   static constexpr int steps_per_chunk = kChunkK / step_k;
   static constexpr uint32_t a_bytes = kTileM * 128;
-  // Rows of one copy of activations. Single CTAs' tiles often have few rows, and copies of rows that are not there are
-  // not free (17 rows: boxes of 128 rows took longer than 128 rows did): they copy 32 at a time, as many as live ones.
-  static constexpr int x_rows = PAIR ? kTileM : 32;
+  // Rows of one copy of activations: a CTA makes as many as its live rows need. Copies of rows that are not there are
+  // not free (17 rows: boxes of 128 rows took longer than 128 rows did), and an expert's last tile is half empty.
+  static constexpr int x_rows = PAIR ? 64 : 32;
   static constexpr int b_rows = PAIR ? TN / 2 : TN;         // a pair's CTAs hold half of the weights each
   static constexpr uint32_t b_bytes = b_rows * 128;
   static constexpr uint32_t stage_bytes = a_bytes + b_bytes;
@@ -530,21 +530,21 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
       for (int t = t0; t < tiles && ok; t += dt) {
         const Tile tile = tile_of(t);
         const int rt = tile.n * (TN / 8) + rank * (F::b_rows / 8);
-        const int copies = (min(tile.rows, kTileM) + F::x_rows - 1) / F::x_rows;
+        const auto copies_of = [](int rows) { return (max(0, min(rows, kTileM)) + F::x_rows - 1) / F::x_rows; };
+        const int copies = copies_of(tile.rows);
+        // bytes of a step that the leader's barrier waits for; rows past the last copy keep what the stage held: their
+        // products are not stored
+        const uint32_t bytes = (uint32_t)(copies + (PAIR ? copies_of(tile.rows - kTileM) : 0)) * F::x_rows * 128 +
+                               kCtas * F::b_bytes;
         for (int s = 0; s < steps; ++s, ++it) {
           const int st = it % kStages;
           if (!wait_used(it, kStages)) { ok = false; break; }
           uint32_t bar = smem_addr(&full[st]);
           const uint32_t dst = smem_addr(stages + (uint32_t)st * F::stage_bytes);
-          if constexpr (PAIR) {
-            if (rank == 0) mbar_arrive_expect_tx(bar, kCtas * (F::a_bytes + F::b_bytes));
-            bar = leader_addr(bar);
-            tma_load_2d<PAIR>(dst, &map_x, s * 128, tile.row0, bar);
-          } else {   // rows past the last live copy keep what the stage held: their products are not stored
-            mbar_arrive_expect_tx(bar, (uint32_t)copies * F::x_rows * 128 + F::b_bytes);
-            for (int i = 0; i < copies; ++i) {
-              tma_load_2d<PAIR>(dst + (uint32_t)i * F::x_rows * 128, &map_x, s * 128, tile.row0 + i * F::x_rows, bar);
-            }
+          if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
+          if constexpr (PAIR) bar = leader_addr(bar);
+          for (int i = 0; i < copies; ++i) {
+            tma_load_2d<PAIR>(dst + (uint32_t)i * F::x_rows * 128, &map_x, s * 128, tile.row0 + i * F::x_rows, bar);
           }
           const int chunk = s / F::steps_per_chunk;
           const int x = (s % F::steps_per_chunk) * 128;

@@ -225,63 +225,78 @@ cudaError_t launch_rms_norm(const NormArgs& a) {
 
 // ---------------------------------------------------------------------------
 // Microscaled quantization of rows (and, with row_of_slot, their dispatch to
-// the experts' order). Sixteen lanes take 128 columns of one row: 16 bytes in
-// per lane (bf16), a group's maximum by two shuffles, codes and one scale word
-// out. A routed token is read and quantized once and written to its top_k
-// rows; a dropped slot's row (~row in row_of_slot) is written as zeros.
+// the experts' order). A thread takes a group of 32 columns: 64 bytes in (bf16)
+// under way at once, the maximum without another lane, 16 or 32 bytes of codes
+// out; four lanes' scale bytes make a word. (Eight columns a thread, with
+// shuffles for the maximum, took 29.5 us for 8192 x 7168 to MXFP4.) A routed
+// token is read and quantized once and written to its top_k rows; a dropped
+// slot's row (~row in row_of_slot) is written as zeros.
 // Bound by memory: 2 bytes in, 0.53 (E2M1) or 1.03 (E4M3) out per row.
 // ---------------------------------------------------------------------------
-template <typename T, int FMT, bool ROUTED, bool VEC, int U>
+template <typename T, int FMT, bool ROUTED, bool VEC>
 __global__ void __launch_bounds__(256)
 quantize_mx_kernel(QuantArgs a) {
-  const int lane = threadIdx.x & 31;
+  constexpr int kWords = FMT == MXFP4 ? 4 : 8;   // of a group's codes
   const unsigned words = (unsigned)mx_scale_words(a.K);
-  const unsigned total = (unsigned)a.ntok * words;   // at most 2^22 rows of 2^9 words
-  const unsigned unit0 = blockIdx.x * (16u * U) + threadIdx.x / 16u;   // U units of 128 columns, 16 apart
-  Raw8<T> raw[U];
-  unsigned t[U], kb[U];
+  const unsigned unit = blockIdx.x * 64u + threadIdx.x / 4u;   // 128 columns of a row, four lanes
+  const unsigned total = (unsigned)a.ntok * words;             // at most 2^22 rows of 2^9 words
+  const bool live = unit < total;
+  const unsigned t = live ? unit / words : 0u, kb = live ? unit - t * words : 0u;
+  const int c = (int)(kb * 128u) + (int)(threadIdx.x & 3u) * 32;
+  const bool in = live && c < a.K;
   pdl_wait();
+  Raw8<T> raw[4];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const unsigned unit = unit0 + 16u * i;
-    t[i] = unit < total ? unit / words : 0u;
-    kb[i] = unit - t[i] * words;
-    const int c = (int)(kb[i] * 128u) + (lane & 15) * 8;
-    if (unit < total && c < a.K) load_raw8<T, VEC>(static_cast<const T*>(a.x) + (int64_t)t[i] * a.ldx + c, raw[i]);
+  for (int i = 0; i < 4; ++i) {
+    if (in) load_raw8<T, VEC>(static_cast<const T*>(a.x) + (int64_t)t * a.ldx + c + 8 * i, raw[i]);
     else clear_raw8(raw[i]);
   }
-  uint8_t* out = static_cast<uint8_t*>(a.xq);
-  const uint64_t row_bytes = mx_row_bytes(FMT, a.K);
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const bool live = unit0 + 16u * i < total;
-    const int c = (int)(kb[i] * 128u) + (lane & 15) * 8;
-    const bool in = live && c < a.K;
+  for (int i = 0; i < 4; ++i) m = max(m, amax_bits8(raw[i]));
+  const uint32_t e = group_e8m0<FMT>(m);
+  uint4 codes[kWords / 4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = to_f32(raw[i].e[k]);
-    uint32_t m = amax_bits8(raw[i]);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t e = group_e8m0<FMT>(m);
-    uint32_t w[FMT == MXFP4 ? 1 : 2];
-    mx_codes8<FMT>(v, e, w);
-    const uint32_t word = scale_word16(e);
-    uint32_t* scales = reinterpret_cast<uint32_t*>(out + a.scale_offset) + (int64_t)kb[i] * a.nrows;
-    if constexpr (!ROUTED) {
-      if (in) store_codes8<FMT>(out + t[i] * row_bytes, c, w);
-      if (live && (lane & 15) == 0) scales[t[i]] = word;
-    } else if (live) {
-      for (int j = 0; j < a.top_k; ++j) {
-        const int r = __ldg(a.row_of_slot + (int64_t)t[i] * a.top_k + j);
-        const bool keep = r >= 0;
-        const int row = keep ? r : ~r;
-        uint32_t z[FMT == MXFP4 ? 1 : 2];
+    mx_codes8<FMT>(v, e, *reinterpret_cast<uint32_t(*)[kWords / 4]>(reinterpret_cast<uint32_t*>(codes) + i * (kWords / 4)));
+  }
+  // E4M3: two lanes trade halves, so that each store of a lane pair fills a group's 32 bytes
+  // (8191 tokens to 4 rows of 2880 each: 30.3 us with a lane's own two stores).
+  const bool odd = (threadIdx.x & 1u) != 0;
+  const int c0 = c - (odd ? 32 : 0);   // the pair's first group
+  if constexpr (FMT == MXFP8) {
+    uint4 other = odd ? codes[0] : codes[1];
+    other.x = __shfl_xor_sync(0xffffffffu, other.x, 1);
+    other.y = __shfl_xor_sync(0xffffffffu, other.y, 1);
+    other.z = __shfl_xor_sync(0xffffffffu, other.z, 1);
+    other.w = __shfl_xor_sync(0xffffffffu, other.w, 1);
+    if (odd) codes[0] = other;
+    else codes[1] = other;
+  }
+  // the unit's four scale bytes, in its first lane
+  uint32_t word = e | __shfl_down_sync(0xffffffffu, e, 1) << 8;
+  word |= __shfl_down_sync(0xffffffffu, word, 2) << 16;
+  uint8_t* out = static_cast<uint8_t*>(a.xq);
+  const uint64_t row_bytes = mx_row_bytes(FMT, a.K);
+  const int at = FMT == MXFP8 ? c0 + (odd ? 16 : 0) : c / 2;
+  uint32_t* scales = reinterpret_cast<uint32_t*>(out + a.scale_offset) + (int64_t)kb * a.nrows;
+  if (live) {
+    const int copies = ROUTED ? a.top_k : 1;
+#pragma unroll 4
+    for (int j = 0; j < copies; ++j) {
+      const int r = ROUTED ? __ldg(a.row_of_slot + (int64_t)t * copies + j) : (int)t;
+      const bool keep = r >= 0;
+      const int row = keep ? r : ~r;
 #pragma unroll
-        for (int k = 0; k < (FMT == MXFP4 ? 1 : 2); ++k) z[k] = keep ? w[k] : 0u;
-        if (in) store_codes8<FMT>(out + (uint64_t)row * row_bytes, c, z);
-        if ((lane & 15) == 0) scales[row] = keep ? word : 0u;
+      for (int i = 0; i < kWords / 4; ++i) {
+        if (FMT == MXFP8 ? c0 + 32 * i < a.K : in) {
+          *reinterpret_cast<uint4*>(out + (uint64_t)row * row_bytes + at + 32 * i) = keep ? codes[i] : make_uint4(0, 0, 0, 0);
+        }
       }
+      if ((threadIdx.x & 3u) == 0) scales[row] = keep ? word : 0u;
     }
   }
   pdl_launch_dependents();
@@ -289,25 +304,17 @@ quantize_mx_kernel(QuantArgs a) {
 
 namespace {
 
-template <typename T, int FMT, bool ROUTED, bool VEC>
-cudaError_t quant_launch(const QuantArgs& a) {
-  // Two units in flight a thread once that still gives every SM threads enough
-  // (8192 x 7168 to MXFP4: 29.6 us; one unit 33.5, four 31.1, eight 43.8).
-  const int64_t units = a.ntok * mx_scale_words(a.K);
-  constexpr int U = 2;
-  if (units >= (int64_t)device_sm_count() * 16 * 8 * U) {
-    return launch_pdl(quantize_mx_kernel<T, FMT, ROUTED, VEC, U>, dim3((unsigned)((units + 16 * U - 1) / (16 * U))),
-                      dim3(256), 0, a.stream, a);
-  }
-  return launch_pdl(quantize_mx_kernel<T, FMT, ROUTED, VEC, 1>, dim3((unsigned)((units + 15) / 16)), dim3(256), 0,
-                    a.stream, a);
-}
-
 template <typename T, int FMT>
 cudaError_t quant_go(const QuantArgs& a) {
+  const int64_t units = a.ntok * mx_scale_words(a.K);
+  const dim3 grid((unsigned)((units + 63) / 64)), block(256);
   const bool vec = a.ldx % (16 / (int)sizeof(T)) == 0;
-  if (a.row_of_slot != nullptr) return vec ? quant_launch<T, FMT, true, true>(a) : quant_launch<T, FMT, true, false>(a);
-  return vec ? quant_launch<T, FMT, false, true>(a) : quant_launch<T, FMT, false, false>(a);
+  if (a.row_of_slot != nullptr) {
+    return vec ? launch_pdl(quantize_mx_kernel<T, FMT, true, true>, grid, block, 0, a.stream, a)
+               : launch_pdl(quantize_mx_kernel<T, FMT, true, false>, grid, block, 0, a.stream, a);
+  }
+  return vec ? launch_pdl(quantize_mx_kernel<T, FMT, false, true>, grid, block, 0, a.stream, a)
+             : launch_pdl(quantize_mx_kernel<T, FMT, false, false>, grid, block, 0, a.stream, a);
 }
 
 template <typename T>
