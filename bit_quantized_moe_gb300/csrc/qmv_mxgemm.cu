@@ -29,8 +29,9 @@
 //   4..11  the epilogue, one warpgroup an accumulator: a thread has a row's
 //          columns in order, so SwiGLU, a group's maximum and its quantization
 //          need no other thread
-//   2, 3, 12..19  read the scales of one step in ten each, a turn ahead, and
+//   3, 12..19  read the scales of one step in nine each, a turn ahead, and
 //          write them as tcgen05.cp wants them
+//   2      tells warp 1, on the codes' barrier, that a step's scales are there
 // Tiles of an expert follow one another along its rows, so that its weights
 // are read from memory once and again from L2.
 #include <atomic>
@@ -45,7 +46,7 @@ namespace qmv {
 
 constexpr int kTileM = 128;        // rows of activations of one CTA
 constexpr int kGemmThreads = 640;
-constexpr int kScaleWarps = 10;     // warps 2, 3 and 12..19 (six: 8192 x 7168 x 7168 MXFP4 152 us, ten: 143)
+constexpr int kScaleWarps = 9;      // warps 3 and 12..19 (six: 8192 x 7168 x 7168 MXFP4 152 us, ten: 143)
 // Columns of 16-bit outputs that a thread parks in shared memory before its
 // warp stores them row by row, and the pitch of a row there (an odd number of
 // 16 bytes: no bank conflicts between rows).
@@ -72,15 +73,17 @@ struct GemmFmt {
   static constexpr uint32_t sf_bytes = sfa_bytes + sfb_bytes;
   static constexpr uint32_t atom_cols = 4 + 4 * b_blocks;   // tensor memory columns of 128 columns' scales
   static constexpr uint32_t sf_cols = atoms * atom_cols;
-  static constexpr int stages = PAIR ? 5 : (TN == 128 ? 5 : 7);
+  static constexpr int stages = PAIR ? 6 : (TN == 128 ? 5 : 7);
   // Steps that the scales may be ahead. At least the scale warps: a warp may then not be two uses of a place ahead of
   // the MMAs, which its barrier's phase bit could not tell from none.
-  static constexpr int sf_stages = 10;
+  static constexpr int sf_stages = 9;
   static_assert(kScaleWarps <= sf_stages && stages <= sf_stages, "phases of the barriers");
   static constexpr uint32_t park_bytes = 2 * kTileM * kParkPitch;
   static constexpr uint32_t sf_col0 = 2 * TN;               // scales follow the two accumulators
-  static constexpr uint32_t tmem_cols = sf_col0 + stages * sf_cols <= 256 ? 256 : 512;
-  static_assert(sf_col0 + stages * sf_cols <= tmem_cols, "tensor memory");
+  // Steps whose scales tensor memory holds; a step waits for the MMAs of the one whose place it takes.
+  static constexpr int sf_slots = (int)((512 - sf_col0) / sf_cols) < stages ? (int)((512 - sf_col0) / sf_cols) : stages;
+  static constexpr uint32_t tmem_cols = sf_col0 + sf_slots * sf_cols <= 256 ? 256 : 512;
+  static_assert(sf_slots >= 4 && sf_col0 + sf_slots * sf_cols <= tmem_cols, "tensor memory");
 };
 
 struct GemmParams {
@@ -221,20 +224,14 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
   else return mbar_wait_bounded(bar, parity, kWaitLimitNs);
 }
 // Whether a phase is already complete; does not wait.
-template <bool PAIR>
 __device__ __forceinline__ bool peek(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  if constexpr (PAIR) {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  } else {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  }
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
+
 __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
@@ -446,7 +443,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
   uint8_t* park = scales + F::sf_stages * F::sf_bytes;
   int* first_tile = reinterpret_cast<int*>(park + F::park_bytes);   // [n_experts + 1]
   int* first_row = first_tile + p.n_experts + 1;                    // [n_experts + 1]
-  // Barriers of a step: its codes and its scales have arrived, its MMAs are complete. The scales run up to 2 kStages
+  // Barriers of a step: all of it has arrived, its scales have, its MMAs are complete. The scales run up to sf_stages
   // steps ahead, the codes kStages; both wait for the MMAs of the step whose place they take.
   __shared__ __align__(8) uint64_t full[F::stages], sf_full[F::sf_stages], used[F::sf_stages];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], done;
@@ -523,42 +520,44 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     return j < 0 || wait_for<false>(smem_addr(&used[j % F::sf_stages]), (j / F::sf_stages) & 1);
   };
 
+  // Copies of F::x_rows rows that a CTA with so many rows of the tile left makes. Rows past the last copy keep what the
+  // stage held: their products are not stored.
+  const auto x_copies = [](int rows) { return (max(0, min(rows, kTileM)) + F::x_rows - 1) / F::x_rows; };
+
   if (warp == 0) {
-    // ---- copies of codes
-    int it = 0;
-    if (elect_one()) {
-      for (int t = t0; t < tiles && ok; t += dt) {
-        const Tile tile = tile_of(t);
-        const int rt = tile.n * (TN / 8) + rank * (F::b_rows / 8);
-        const auto copies_of = [](int rows) { return (max(0, min(rows, kTileM)) + F::x_rows - 1) / F::x_rows; };
-        const int copies = copies_of(tile.rows);
-        // bytes of a step that the leader's barrier waits for; rows past the last copy keep what the stage held: their
-        // products are not stored
-        const uint32_t bytes = (uint32_t)(copies + (PAIR ? copies_of(tile.rows - kTileM) : 0)) * F::x_rows * 128 +
-                               kCtas * F::b_bytes;
-        for (int s = 0; s < steps; ++s, ++it) {
-          const int st = it % kStages;
-          if (!wait_used(it, kStages)) { ok = false; break; }
-          uint32_t bar = smem_addr(&full[st]);
-          const uint32_t dst = smem_addr(stages + (uint32_t)st * F::stage_bytes);
-          if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
-          if constexpr (PAIR) bar = leader_addr(bar);
+    // ---- copies of codes (the same in all lanes, one issues; as the products' warp)
+    const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
+    const uint32_t code0 = smem_addr(stages);
+    int it = 0, st = 0;
+    for (int n = 0; n < my_tiles && ok; ++n) {
+      Tile tile = tile_of(t0 + n * dt);
+      tile.expert = __shfl_sync(0xffffffffu, tile.expert, 0);
+      tile.row0 = __shfl_sync(0xffffffffu, tile.row0, 0);
+      tile.n = __shfl_sync(0xffffffffu, tile.n, 0);
+      const int copies = __shfl_sync(0xffffffffu, x_copies(tile.rows), 0);
+      const int rt = tile.n * (TN / 8) + rank * (F::b_rows / 8);
+      int chunk = 0, x = 0;   // of the step in the weights
+      for (int s = 0; s < steps; ++s, ++it) {
+        if (!__all_sync(0xffffffffu, wait_used(it, kStages))) { ok = false; break; }
+        uint32_t bar = smem_addr(&full[st]);
+        if constexpr (PAIR) bar = leader_addr(bar);
+        const uint32_t dst = code0 + (uint32_t)st * F::stage_bytes;
+        if (elect_one()) {
+          if (chunk < p.chunks_full) tma_load_5d<PAIR>(dst + F::a_bytes, &map_w, x, 0, rt, chunk, tile.expert, bar);
+          else tma_load_5d<PAIR>(dst + F::a_bytes, &map_last, x, 0, rt, 0, tile.expert, bar);
           for (int i = 0; i < copies; ++i) {
             tma_load_2d<PAIR>(dst + (uint32_t)i * F::x_rows * 128, &map_x, s * 128, tile.row0 + i * F::x_rows, bar);
           }
-          const int chunk = s / F::steps_per_chunk;
-          const int x = (s % F::steps_per_chunk) * 128;
-          if (chunk < p.chunks_full) {
-            tma_load_5d<PAIR>(dst + F::a_bytes, &map_w, x, 0, rt, chunk, tile.expert, bar);
-          } else {
-            tma_load_5d<PAIR>(dst + F::a_bytes, &map_last, x, 0, rt, 0, tile.expert, bar);
-          }
+        }
+        __syncwarp();
+        if (++st == kStages) st = 0;
+        x += 128;
+        if (x == F::steps_per_chunk * 128) {
+          x = 0;
+          ++chunk;
         }
       }
     }
-    __syncwarp();
-    it = __reduce_max_sync(0xffffffffu, it);
-    ok = __all_sync(0xffffffffu, ok);
     if (!ok) {   // leave no copy in flight
       if constexpr (PAIR) {
         const unsigned long long from = global_timer_ns();   // the copies report to the leader: give them their time
@@ -578,9 +577,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
       const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t code0 = smem_addr(stages), scale0 = smem_addr(scales);
-      int st = 0, ss = 0;                   // places of the step's codes and scales,
-      uint32_t st_phase = 0, ss_phase = 0;  // and their barriers' phases
-      // a step's barriers are looked at before the step before it is issued: the look's latency is then hidden
+      int st = 0, ss = 0, sl = 0;   // places of the step's codes, its scales, and these in tensor memory
+      uint32_t st_phase = 0;
+      // a step's barrier is looked at before the step before it is issued: the look's latency is then hidden
       bool ready = false;
       for (int n = 0; n < my_tiles && ok; ++n) {
         const int acc = n & 1;
@@ -589,20 +588,19 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         const uint32_t d = tm + (uint32_t)(acc * TN);
         int left = p.K;
         for (int s = 0; s < steps; ++s, left -= F::step_k) {
-          if (!ready && !__all_sync(0xffffffffu, wait_for<PAIR>(smem_addr(&sf_full[ss]), ss_phase) &&
-                                                     wait_for<false>(smem_addr(&full[st]), st_phase))) {
+          if (!ready && !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&full[st]), st_phase))) {
             ok = false;
             break;
           }
           tc_after_sync();
           const uint32_t a0 = code0 + (uint32_t)st * F::stage_bytes, b0 = a0 + F::a_bytes;
           const uint32_t sfa = scale0 + (uint32_t)ss * F::sf_bytes, sfb = sfa + F::sfa_bytes;
-          const uint32_t sf = tm + F::sf_col0 + (uint32_t)st * F::sf_cols;
+          const uint32_t sf = tm + F::sf_col0 + (uint32_t)sl * F::sf_cols;
           const uint32_t used_bar = smem_addr(&used[ss]);
           if (++st == kStages) { st = 0; st_phase ^= 1; }
-          if (++ss == F::sf_stages) { ss = 0; ss_phase ^= 1; }
-          ready = __all_sync(0xffffffffu, peek<PAIR>(smem_addr(&sf_full[ss]), ss_phase) &
-                                              peek<false>(smem_addr(&full[st]), st_phase));
+          if (++ss == F::sf_stages) ss = 0;
+          if (++sl == F::sf_slots) sl = 0;
+          ready = __all_sync(0xffffffffu, peek(smem_addr(&full[st]), st_phase));
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < F::atoms; ++k) {
@@ -639,10 +637,30 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
       __syncwarp();
       if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
     }
-  } else if (warp < 4 || warp >= 12) {
-    // ---- scales: every tenth step, loaded one turn ahead of its slot in the ring
+  } else if (warp == 2) {
+    // ---- a step's one arrival, with the bytes to wait for, once its scales are there and their place in tensor memory
+    // is free: the products then look at one barrier
+    if (rank == 0) {
+      int it = 0;
+      for (int t = t0; t < tiles && ok; t += dt) {
+        const int rows = tile_of(t).rows;
+        const uint32_t bytes = (uint32_t)(x_copies(rows) + (PAIR ? x_copies(rows - kTileM) : 0)) * F::x_rows * 128 +
+                               kCtas * F::b_bytes;
+        for (int s = 0; s < steps; ++s, ++it) {
+          if (!wait_for<PAIR>(smem_addr(&sf_full[it % F::sf_stages]), (it / F::sf_stages) & 1) ||
+              !wait_used(it, F::sf_slots)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(smem_addr(&full[it % kStages]), bytes);
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp == 3 || warp >= 12) {
+    // ---- scales: every ninth step, loaded one turn ahead of its slot in the ring
     StepScales<FMT, TN> cur;
-    int it = warp < 4 ? warp - 2 : warp - 10;
+    int it = warp == 3 ? 0 : warp - 11;
     int t = t0, s = it;
     Tile tile{};
     while (t < tiles && s >= steps) { s -= steps; t += dt; }
