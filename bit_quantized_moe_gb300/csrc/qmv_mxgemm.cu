@@ -336,7 +336,7 @@ struct StepScales {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t row = min((int64_t)t.row0 + lane + 32 * i, p.nrows - 1);   // rows past the last are not stored
-        a[k][i] = kb < words ? __ldg(p.x_scales + (int64_t)kb * p.nrows + row) : 0u;
+        a[k][i] = kb < words ? p.x_scales[(int64_t)kb * p.nrows + row] : 0u;
       }
     }
     const int chunk = step / F::steps_per_chunk;
@@ -483,8 +483,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
       const int e = e0 + lane;
       int lo = 0, hi = 0;
       if (e < p.n_experts) {
-        lo = p.offsets != nullptr ? __ldg(p.offsets + e) : 0;
-        hi = p.offsets != nullptr ? __ldg(p.offsets + e + 1) : (int)p.nrows;
+        lo = p.offsets != nullptr ? p.offsets[e] : 0;
+        hi = p.offsets != nullptr ? p.offsets[e + 1] : (int)p.nrows;
         // offsets that do not name rows of this call name none
         lo = max(0, min(lo, (int)p.nrows));
         hi = max(lo, min(hi, (int)p.nrows));

@@ -284,19 +284,29 @@ quantize_mx_kernel(QuantArgs a) {
   const int at = FMT == MXFP8 ? c0 + (odd ? 16 : 0) : c / 2;
   uint32_t* scales = reinterpret_cast<uint32_t*>(out + a.scale_offset) + (int64_t)kb * a.nrows;
   if (live) {
+    constexpr int kGroup = ROUTED ? 4 : 1;   // rows looked up together
     const int copies = ROUTED ? a.top_k : 1;
-#pragma unroll 4
-    for (int j = 0; j < copies; ++j) {
-      const int r = ROUTED ? __ldg(a.row_of_slot + (int64_t)t * copies + j) : (int)t;
-      const bool keep = r >= 0;
-      const int row = keep ? r : ~r;
+    for (int j0 = 0; j0 < copies; j0 += kGroup) {
+      int r[kGroup];
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        if (FMT == MXFP8 ? c0 + 32 * i < a.K : in) {
-          *reinterpret_cast<uint4*>(out + (uint64_t)row * row_bytes + at + 32 * i) = keep ? codes[i] : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < kGroup; ++j) {
+        r[j] = !ROUTED ? (int)t : (j0 + j < copies ? a.row_of_slot[(int64_t)t * copies + j0 + j] : 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        if (j0 + j < copies) {
+          const bool keep = r[j] >= 0;
+          const int row = keep ? r[j] : ~r[j];
+#pragma unroll
+          for (int i = 0; i < kWords / 4; ++i) {
+            if (FMT == MXFP8 ? c0 + 32 * i < a.K : in) {
+              *reinterpret_cast<uint4*>(out + (uint64_t)row * row_bytes + at + 32 * i) =
+                  keep ? codes[i] : make_uint4(0, 0, 0, 0);
+            }
+          }
+          if ((threadIdx.x & 3u) == 0) scales[row] = keep ? word : 0u;
         }
       }
-      if ((threadIdx.x & 3u) == 0) scales[row] = keep ? word : 0u;
     }
   }
   pdl_launch_dependents();

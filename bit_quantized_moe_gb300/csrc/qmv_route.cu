@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs a) {
   uint32_t* mine = hist + warp * E1;
   auto expert_of = [&](int64_t s) -> int {
     if (s >= s1) return -1;
-    const int e = __ldg(a.ids + s);
+    const int e = a.ids[s];
     return e >= 0 && e < a.n_experts ? e : a.n_experts;
   };
   // Counts 32 slots of a warp; the lane's own place among its warp's slots of its expert.
@@ -231,11 +231,18 @@ __global__ void __launch_bounds__(kMoveThreads, 4) dispatch_kernel(RouteArgs a, 
     const int32_t* rows = a.row_of_slot + (int64_t)t * top_k;
     const U* in = static_cast<const U*>(a.tok) + t * m.ld;
     for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < m.vecs; v += gridDim.y * blockDim.x) {
-      const U x = __ldg(in + v);
-#pragma unroll 4
-      for (int j = 0; j < top_k; ++j) {
-        const int r = __ldg(rows + j);
-        static_cast<U*>(a.out_rows)[(int64_t)(r >= 0 ? r : ~r) * m.vecs + v] = r >= 0 ? x : U{};
+      const U x = in[v];
+      for (int j0 = 0; j0 < top_k; j0 += kSlotGroup) {
+        int row[kSlotGroup];
+#pragma unroll
+        for (int j = 0; j < kSlotGroup; ++j) row[j] = j0 + j < top_k ? rows[j0 + j] : 0;
+#pragma unroll
+        for (int j = 0; j < kSlotGroup; ++j) {
+          if (j0 + j < top_k) {
+            const int r = row[j];
+            static_cast<U*>(a.out_rows)[(int64_t)(r >= 0 ? r : ~r) * m.vecs + v] = r >= 0 ? x : U{};
+          }
+        }
       }
     }
   }
@@ -250,7 +257,7 @@ struct RowVec {
   __device__ __forceinline__ void load(const void* rows, int64_t at) {
     const auto* p = static_cast<const typename Bytes<access>::type*>(rows) + at * count;
 #pragma unroll
-    for (int i = 0; i < count; ++i) u[i] = __ldg(p + i);
+    for (int i = 0; i < count; ++i) u[i] = __ldcg(p + i);
   }
   __device__ __forceinline__ float operator[](int i) const { return to_f32(reinterpret_cast<const R*>(u)[i]); }
 };
@@ -277,7 +284,7 @@ return_kernel(RouteArgs a, MoveShape m) {
         uint32_t live = 0;
 #pragma unroll
         for (int j = 0; j < kSlotGroup; ++j) {
-          const int r = j0 + j < top_k ? __ldg(rows + j0 + j) : -1;
+          const int r = j0 + j < top_k ? rows[j0 + j] : -1;
           if (r >= 0) {
             x[j].load(a.rows, (int64_t)r * m.vecs + v);
             live |= 1u << j;
@@ -286,7 +293,7 @@ return_kernel(RouteArgs a, MoveShape m) {
 #pragma unroll
         for (int j = 0; j < kSlotGroup; ++j) {
           if (live >> j & 1u) {
-            const float w = a.weights != nullptr ? __ldg(a.weights + (int64_t)t * top_k + j0 + j) : 1.0f;
+            const float w = a.weights != nullptr ? a.weights[(int64_t)t * top_k + j0 + j] : 1.0f;
 #pragma unroll
             for (int i = 0; i < EV; ++i) acc[i] = fmaf(w, x[j][i], acc[i]);
           }
@@ -323,13 +330,15 @@ __global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs 
 #pragma unroll
       for (int j = 0; j < kSlotGroup; ++j) dot[j] = 0.0f;
       for (int v = threadIdx.x; v < m.vecs; v += blockDim.x) {
-        const U g = __ldg(grad + v);
+        const U g = grad[v];
         U y[kSlotGroup];
         int row[kSlotGroup];
+        float w[kSlotGroup];
 #pragma unroll
         for (int j = 0; j < kSlotGroup; ++j) {
-          row[j] = j0 + j < top_k ? __ldg(rows + j0 + j) : -1;
-          if (row[j] >= 0) y[j] = __ldg(static_cast<const U*>(a.rows) + (int64_t)row[j] * m.vecs + v);
+          row[j] = j0 + j < top_k ? rows[j0 + j] : -1;
+          w[j] = j0 + j < top_k ? weights[j0 + j] : 0.0f;
+          if (row[j] >= 0) y[j] = static_cast<const U*>(a.rows)[(int64_t)row[j] * m.vecs + v];
         }
         const T* ge = reinterpret_cast<const T*>(&g);
 #pragma unroll
@@ -337,14 +346,13 @@ __global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs 
           if (j0 + j < top_k) {
             U out{};
             if (row[j] >= 0) {
-              const float w = __ldg(weights + j0 + j);
               const T* ye = reinterpret_cast<const T*>(&y[j]);
               T* oe = reinterpret_cast<T*>(&out);
 #pragma unroll
               for (int i = 0; i < EV; ++i) {
                 const float d = to_f32(ge[i]);
                 dot[j] = fmaf(to_f32(ye[i]), d, dot[j]);
-                oe[i] = from_f32<T>(w * d);
+                oe[i] = from_f32<T>(w[j] * d);
               }
             }
             static_cast<U*>(a.out_rows)[(int64_t)(row[j] >= 0 ? row[j] : ~row[j]) * m.vecs + v] = out;
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs 
     if ((int)threadIdx.x < top_k && (int)threadIdx.x / kSlotGroup % gridDim.y == blockIdx.y) {
       float d = 0.0f;
       for (int i = 0; i < (int)blockDim.x / 32; ++i) d += part[threadIdx.x][i];
-      a.dweights[(int64_t)t * top_k + threadIdx.x] = __ldg(rows + threadIdx.x) >= 0 ? d : 0.0f;
+      a.dweights[(int64_t)t * top_k + threadIdx.x] = rows[threadIdx.x] >= 0 ? d : 0.0f;
     }
     __syncthreads();
   }

@@ -30,13 +30,16 @@ struct alignas(16) Raw8 {
   T e[8];
 };
 
-// VEC: the address is 16-byte aligned.
+// VEC: the address is 16-byte aligned. Plain loads here and in the kernels that
+// read what another kernel wrote: these kernels start before the one before
+// them has ended (griddepcontrol.wait), so what it writes is not constant for
+// their lifetime, as the non-coherent loads of __ldg demand.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_raw8(const T* __restrict__ p, Raw8<T>& r) {
+__device__ __forceinline__ void load_raw8(const T* p, Raw8<T>& r) {
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(r) / 16; ++i) {
-      reinterpret_cast<uint4*>(r.e)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      reinterpret_cast<uint4*>(r.e)[i] = reinterpret_cast<const uint4*>(p)[i];
     }
   } else {
 #pragma unroll
@@ -52,7 +55,7 @@ __device__ __forceinline__ void clear_raw8(Raw8<T>& r) {
 
 // Eight consecutive elements as fp32.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* __restrict__ p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
   Raw8<T> r;
   load_raw8<T, VEC>(p, r);
 #pragma unroll
@@ -60,7 +63,7 @@ __device__ __forceinline__ void load8(const T* __restrict__ p, float (&v)[8]) {
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* __restrict__ p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   if constexpr (!VEC) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = from_f32<T>(v[i]);
