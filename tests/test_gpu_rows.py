@@ -273,7 +273,8 @@ def test_product_scale_range(fmt):
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("counts", [[1], [0, 3, 0], [128, 0, 129, 1], [5, 300, 2, 0, 0, 77, 128], [0, 0], [1] * 40,
-                                    [300, 0, 513, 129], [256, 1, 1000], [700]])
+                                    [300, 0, 513, 129], [256, 1, 1000], [700],
+                                    [33, 64, 65, 97, 31], [320, 449, 257, 193]])
 def test_grouped_product(fmt, counts):
     """Rows of each expert by its own matrix; rows of no expert stay as they are."""
     E, N, K, tail = len(counts), 200, 1184, 5
@@ -291,6 +292,111 @@ def test_grouped_product(fmt, counts):
         a, b = offsets[e], offsets[e + 1]
         want[a:b] = xv[a:b] @ ref.decode(wc[e], ws[e], fmt).T
     assert np.array_equal(host(y), want) and status_clean()
+
+
+@pytest.mark.parametrize("counts", [[140, 3, 0, 33], [300, 290, 5, 600]])
+def test_grouped_product_keeps_rows_apart(counts):
+    """E4M3 rows of NaN codes, and rows with NaN scales, leave the rows after them alone, in their own tile and in later ones."""
+    E, N, K, rows = len(counts), 136, 416, sum(counts)
+    g = qi.rng(8)
+    wc, ws = exact_inputs(g, "mxfp8", (E, N, K))
+    xc, xs = exact_inputs(g, "mxfp8", (rows, K))
+    bad = np.zeros(rows, dtype=bool)
+    bad[:counts[0]:2] = True
+    bad[-counts[-1]:-counts[-1] + 7] = True
+    xc[bad], xs[:counts[0]:6] = 0x7f, 255
+    desc, w = packed_weights("mxfp8", wc, ws)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    y = torch.full((rows, N), 7.0, dtype=torch.float32, device=DEV)
+    qmv.qmv_mx_product(desc, w, dev(ref.act_buffer(xc, xs, "mxfp8")), rows, dev(offsets), "f32", y)
+    got = host(y)
+    assert np.isnan(got[bad]).all()
+    xv = ref.decode(np.where(bad[:, None], 0, xc), np.where(bad[:, None], 0, xs), "mxfp8")
+    for e in range(E):
+        at = np.arange(offsets[e], offsets[e + 1])
+        at = at[~bad[at]]
+        assert np.array_equal(got[at], xv[at] @ ref.decode(wc[e], ws[e], "mxfp8").T), e
+
+
+def test_grouped_product_of_many_experts():
+    """The most experts that a call takes, most of them with no row or one."""
+    E, N, K = qmv.MAX_SORT_EXPERTS, 24, 96
+    g = qi.rng(12)
+    counts = g.integers(0, 3, size=E)
+    counts[17], counts[E - 1] = 150, 40
+    rows = int(counts.sum())
+    wc, ws = exact_inputs(g, "mxfp4", (E, N, K))
+    xc, xs = exact_inputs(g, "mxfp4", (rows, K))
+    desc, w = packed_weights("mxfp4", wc, ws)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    y = torch.empty(rows, N, dtype=torch.float32, device=DEV)
+    qmv.qmv_mx_product(desc, w, dev(ref.act_buffer(xc, xs, "mxfp4")), rows, dev(offsets), "f32", y)
+    expert = np.repeat(np.arange(E), counts)
+    want = np.einsum("rk,rnk->rn", ref.decode(xc, xs, "mxfp4"), ref.decode(wc, ws, "mxfp4")[expert])
+    assert np.array_equal(host(y), want) and status_clean()
+
+
+@pytest.mark.parametrize("offsets", [[0, 5, 3, 9], [-7, 4, 4, 1000], [6, 6, 6, 6], [20, 30, 40, 50]])
+def test_grouped_product_takes_offsets_into_its_rows(offsets):
+    """Offsets that do not ascend or name rows that are not there: each expert's range is taken into [0, nrows], and what a
+    descending pair names is nothing."""
+    rows, E, N, K = 9, 3, 40, 64
+    g = qi.rng(4)
+    wc, ws = exact_inputs(g, "mxfp4", (E, N, K))
+    xc, xs = exact_inputs(g, "mxfp4", (rows, K))
+    desc, w = packed_weights("mxfp4", wc, ws)
+    y = torch.full((rows + 2, N), 7.0, dtype=torch.float32, device=DEV)
+    qmv.qmv_mx_product(desc, w, dev(ref.act_buffer(xc, xs, "mxfp4")), rows, dev(np.array(offsets, dtype=np.int32)), "f32", y)
+    torch.cuda.synchronize()
+    assert (y[rows:] == 7.0).all() and status_clean()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_product_longest_k(fmt):
+    """K at its limit: 256 or 512 steps a tile; entries of one magnitude, so that every partial sum is exact."""
+    rows, N, K = 5, 24, 65536
+    g = qi.rng(6)
+    one = 2 if fmt == "mxfp4" else 0x38           # 1.0
+    sign = 8 if fmt == "mxfp4" else 0x80
+    wc = (one + sign * g.integers(0, 2, size=(1, N, K))).astype(np.uint8)
+    xc = (one + sign * g.integers(0, 2, size=(rows, K))).astype(np.uint8)
+    ws, xs = g.integers(126, 129, size=(1, N, K // 32), dtype=np.uint8), np.full((rows, K // 32), 127, dtype=np.uint8)
+    desc, w = packed_weights(fmt, wc, ws)
+    y = torch.empty(rows, N, dtype=torch.float32, device=DEV)
+    qmv.qmv_mx_product(desc, w, dev(ref.act_buffer(xc, xs, fmt)), rows, None, "f32", y)
+    assert np.array_equal(host(y), ref.decode(xc, xs, fmt) @ ref.decode(wc[0], ws[0], fmt).T)
+
+
+def test_rows_past_32_bits():
+    """Rows whose elements and bytes lie past 2^32 in every buffer: norm, quantization, product, dispatch and return."""
+    rows, K, N = 70000, 65536, 40
+    last = slice(rows - 3, rows)
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[last] = dev(randn(1, 3, K), "bf16")
+    xv = host(x[last])
+    y = torch.empty_like(x)
+    qmv.qmv_rms_norm("bf16", x, K, None, 0, torch.ones(K, dtype=torch.bfloat16, device=DEV), rows, K, 1e-5, None, "plain", y)
+    want = xv / np.sqrt((xv ** 2).mean(-1, keepdims=True) + 1e-5)
+    assert_within(host(y[last]), want, 1e-5 * np.abs(want), "bf16", "norm")
+    xq = buf(qmv.qmv_act_mx_bytes("mxfp8", rows, K))
+    qmv.qmv_quantize_act_mx("mxfp8", "bf16", x, K, rows, K, xq)
+    codes, scales = ref.quantize(xv, "mxfp8")
+    assert np.array_equal(xq[(rows - 3) * K:rows * K].view(3, K).cpu().numpy(), codes)
+    g = qi.rng(2)
+    wc, ws = exact_inputs(g, "mxfp8", (1, N, K))
+    desc, w = packed_weights("mxfp8", wc, ws)
+    out = torch.empty(rows, N, dtype=torch.float32, device=DEV)
+    qmv.qmv_mx_product(desc, w, xq, rows, None, "f32", out)
+    v, wv = ref.decode(codes, scales, "mxfp8"), ref.decode(wc[0], ws[0], "mxfp8")
+    assert_close(host(out[last]), v @ wv.T, np.abs(v) @ np.abs(wv).T, "f32", "product")
+    assert not out[:rows - 3].any()
+    del xq
+    row = torch.arange(rows - 1, -1, -1, dtype=torch.int32, device=DEV)   # one slot a token, in reverse
+    qmv.qmv_moe_dispatch("bf16", x, K, rows, 1, K, row, y)
+    assert torch.equal(y[:3], x[last].flip(0)) and not y[3:].any()
+    back = torch.empty_like(x)
+    qmv.qmv_moe_return("bf16", y, torch.full((rows, 1), 2.0, device=DEV), rows, 1, K, row, back, K)
+    assert torch.equal(back[last], 2 * x[last]) and not back[:rows - 3].any()
 
 
 @pytest.mark.parametrize("fmt,h_fmt", [("mxfp4", "mxfp4"), ("mxfp4", "mxfp8"), ("mxfp8", "mxfp4"), ("mxfp8", "mxfp8")])
