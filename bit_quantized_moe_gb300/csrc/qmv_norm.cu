@@ -306,6 +306,7 @@ quantize_mx_kernel(QuantArgs a) {
         if (j0 + j < copies) {
           const bool keep = r[j] >= 0;
           const int row = keep ? r[j] : ~r[j];
+          if (row >= a.nrows) continue;   // no row of this call
 #pragma unroll
           for (int i = 0; i < kWords / 4; ++i) {
             if (FMT == MXFP8 ? c0 + 32 * i < a.K : in) {

@@ -14,7 +14,7 @@ namespace qmv {
 
 // ---------------------------------------------------------------------------
 // Stable counting sort of slots by expert, in one launch of one cluster of up
-// to 16 CTAs (65,536 slots of 256 experts: 12.4 us, 8 CTAs 17.9).
+// to 16 CTAs (65,536 slots of 256 experts: 11.8 us, 8 CTAs 17.5).
 //
 // Every CTA of the cluster takes a contiguous range of slots, every warp of it
 // a contiguous part. A warp counts its slots per expert 32 at a time: lanes
@@ -238,8 +238,14 @@ struct Bytes<4> { using type = uint32_t; };
 template <>
 struct Bytes<2> { using type = uint16_t; };
 
-// Slot values beyond the call's top_k are never used.
 constexpr int kTopK = QMV_MAX_TOPK;
+
+// The row that row_of_slot names (r, or ~r of a dropped slot) if the call has
+// it; -1 otherwise: such an entry is neither read from nor written to.
+__device__ __forceinline__ int row_named(int r, int nslots) {
+  const int row = r >= 0 ? r : ~r;
+  return row < nslots ? row : -1;
+}
 
 // Slots of a token whose rows are asked for together.
 constexpr int kSlotGroup = 4;
@@ -248,10 +254,12 @@ static_assert(kTopK % kSlotGroup == 0, "part[] of the gradient");
 constexpr int kMoveThreads = 384;   // most threads of a mover's CTA
 
 // Arguments of the movers beside RouteArgs: accesses of a row, and between
-// rows of the token-major side; tokens of one pass of the grid.
+// rows of the token-major side; tokens of one pass of the grid; the call's rows
+// (as a parameter: a register for it makes return_kernel spill).
 struct MoveShape {
   int vecs;
   int tokens;
+  int nslots;
   int64_t ld;
 };
 
@@ -271,9 +279,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) dispatch_kernel(RouteArgs a, 
         for (int j = 0; j < kSlotGroup; ++j) row[j] = j0 + j < top_k ? rows[j0 + j] : 0;
 #pragma unroll
         for (int j = 0; j < kSlotGroup; ++j) {
-          if (j0 + j < top_k) {
-            const int r = row[j];
-            static_cast<U*>(a.out_rows)[(int64_t)(r >= 0 ? r : ~r) * m.vecs + v] = r >= 0 ? x : U{};
+          const int at = row_named(row[j], m.nslots);
+          if (j0 + j < top_k && at >= 0) {
+            static_cast<U*>(a.out_rows)[(int64_t)at * m.vecs + v] = row[j] >= 0 ? x : U{};
           }
         }
       }
@@ -318,7 +326,7 @@ return_kernel(RouteArgs a, MoveShape m) {
 #pragma unroll
         for (int j = 0; j < kSlotGroup; ++j) {
           const int r = j0 + j < top_k ? rows[j0 + j] : -1;
-          if (r >= 0) {
+          if ((unsigned)r < (unsigned)m.nslots) {   // a row of this call, not dropped
             x[j].load(a.rows, (int64_t)r * m.vecs + v);
             live |= 1u << j;
           }
@@ -343,8 +351,8 @@ return_kernel(RouteArgs a, MoveShape m) {
 }
 
 // dys[row] = w dy[t] and dw = <ys[row], dy[t]>: one CTA per token (or, of few
-// tokens, per token and group of slots), its slots in groups, each thread's part of a group's dot products reduced over the CTA in
-// a fixed order. A dropped slot's row of dys and its weight's gradient are 0.
+// tokens, per token and group of slots), its slots in groups, each thread's
+// part of a group's dot products reduced over the CTA in a fixed order. A dropped slot's row of dys and its weight's gradient are 0.
 template <typename T, int VB>
 __global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs a, MoveShape m) {
   using U = typename Bytes<VB>::type;
@@ -371,12 +379,14 @@ __global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs 
         for (int j = 0; j < kSlotGroup; ++j) {
           row[j] = j0 + j < top_k ? rows[j0 + j] : -1;
           w[j] = j0 + j < top_k ? weights[j0 + j] : 0.0f;
+          if (row[j] >= m.nslots) row[j] = ~m.nslots;   // no row of this call
           if (row[j] >= 0) y[j] = static_cast<const U*>(a.rows)[(int64_t)row[j] * m.vecs + v];
         }
         const T* ge = reinterpret_cast<const T*>(&g);
 #pragma unroll
         for (int j = 0; j < kSlotGroup; ++j) {
-          if (j0 + j < top_k) {
+          const int at = row_named(row[j], m.nslots);
+          if (j0 + j < top_k && at >= 0) {
             U out{};
             if (row[j] >= 0) {
               const T* ye = reinterpret_cast<const T*>(&y[j]);
@@ -388,7 +398,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs 
                 oe[i] = from_f32<T>(w[j] * d);
               }
             }
-            static_cast<U*>(a.out_rows)[(int64_t)(row[j] >= 0 ? row[j] : ~row[j]) * m.vecs + v] = out;
+            static_cast<U*>(a.out_rows)[(int64_t)at * m.vecs + v] = out;
           }
         }
       }
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) return_grad_kernel(RouteArgs 
     if ((int)threadIdx.x < top_k && (int)threadIdx.x / kSlotGroup % gridDim.y == blockIdx.y) {
       float d = 0.0f;
       for (int i = 0; i < (int)blockDim.x / 32; ++i) d += part[threadIdx.x][i];
-      a.dweights[(int64_t)t * top_k + threadIdx.x] = rows[threadIdx.x] >= 0 ? d : 0.0f;
+      a.dweights[(int64_t)t * top_k + threadIdx.x] = (unsigned)rows[threadIdx.x] < (unsigned)m.nslots ? d : 0.0f;
     }
     __syncthreads();
   }
@@ -419,9 +429,11 @@ struct RowShape {
 };
 
 // Accesses as wide as the row's bytes and stride allow; a CTA's threads cover
-// a row in as few, evenly filled rounds as kMoveThreads threads need. Where that makes
-// fewer CTAs than SMs, a row's columns (or, for one_token, its slots) are
-// spread over several (16 tokens x 8 slots of 7168: return 4.8 -> 3.2 us).
+// a row in as few, evenly filled rounds as kMoveThreads threads need. Where
+// that makes fewer CTAs than SMs, a row's columns (or, for one_token, its
+// slots) are spread over several (16 tokens x 8 slots of 7168, one CTA a token
+// against several: dispatch 3.4 and 1.7 us, return 5.5 and 2.3, its gradients
+// 6.2 and 4.0).
 RowShape row_shape(const RouteArgs& a, int64_t ld_elems, bool one_token) {
   const int size = a.type == QMV_F32 ? 4 : 2;
   const int64_t bytes = (int64_t)a.K * size, stride = ld_elems * size;
@@ -444,7 +456,7 @@ RowShape row_shape(const RouteArgs& a, int64_t ld_elems, bool one_token) {
   if (grid > (1 << 20)) grid = 1 << 20;
   s.block = dim3((unsigned)x, (unsigned)y);
   s.grid = dim3((unsigned)grid, (unsigned)split);
-  s.move = {(int)vecs, (int)(grid * y), stride / s.vb};
+  s.move = {(int)vecs, (int)(grid * y), (int)(a.ntok * a.top_k), stride / s.vb};
   return s;
 }
 

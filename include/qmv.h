@@ -518,6 +518,7 @@ int qmv_mx_gate_up_swiglu(const qmv_wdesc* desc, const void* w_gate_up_dev, cons
  *       the number of slots that are not dropped
  *   row_of_slot [ntok * top_k]: the slot's row; ~row (negative) for a dropped
  *       slot, whose row the calls below write as zeros and read as nothing
+ *       (they neither read nor write a row that is not one of the call's)
  *   slot_of_row [ntok * top_k]: the inverse
  * workspace: qmv_moe_sort_workspace_bytes(...) bytes of device scratch, which
  * may be 0 (workspace_dev may then be NULL). One launch; the same result every run.

@@ -514,6 +514,33 @@ def test_dispatch_and_return(dtype, extra, ntok, top_k, E, K, drop):
     assert not got[~valid].any()
 
 
+@pytest.mark.parametrize("K", [64, 9])
+def test_rows_that_the_call_does_not_have(K):
+    """Entries of row_of_slot past the call's rows are neither written to nor read from; the others do their work."""
+    ntok, top_k = 3, 2
+    n = ntok * top_k
+    row = dev(np.array([0, 6, ~7, 2, 1000000, ~3], dtype=np.int32))
+    x = dev(randn(1, ntok, K), "f32")
+    xs = torch.full((n + 2, K), 7.0, dtype=torch.float32, device=DEV)
+    qmv.qmv_moe_dispatch("f32", x, K, ntok, top_k, K, row, xs)
+    want = torch.full_like(xs, 7.0)
+    want[0], want[2], want[3] = x[0], x[1], 0
+    assert torch.equal(xs, want)
+    ys, w, dy = dev(randn(2, n + 2, K), "f32"), torch.ones(ntok, top_k, device=DEV), dev(randn(3, ntok, K), "f32")
+    y, dys, dw = torch.empty(ntok, K, device=DEV), torch.full_like(xs, 7.0), torch.empty(ntok, top_k, device=DEV)
+    qmv.qmv_moe_return("f32", ys, w, ntok, top_k, K, row, y, K)
+    assert torch.equal(y, torch.stack([ys[0], ys[2], torch.zeros_like(ys[0])]))
+    qmv.qmv_moe_return_grad("f32", dy, K, ys, w, ntok, top_k, K, row, dys, dw)
+    want = torch.full_like(xs, 7.0)
+    want[0], want[2], want[3] = dy[0], dy[1], 0
+    assert torch.equal(dys, want) and (dw.flatten()[[1, 2, 4, 5]] == 0).all() and (dw.flatten()[[0, 3]] != 0).all()
+    if K % 32 == 0:
+        size = qmv.qmv_act_mx_bytes("mxfp8", n, K)
+        xq = torch.full((size + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+        qmv.qmv_moe_dispatch_mx("mxfp8", "f32", x, K, ntok, top_k, K, row, xq)
+        assert (xq[size:] == 0xA5).all() and (xq[K:2 * K] == 0xA5).all() and not xq[3 * K:4 * K].any()
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("dtype,ntok,top_k,E,K,drop", [("bf16", 1, 1, 2, 32, 0), ("f16", 33, 4, 8, 2880, 0.2), ("f32", 9, 8, 16, 96, 0.1),
                                                        ("bf16", 300, 2, 4, 160, 0)])
