@@ -143,8 +143,8 @@ def _load() -> ctypes.CDLL:
         "qmv_act_mx_unpack": (ctypes.c_int, [I32, P, I32, I32, P, P]),
         "qmv_quantize_act_mx": (ctypes.c_int, [I32, I32, P, I64, I32, I32, P, SZ, P]),
         "qmv_rms_norm": (ctypes.c_int, [I32, P, I64, P, I64, P, I32, I32, ctypes.c_float, P, I32, P, SZ, P]),
-        "qmv_mx_product": (ctypes.c_int, [D, P, P, I32, P, I32, P, P]),
-        "qmv_mx_gate_up_swiglu": (ctypes.c_int, [D, P, P, I32, P, I32, P, SZ, P]),
+        "qmv_mx_product": (ctypes.c_int, [D, P, P, SZ, I32, P, I32, P, P]),
+        "qmv_mx_gate_up_swiglu": (ctypes.c_int, [D, P, P, SZ, I32, P, I32, P, SZ, P]),
         "qmv_moe_sort_workspace_bytes": (SZ, [I32, I32, I32]),
         "qmv_moe_sort": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P, SZ, P]),
         "qmv_moe_dispatch": (ctypes.c_int, [I32, P, I64, I32, I32, I32, P, P, P]),
@@ -412,13 +412,13 @@ def qmv_rms_norm(dtype, x, ldx: int, residual, ldr: int, gain, nrows: int, K: in
 
 
 def qmv_mx_product(desc: WDesc, w, xq, nrows: int, offsets, dtype, y, stream=None) -> None:
-    _check(lib.qmv_mx_product(ctypes.byref(desc), _ptr(w), _ptr(xq), nrows, _ptr(offsets), _type(dtype), _ptr(y),
-                              _stream(stream)))
+    _check(lib.qmv_mx_product(ctypes.byref(desc), _ptr(w), _ptr(xq), _nbytes(xq), nrows, _ptr(offsets), _type(dtype),
+                              _ptr(y), _stream(stream)))
 
 
 def qmv_mx_gate_up_swiglu(desc: WDesc, w_gate_up, xq, nrows: int, offsets, h_fmt, hq, stream=None) -> None:
-    _check(lib.qmv_mx_gate_up_swiglu(ctypes.byref(desc), _ptr(w_gate_up), _ptr(xq), nrows, _ptr(offsets), _fmt(h_fmt),
-                                     _ptr(hq), _nbytes(hq), _stream(stream)))
+    _check(lib.qmv_mx_gate_up_swiglu(ctypes.byref(desc), _ptr(w_gate_up), _ptr(xq), _nbytes(xq), nrows, _ptr(offsets),
+                                     _fmt(h_fmt), _ptr(hq), _nbytes(hq), _stream(stream)))
 
 
 def qmv_moe_sort_workspace_bytes(ntok: int, top_k: int, n_experts: int) -> int:

@@ -46,7 +46,7 @@ namespace qmv {
 
 constexpr int kTileM = 128;        // rows of activations of one CTA
 constexpr int kGemmThreads = 640;
-constexpr int kScaleWarps = 9;      // warps 3 and 12..19 (six: 8192 x 7168 x 7168 MXFP4 152 us, ten: 143)
+constexpr int kScaleWarps = 9;      // warps 3 and 12..19 (8192 x 7168 x 7168 MXFP4: six 152 us, nine 141, ten 143)
 // Columns of 16-bit outputs that a thread parks in shared memory before its
 // warp stores them row by row, and the pitch of a row there (an odd number of
 // 16 bytes: no bank conflicts between rows).

@@ -75,8 +75,8 @@ int check_slots(int ntok, int top_k, const char* name) {
   } while (0)
 
 // Common checks of the two products; fills `g`.
-int product_args(const qmv_wdesc* desc, const void* w, const void* xq, int nrows, const int32_t* offsets, const void* y,
-                 void* stream, const char* name, MxGemmArgs& g) {
+int product_args(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_bytes, int nrows, const int32_t* offsets,
+                 const void* y, void* stream, const char* name, MxGemmArgs& g) {
   QMV_TRY(check_weight_desc(desc));
   if (!fmt_is_mx(desc->fmt)) return record_error(QMV_EINVAL, "%s: MX formats only (got format %d)", name, desc->fmt);
   QMV_TRY(check_rows(nrows, name));
@@ -86,6 +86,8 @@ int product_args(const qmv_wdesc* desc, const void* w, const void* xq, int nrows
     return record_error(QMV_EINVAL, "%s: %d experts > %d", name, desc->n_experts, QMV_MAX_SORT_EXPERTS);
   if (any_null(w, xq, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(w, xq, y, offsets)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
+  const size_t need = mx_act_bytes(desc->fmt, nrows, desc->K);
+  if (xq_bytes < need) return record_error(QMV_ESIZE, "%s: activations %zu bytes < %zu", name, xq_bytes, need);
   g = MxGemmArgs();
   g.fmt = desc->fmt;
   g.N = desc->N;
@@ -278,22 +280,22 @@ int qmv_rms_norm(int32_t type, const void* x, int64_t ldx, const void* res, int6
   return launched(launch_rms_norm(a), name);
 }
 
-int qmv_mx_product(const qmv_wdesc* desc, const void* w, const void* xq, int32_t nrows, const int32_t* offsets,
-                   int32_t out_type, void* y, void* stream) {
+int qmv_mx_product(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_bytes, int32_t nrows,
+                   const int32_t* offsets, int32_t out_type, void* y, void* stream) {
   const char* name = "qmv_mx_product";
   MxGemmArgs g;
   QMV_TRY(check_type(out_type, name));
-  QMV_TRY(product_args(desc, w, xq, nrows, offsets, y, stream, name, g));
+  QMV_TRY(product_args(desc, w, xq, xq_bytes, nrows, offsets, y, stream, name, g));
   if (nrows == 0) return done();
   g.out_type = out_type;
   return launched(launch_mx_gemm(g), name);
 }
 
-int qmv_mx_gate_up_swiglu(const qmv_wdesc* desc, const void* w, const void* xq, int32_t nrows, const int32_t* offsets,
-                          int32_t h_fmt, void* hq, size_t hq_bytes, void* stream) {
+int qmv_mx_gate_up_swiglu(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_bytes, int32_t nrows,
+                          const int32_t* offsets, int32_t h_fmt, void* hq, size_t hq_bytes, void* stream) {
   const char* name = "qmv_mx_gate_up_swiglu";
   MxGemmArgs g;
-  QMV_TRY(product_args(desc, w, xq, nrows, offsets, hq, stream, name, g));
+  QMV_TRY(product_args(desc, w, xq, xq_bytes, nrows, offsets, hq, stream, name, g));
   if (h_fmt != QMV_MXFP4 && h_fmt != QMV_MXFP8) return record_error(QMV_EINVAL, "%s: not an MX format: %d", name, h_fmt);
   if (desc->N > QMV_MAX_N / 2) return record_error(QMV_ESHAPE, "%s: N=%d too large for gate/up fusion", name, desc->N);
   QMV_TRY(check_width(desc->N, true, name));
@@ -446,10 +448,11 @@ int qmv_moe_prefill_layer(const qmv_wdesc* gu, const void* w_gu, const qmv_wdesc
   QMV_TRY(qmv_moe_sort(ids, ntok, top_k, gu->n_experts, offsets, row_of_slot, slot_of_row, nullptr, 0, stream));
   QMV_TRY(qmv_moe_dispatch_mx(gu->fmt, type, x, ldx, ntok, top_k, gu->K, row_of_slot, base + s.xq,
                               mx_act_bytes(gu->fmt, slots, gu->K), stream));
-  QMV_TRY(qmv_mx_gate_up_swiglu(gu, w_gu, base + s.xq, (int32_t)slots, offsets, down->fmt, base + s.hq,
-                                mx_act_bytes(down->fmt, slots, gu->N), stream));
+  QMV_TRY(qmv_mx_gate_up_swiglu(gu, w_gu, base + s.xq, mx_act_bytes(gu->fmt, slots, gu->K), (int32_t)slots, offsets,
+                                down->fmt, base + s.hq, mx_act_bytes(down->fmt, slots, gu->N), stream));
   const bool exact = rows_in_f32(slots, down->N);
-  QMV_TRY(qmv_mx_product(down, w_down, base + s.hq, (int32_t)slots, offsets, exact ? QMV_F32 : type, base + s.ys, stream));
+  QMV_TRY(qmv_mx_product(down, w_down, base + s.hq, mx_act_bytes(down->fmt, slots, gu->N), (int32_t)slots, offsets,
+                         exact ? QMV_F32 : type, base + s.ys, stream));
   return return_rows(type, base + s.ys, exact, weights, ntok, top_k, down->N, row_of_slot, y, down->N, stream, name);
 }
 

@@ -485,16 +485,16 @@ int qmv_rms_norm(int32_t type, const void* x_dev, int64_t ldx, const void* resid
  * Product of microscaled activations and weights on the tensor cores:
  *   y[r] = W . x[r],   products of codes and scales exact, sums in fp32.
  * desc: an MX format; w_dev the packed weights (qmv_pack_weights), xq_dev an
- * activation buffer of the same format, of nrows rows. y_dev: out_type
- * [nrows][N].
+ * activation buffer of the same format, of nrows rows (xq_bytes: its size).
+ * y_dev: out_type [nrows][N].
  * offsets_dev == NULL: a dense product (n_experts 1). Otherwise a product
  * grouped by expert: int32 [n_experts + 1], rows offsets[e] .. offsets[e + 1]
  * of x (as qmv_moe_sort orders them) are multiplied by expert e's matrix; rows
  * of no expert are not written. Offsets are read on the device; they must
  * ascend, and are taken into [0, nrows].
- * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ECUDA.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
  */
-int qmv_mx_product(const qmv_wdesc* desc, const void* w_dev, const void* xq_dev, int32_t nrows,
+int qmv_mx_product(const qmv_wdesc* desc, const void* w_dev, const void* xq_dev, size_t xq_bytes, int32_t nrows,
                    const int32_t* offsets_dev, int32_t out_type, void* y_dev, void* stream);
 
 /*
@@ -507,8 +507,9 @@ int qmv_mx_product(const qmv_wdesc* desc, const void* w_dev, const void* xq_dev,
  * offsets as qmv_mx_product.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
  */
-int qmv_mx_gate_up_swiglu(const qmv_wdesc* desc, const void* w_gate_up_dev, const void* xq_dev, int32_t nrows,
-                          const int32_t* offsets_dev, int32_t h_fmt, void* hq_dev, size_t hq_bytes, void* stream);
+int qmv_mx_gate_up_swiglu(const qmv_wdesc* desc, const void* w_gate_up_dev, const void* xq_dev, size_t xq_bytes,
+                          int32_t nrows, const int32_t* offsets_dev, int32_t h_fmt, void* hq_dev, size_t hq_bytes,
+                          void* stream);
 
 /*
  * Routed slots sorted by expert. Slot s = t * top_k + j goes to expert

@@ -72,12 +72,12 @@ RETURN_GRAD = dict(type=0, dy=P, ld=64, ys=P, weights=P, ntok=4, top_k=2, N=64, 
 
 
 def product(**over):
-    good = dict(desc=qmv.wdesc("mxfp4", 64, 64, 4), w=P, xq=P, nrows=3, offsets=P, out_type=0, y=P)
+    good = dict(desc=qmv.wdesc("mxfp4", 64, 64, 4), w=P, xq=P, xq_bytes=BIG, nrows=3, offsets=P, out_type=0, y=P)
     return _call("qmv_mx_product", good, **over)
 
 
 def gate_up(**over):
-    good = dict(desc=qmv.wdesc("mxfp4", 64, 64, 4), w=P, xq=P, nrows=3, offsets=P, h_fmt=0, hq=P, hq_bytes=BIG)
+    good = dict(desc=qmv.wdesc("mxfp4", 64, 64, 4), w=P, xq=P, xq_bytes=BIG, nrows=3, offsets=P, h_fmt=0, hq=P, hq_bytes=BIG)
     return _call("qmv_mx_gate_up_swiglu", good, **over)
 
 
@@ -122,6 +122,7 @@ def test_product_refusals():
     assert product(nrows=-1) == -1 and product(out_type=3) == -1
     assert product(w=None) == -1 and product(y=None) == -1
     assert product(xq=ODD) == -3 and product(offsets=ODD) == -3
+    assert product(xq_bytes=qmv.qmv_act_mx_bytes("mxfp4", 3, 64) - 1) == -4 and gate_up(xq_bytes=7) == -4
     assert product(nrows=0) == 0                                         # nothing to do, nothing enqueued
     assert gate_up(h_fmt=1) == -1 and gate_up(hq_bytes=5) == -4
     assert gate_up(desc=qmv.wdesc("mxfp4", 48, 64, 4)) == -2             # h in groups of 32
