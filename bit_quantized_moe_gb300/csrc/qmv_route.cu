@@ -14,7 +14,7 @@ namespace qmv {
 
 // ---------------------------------------------------------------------------
 // Stable counting sort of slots by expert, in one launch of one cluster of up
-// to 16 CTAs (65,536 slots of 256 experts: 11.8 us, 8 CTAs 17.5).
+// to 16 CTAs (65,536 slots of 256 experts: 11.7 us, 8 CTAs 17.2).
 //
 // Every CTA of the cluster takes a contiguous range of slots, every warp of it
 // a contiguous part. A warp counts its slots per expert 32 at a time: lanes
