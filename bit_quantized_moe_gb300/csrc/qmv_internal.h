@@ -129,6 +129,7 @@ struct RouteArgs {
   int64_t ld_tok = 0;
   const void* rows = nullptr;   // expert-major rows read (ys, dxs)
   bool rows_f32 = false;        // launch_return: rows are fp32 whatever `type`
+  const float* wide = nullptr;  // launch_return, fp16 rows: the values of the infinite ones; null: infinity
   const float* weights = nullptr;   // null: every weight is 1
   void* out_tok = nullptr;      // token-major rows written (y, dx)
   int64_t ld_out = 0;
@@ -151,6 +152,7 @@ struct MxGemmArgs {
   const int32_t* offsets = nullptr;   // [n_experts + 1] first row of each expert; null: every row, expert 0
   int out_n = 0;                // output columns
   int out_type = 0;             // qmv_type (plain outputs)
+  float* wide = nullptr;        // out_type fp16: [nrows][out_n], the sums that fp16 stores as infinity; null: none kept
   void* y = nullptr;            // [nrows][out_n], or the mx_act buffer of h (glu)
   bool glu = false;             // store silu(gate) * up, quantized to h_fmt
   int h_fmt = 0;

@@ -91,6 +91,7 @@ struct GemmParams {
   const uint32_t* x_scales;   // words [ceil(K / 128)][nrows]
   const int32_t* offsets;
   void* y;
+  float* wide;                // out_type fp16: null, or where sums that fp16 does not hold are kept
   uint32_t* h_scales;         // glu
   int64_t nrows;
   uint64_t expert_stride, rowtile;
@@ -716,6 +717,13 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         }
       };
       if constexpr (HFMT < 0) {
+        // 32 columns of this thread's row, where one of them rounds to an infinite fp16
+        const auto keep_wide = [&](const uint32_t (&v)[32], int n0) {
+          bool over = false;
+#pragma unroll
+          for (uint32_t e : v) over |= fabsf(__uint_as_float(e)) >= 65520.0f;
+          if (over && live && n0 < p.out_n) store_columns(p.wide + row * p.out_n + n0, v, p.out_n - n0, false);
+        };
         if (p.out_type != QMV_F32 && p.out_n % 8 == 0) {
           // rows of whole 16 bytes: a warp parks its 32 rows and stores them row by row
           uint8_t* out = static_cast<uint8_t*>(p.y) + ((int64_t)tile.row0 + quad * 32) * p.out_n * 2;
@@ -729,6 +737,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
               tmem_ld_wait(v);
               if (p.out_type == QMV_BF16) park_columns<__nv_bfloat16>(my_park + i * 2, v);
               else park_columns<__half>(my_park + i * 2, v);
+              if (p.wide != nullptr) keep_wide(v, tile.n * TN + c + i);
             }
             if (c + kParkCols == TN) release();
             __syncwarp();
@@ -752,6 +761,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             tmem_ld32(d + (uint32_t)c, v);
             tmem_ld_wait(v);
             const int n0 = tile.n * TN + c;
+            if (p.wide != nullptr) keep_wide(v, n0);
             if (live && n0 < p.out_n) {
               const int64_t at = row * p.out_n + n0;
               if (p.out_type == QMV_BF16) store_columns(static_cast<__nv_bfloat16*>(p.y) + at, v, p.out_n - n0, false);
@@ -866,6 +876,7 @@ cudaError_t go(const MxGemmArgs& a) {
   p.x_scales = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.xq) + mx_scale_offset(FMT, a.nrows, a.K));
   p.offsets = a.offsets;
   p.y = a.y;
+  p.wide = a.wide;
   if (HFMT >= 0) {
     p.h_scales = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + mx_scale_offset(a.h_fmt, a.nrows, a.out_n));
   }

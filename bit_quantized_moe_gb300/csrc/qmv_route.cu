@@ -2,6 +2,7 @@
 // slots, the copies between the tokens' and the experts' row order, the
 // weighted sum, and the gradients of both.
 #include <atomic>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -305,9 +306,10 @@ struct RowVec {
 
 // R: the element type of the experts' rows. SPLIT: blockIdx.y takes a part of
 // the columns. Without it the kernel fits 40 registers and four CTAs an SM
-// (8191 tokens x 4 slots of 2880: 41 us against 47).
-template <typename R, typename T, int VB, bool SPLIT>
-__global__ void __launch_bounds__(kMoveThreads, SPLIT || sizeof(R) > sizeof(T) ? 3 : 4)
+// (8191 tokens x 4 slots of 2880: 41 us against 47). WIDE: fp16 rows whose
+// infinite elements are read as a.wide has them.
+template <typename R, typename T, int VB, bool SPLIT, bool WIDE>
+__global__ void __launch_bounds__(kMoveThreads, SPLIT || WIDE || sizeof(R) > sizeof(T) ? 3 : 4)
 return_kernel(RouteArgs a, MoveShape m) {
   using U = typename Bytes<VB>::type;
   constexpr int EV = VB / (int)sizeof(T);
@@ -336,7 +338,13 @@ return_kernel(RouteArgs a, MoveShape m) {
           if (live >> j & 1u) {
             const float w = a.weights != nullptr ? a.weights[(int64_t)t * top_k + j0 + j] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < EV; ++i) acc[i] = fmaf(w, x[j][i], acc[i]);
+            for (int i = 0; i < EV; ++i) {
+              float e = x[j][i];
+              if constexpr (WIDE) {
+                if (isinf(e)) e = a.wide[((int64_t)rows[j0 + j] * m.vecs + v) * EV + i];
+              }
+              acc[i] = fmaf(w, e, acc[i]);
+            }
           }
         }
       }
@@ -483,12 +491,18 @@ cudaError_t by_type(const RouteArgs& a, const RowShape& s) {
 
 template <typename R, typename T, int VB>
 cudaError_t go_return(const RouteArgs& a, const RowShape& s) {
-  return s.grid.y > 1 ? launch_pdl(return_kernel<R, T, VB, true>, s.grid, s.block, 0, a.stream, a, s.move)
-                      : launch_pdl(return_kernel<R, T, VB, false>, s.grid, s.block, 0, a.stream, a, s.move);
+  return s.grid.y > 1 ? launch_pdl(return_kernel<R, T, VB, true, false>, s.grid, s.block, 0, a.stream, a, s.move)
+                      : launch_pdl(return_kernel<R, T, VB, false, false>, s.grid, s.block, 0, a.stream, a, s.move);
 }
 template <typename T, int VB>
 struct Return {
   static cudaError_t go(const RouteArgs& a, const RowShape& s) {
+    if constexpr (std::is_same_v<T, __half>) {
+      if (a.wide != nullptr) {
+        return s.grid.y > 1 ? launch_pdl(return_kernel<T, T, VB, true, true>, s.grid, s.block, 0, a.stream, a, s.move)
+                            : launch_pdl(return_kernel<T, T, VB, false, true>, s.grid, s.block, 0, a.stream, a, s.move);
+      }
+    }
     return a.rows_f32 ? go_return<float, T, VB>(a, s) : go_return<T, T, VB>(a, s);
   }
 };

@@ -103,6 +103,17 @@ int product_args(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq
   return QMV_OK;
 }
 
+int mx_product(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_bytes, int nrows, const int32_t* offsets,
+               int out_type, float* wide, void* y, void* stream, const char* name) {
+  MxGemmArgs g;
+  QMV_TRY(check_type(out_type, name));
+  QMV_TRY(product_args(desc, w, xq, xq_bytes, nrows, offsets, y, stream, name, g));
+  if (nrows == 0) return done();
+  g.out_type = out_type;
+  g.wide = wide;
+  return launched(launch_mx_gemm(g), name);
+}
+
 int route_args(int type, int ntok, int top_k, int K, const int32_t* row_of_slot, void* stream, const char* name,
                RouteArgs& r) {
   QMV_TRY(check_type(type, name));
@@ -120,7 +131,7 @@ int route_args(int type, int ntok, int top_k, int K, const int32_t* row_of_slot,
   return QMV_OK;
 }
 
-int return_rows(int type, const void* ys, bool ys_f32, const float* weights, int ntok, int top_k, int N,
+int return_rows(int type, const void* ys, bool ys_f32, const float* wide, const float* weights, int ntok, int top_k, int N,
                 const int32_t* row_of_slot, void* y, int64_t ldy, void* stream, const char* name) {
   RouteArgs r;
   QMV_TRY(route_args(type, ntok, top_k, N, row_of_slot, stream, name, r));
@@ -130,6 +141,7 @@ int return_rows(int type, const void* ys, bool ys_f32, const float* weights, int
   if (ntok == 0) return done();
   r.rows = ys;
   r.rows_f32 = ys_f32 && type != QMV_F32;
+  r.wide = wide;
   r.weights = weights;
   r.out_tok = y;
   r.ld_out = ldy;
@@ -144,12 +156,15 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // rounded once: they stay in L2 then, and cost about nothing. Larger calls
 // keep them in the output's 16 bits, which doubles the rounding error's square
 // and halves 2 x 189 MB of traffic for 4096 tokens x 4 slots of 2880 columns.
+// A sum past fp16's 65,504 may come back into its range with its weight: large
+// fp16 calls keep such sums in fp32 beside the rows, where the weighted sum
+// looks for what it reads as infinity.
 constexpr size_t kExactRowsBytes = 32u << 20;
 bool rows_in_f32(int64_t slots, int N) { return (size_t)slots * N * 4 <= kExactRowsBytes; }
 
 // Parts of the layer's workspace.
 struct LayerSpace {
-  size_t offsets, row_of_slot, slot_of_row, xq, hq, ys, total;
+  size_t offsets, row_of_slot, slot_of_row, xq, hq, ys, wide, total;
 };
 
 LayerSpace layer_space(const qmv_wdesc* gu, const qmv_wdesc* down, int64_t slots) {
@@ -165,7 +180,9 @@ LayerSpace layer_space(const qmv_wdesc* gu, const qmv_wdesc* down, int64_t slots
   s.slot_of_row = take((size_t)slots * 4);
   s.xq = take(mx_act_bytes(gu->fmt, slots, gu->K));
   s.hq = take(mx_act_bytes(down->fmt, slots, gu->N));
-  s.ys = take((size_t)slots * down->N * (rows_in_f32(slots, down->N) ? 4 : 2));
+  const size_t outputs = (size_t)slots * down->N;
+  s.ys = take(outputs * (rows_in_f32(slots, down->N) ? 4 : 2));
+  s.wide = take(rows_in_f32(slots, down->N) ? 0 : outputs * 4);
   s.total = at;
   return s;
 }
@@ -282,13 +299,7 @@ int qmv_rms_norm(int32_t type, const void* x, int64_t ldx, const void* res, int6
 
 int qmv_mx_product(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_bytes, int32_t nrows,
                    const int32_t* offsets, int32_t out_type, void* y, void* stream) {
-  const char* name = "qmv_mx_product";
-  MxGemmArgs g;
-  QMV_TRY(check_type(out_type, name));
-  QMV_TRY(product_args(desc, w, xq, xq_bytes, nrows, offsets, y, stream, name, g));
-  if (nrows == 0) return done();
-  g.out_type = out_type;
-  return launched(launch_mx_gemm(g), name);
+  return mx_product(desc, w, xq, xq_bytes, nrows, offsets, out_type, nullptr, y, stream, "qmv_mx_product");
 }
 
 int qmv_mx_gate_up_swiglu(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_bytes, int32_t nrows,
@@ -398,7 +409,7 @@ int qmv_moe_dispatch_grad(int32_t type, const void* dxs, int32_t ntok, int32_t t
 
 int qmv_moe_return(int32_t type, const void* ys, const float* weights, int32_t ntok, int32_t top_k, int32_t N,
                    const int32_t* row_of_slot, void* y, int64_t ldy, void* stream) {
-  return return_rows(type, ys, false, weights, ntok, top_k, N, row_of_slot, y, ldy, stream, "qmv_moe_return");
+  return return_rows(type, ys, false, nullptr, weights, ntok, top_k, N, row_of_slot, y, ldy, stream, "qmv_moe_return");
 }
 
 int qmv_moe_return_grad(int32_t type, const void* dy, int64_t ld_dy, const void* ys, const float* weights,
@@ -451,9 +462,10 @@ int qmv_moe_prefill_layer(const qmv_wdesc* gu, const void* w_gu, const qmv_wdesc
   QMV_TRY(qmv_mx_gate_up_swiglu(gu, w_gu, base + s.xq, mx_act_bytes(gu->fmt, slots, gu->K), (int32_t)slots, offsets,
                                 down->fmt, base + s.hq, mx_act_bytes(down->fmt, slots, gu->N), stream));
   const bool exact = rows_in_f32(slots, down->N);
-  QMV_TRY(qmv_mx_product(down, w_down, base + s.hq, mx_act_bytes(down->fmt, slots, gu->N), (int32_t)slots, offsets,
-                         exact ? QMV_F32 : type, base + s.ys, stream));
-  return return_rows(type, base + s.ys, exact, weights, ntok, top_k, down->N, row_of_slot, y, down->N, stream, name);
+  float* wide = !exact && type == QMV_F16 ? reinterpret_cast<float*>(base + s.wide) : nullptr;
+  QMV_TRY(mx_product(down, w_down, base + s.hq, mx_act_bytes(down->fmt, slots, gu->N), (int32_t)slots, offsets,
+                     exact ? QMV_F32 : type, wide, base + s.ys, stream, name));
+  return return_rows(type, base + s.ys, exact, wide, weights, ntok, top_k, down->N, row_of_slot, y, down->N, stream, name);
 }
 
 }  // extern "C"

@@ -570,7 +570,7 @@ int qmv_moe_return_grad(int32_t type, const void* dy_dev, int64_t ld_dy, const v
  * Q the quantization to the projection's MX format; MXFP4 and MXFP8 may be
  * mixed as in qmv_moe_layer. The experts' rows stay in fp32 until they are
  * weighted and summed where they take at most 32 MB so; larger calls round them
- * to `type` first. Descriptors and packed weights as qmv_moe_layer; x
+ * to `type` first, but for fp16 sums past 65,504, which stay in fp32. Descriptors and packed weights as qmv_moe_layer; x
  * [ntok][K] of `type` (bf16 or fp16), rows ldx apart; y `type` [ntok][N_down].
  * Five launches. workspace: as qmv_moe_layer.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.

@@ -1,0 +1,40 @@
+"""The many-row operators where they can go wrong beyond ordinary inputs: numbers at the ends of their types' ranges,
+infinities and NaN, offsets that name nothing, the widest layer, host threads and streams at once. Definitions and
+tolerances are those of test_gpu_rows.py; what a test adds to them stands beside it."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+qmv = pytest.importorskip("bit_quantized_moe_gb300")
+import oracle  # noqa: E402
+import qmv_inputs as qi  # noqa: E402
+import rows_reference as ref  # noqa: E402
+from qmv_testutil import DEV, assert_within, status_clean  # noqa: E402
+from test_gpu_rows import (TORCH, buf, dev, drawn_ids, exact_inputs, host, layer_case, packed_weights, quantized_close,  # noqa: E402
+                           randn, sorted_on_gpu, split_layer, unpacked)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("ntok,N_down", [(1100, 4000), (1100, 4001), (140, 32000)])
+def test_layer_rows_past_f16_range_in_a_large_call(ntok, N_down):
+    """fp16 calls above 32 MB of fp32 rows: a row past 65,504 is weighted as the number it is, not as infinity."""
+    top_k, E, K, N = 2, 4, 96, 64
+    gu, w_gu, dn, w_dn, x, ids, weights, _ = layer_case("mxfp4", "mxfp4", "f16", ntok, top_k, E, K, N, N_down, 0.05)
+    assert ntok * top_k * N_down * 4 > 32 << 20
+    x *= 6000.0
+    weights = weights * 2.0 ** -9
+    ws = buf(qmv.qmv_moe_prefill_layer_workspace_bytes(gu, dn, ntok, top_k))
+    y = torch.full((ntok, N_down), 7.0, dtype=torch.float16, device=DEV)
+    qmv.qmv_moe_prefill_layer(gu, w_gu, dn, w_dn, "f16", x, K, dev(ids), weights, ntok, top_k, ws, y)
+    _, ys, row = split_layer(gu, w_gu, dn, w_dn, "f16", x, ids, weights, E, K, N, N_down, "f32")
+    r = row.cpu().numpy().reshape(ntok, top_k)
+    terms = np.where((r >= 0)[..., None], host(ys)[np.where(r >= 0, r, ~r)], 0) * host(weights)[..., None]
+    large = (ys.abs() > 65520).float().mean().item()
+    assert 1e-4 < large < 0.5 and torch.isfinite(ys).all() and np.abs(terms.sum(1)).max() < 60000, (large, np.abs(terms.sum(1)).max())
+    # a row's elements may be rounded to fp16 (11 bits, subnormal steps of 2^-24), then weighted and summed in fp32
+    bound = (2.0 ** -11 + (top_k + 1) * 2.0 ** -24) * np.abs(terms).sum(1) + 2.0 ** -25 * host(weights).sum(1)[:, None]
+    assert_within(host(y), terms.sum(1), bound, "f16", "layer")
+    assert status_clean()
