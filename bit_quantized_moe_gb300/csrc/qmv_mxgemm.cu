@@ -892,6 +892,14 @@ cudaError_t go(const MxGemmArgs& a) {
   p.out_type = a.out_type;
   p.n_tiles = (g.row_tiles * kRows + TN - 1) / TN;
 
+  const size_t smem =
+      1024 + (size_t)F::stages * F::stage_bytes + F::sf_stages * F::sf_bytes + F::park_bytes + 2 * ((size_t)a.n_experts + 1) * sizeof(int);
+  // Before the tensor maps: on a host thread whose first CUDA call this is, it
+  // makes the device's context current, which their encoding needs.
+  g_launch_stage = "cudaFuncSetAttribute";
+  cudaError_t e =
+      cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT, TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   g_launch_stage = "cuTensorMapEncodeTiled";
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
   CUtensorMap mx, mw, ml;
@@ -914,12 +922,6 @@ cudaError_t go(const MxGemmArgs& a) {
   if (p.chunks_full == 0) mw = ml;
   if (p.last_lanes == 0) ml = mw;
 
-  const size_t smem =
-      1024 + (size_t)F::stages * F::stage_bytes + F::sf_stages * F::sf_bytes + F::park_bytes + 2 * ((size_t)a.n_experts + 1) * sizeof(int);
-  g_launch_stage = "cudaFuncSetAttribute";
-  cudaError_t e =
-      cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT, TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   // no more CTAs than tiles there can be: every expert has at most one partial row tile
   constexpr int ctas = PAIR ? 2 : 1;
   const int64_t row_tiles = a.nrows / (ctas * kTileM) + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);

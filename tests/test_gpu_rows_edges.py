@@ -38,3 +38,38 @@ def test_layer_rows_past_f16_range_in_a_large_call(ntok, N_down):
     bound = (2.0 ** -11 + (top_k + 1) * 2.0 ** -24) * np.abs(terms).sum(1) + 2.0 ** -25 * host(weights).sum(1)[:, None]
     assert_within(host(y), terms.sum(1), bound, "f16", "layer")
     assert status_clean()
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_product_as_a_host_threads_first_call(glu):
+    """A thread that has made no CUDA call may begin with a product."""
+    N, K, rows = 32, 96, 5
+    g = qi.rng(1)
+    wc, ws = exact_inputs(g, "mxfp4", (1, N, K))
+    xc, xs = exact_inputs(g, "mxfp4", (rows, K))
+    desc, w = packed_weights("mxfp4", wc, ws)
+    if glu:
+        w = dev(qmv.qmv_pack_gate_up(desc, *[oracle.pack_codes("mxfp4", wc), ws] * 2))
+    xq, y = dev(ref.act_buffer(xc, xs, "mxfp4")), buf(max(rows * N * 4, qmv.qmv_act_mx_bytes("mxfp4", rows, N)))
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    errors = []
+
+    def run():
+        try:
+            if glu:
+                qmv.qmv_mx_gate_up_swiglu(desc, w, xq, rows, None, "mxfp4", y, stream)
+            else:
+                qmv.qmv_mx_product(desc, w, xq, rows, None, "f32", y, stream)
+        except qmv.QmvError as e:
+            errors.append(str(e))
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    if not glu:
+        want = ref.decode(xc, xs, "mxfp4") @ ref.decode(wc[0], ws[0], "mxfp4").T
+        assert np.array_equal(host(y[:rows * N * 4].view(torch.float32).view(rows, N)), want)
+    assert status_clean()
