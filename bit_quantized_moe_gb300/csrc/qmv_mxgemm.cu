@@ -84,6 +84,11 @@ struct GemmFmt {
   static constexpr int sf_slots = (int)((512 - sf_col0) / sf_cols) < stages ? (int)((512 - sf_col0) / sf_cols) : stages;
   static constexpr uint32_t tmem_cols = sf_col0 + sf_slots * sf_cols <= 256 ? 256 : 512;
   static_assert(sf_slots >= 4 && sf_col0 + sf_slots * sf_cols <= tmem_cols, "tensor memory");
+  // Dynamic shared memory: the rings from a 1024-byte boundary on, the parked columns, two tables of the experts.
+  static constexpr size_t smem_bytes(int n_experts) {
+    return 1024 + (size_t)stages * stage_bytes + sf_stages * sf_bytes + park_bytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
+  }
+  static_assert(smem_bytes(QMV_MAX_SORT_EXPERTS) + 1024 <= 227 * 1024, "shared memory, with 1 KB for the barriers");
 };
 
 struct GemmParams {
@@ -892,13 +897,14 @@ cudaError_t go(const MxGemmArgs& a) {
   p.out_type = a.out_type;
   p.n_tiles = (g.row_tiles * kRows + TN - 1) / TN;
 
-  const size_t smem =
-      1024 + (size_t)F::stages * F::stage_bytes + F::sf_stages * F::sf_bytes + F::park_bytes + 2 * ((size_t)a.n_experts + 1) * sizeof(int);
+  const size_t smem = F::smem_bytes(a.n_experts);
+  // The most that any call of this kernel asks for: the attribute is the
+  // function's, and another host thread may be between it and its launch.
   // Before the tensor maps: on a host thread whose first CUDA call this is, it
   // makes the device's context current, which their encoding needs.
   g_launch_stage = "cudaFuncSetAttribute";
-  cudaError_t e =
-      cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT, TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, HFMT, TN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)F::smem_bytes(QMV_MAX_SORT_EXPERTS));
   if (e != cudaSuccess) return e;
   g_launch_stage = "cuTensorMapEncodeTiled";
   if (encode_fn() == nullptr) return cudaErrorNotSupported;

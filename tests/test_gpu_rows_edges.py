@@ -73,3 +73,45 @@ def test_product_as_a_host_threads_first_call(glu):
         want = ref.decode(xc, xs, "mxfp4") @ ref.decode(wc[0], ws[0], "mxfp4").T
         assert np.array_equal(host(y[:rows * N * 4].view(torch.float32).view(rows, N)), want)
     assert status_clean()
+
+
+def test_products_from_two_host_threads():
+    """One kernel launched from two threads at once with the most experts and with few: each launch has the shared memory
+    that it asks for, whatever the other's size."""
+    N, K, rows, calls = 24, 96, 5, 4000
+    errors = []
+    sizes = [qmv.MAX_SORT_EXPERTS, 2]
+    work = []
+    for E in sizes:
+        g = qi.rng(E)
+        wc, ws = exact_inputs(g, "mxfp4", (E, N, K))
+        xc, xs = exact_inputs(g, "mxfp4", (rows, K))
+        desc, w = packed_weights("mxfp4", wc, ws)
+        offsets = np.full(E + 1, rows, dtype=np.int32)
+        offsets[0] = 0
+        want = ref.decode(xc, xs, "mxfp4") @ ref.decode(wc[0], ws[0], "mxfp4").T
+        work.append((desc, w, dev(ref.act_buffer(xc, xs, "mxfp4")), dev(offsets), want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [torch.zeros(rows, N, dtype=torch.float32, device=DEV) for _ in work]
+    torch.cuda.synchronize()
+
+    def run(i):
+        desc, w, xq, offsets, _, stream = work[i]
+        try:
+            for n in range(calls):
+                qmv.qmv_mx_product(desc, w, xq, rows, offsets, "f32", outs[i], stream)
+                if n % 200 == 199:
+                    stream.synchronize()
+        except qmv.QmvError as e:
+            errors.append((sizes[i], str(e)))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for out, w in zip(outs, work):
+        assert np.array_equal(host(out), w[4])
+    assert status_clean()
