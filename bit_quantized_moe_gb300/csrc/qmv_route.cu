@@ -448,7 +448,7 @@ RowShape row_shape(const RouteArgs& a, int64_t ld_elems, bool one_token) {
   RowShape s;
   s.vb = 16;
   while (s.vb > size && (bytes % s.vb != 0 || stride % s.vb != 0)) s.vb /= 2;
-  const int64_t vecs = bytes / s.vb;   // at most 2^17
+  const int64_t vecs = bytes / s.vb;   // at most 2^20: QMV_MAX_N elements
   const int64_t rounds = (vecs + kMoveThreads - 1) / kMoveThreads;
   int64_t x = ((vecs + rounds - 1) / rounds + 31) / 32 * 32;
   const int64_t y = one_token || x >= 256 ? 1 : 256 / x;

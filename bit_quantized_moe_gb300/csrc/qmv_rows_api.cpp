@@ -42,8 +42,8 @@ int check_type(int type, const char* name) {
   return QMV_OK;
 }
 
-int check_width(int K, bool groups, const char* name) {
-  if (K < 1 || K > QMV_MAX_K) return record_error(QMV_ESHAPE, "%s: %d columns outside [1, %d]", name, K, QMV_MAX_K);
+int check_width(int K, bool groups, const char* name, int most = QMV_MAX_K) {
+  if (K < 1 || K > most) return record_error(QMV_ESHAPE, "%s: %d columns outside [1, %d]", name, K, most);
   if (groups && K % 32) return record_error(QMV_ESHAPE, "%s: %d columns are not a multiple of 32", name, K);
   return QMV_OK;
 }
@@ -114,11 +114,12 @@ int mx_product(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_b
   return launched(launch_mx_gemm(g), name);
 }
 
-int route_args(int type, int ntok, int top_k, int K, const int32_t* row_of_slot, void* stream, const char* name,
+// most: columns that a row may have: QMV_MAX_K of a product's input, QMV_MAX_N of its output.
+int route_args(int type, int ntok, int top_k, int K, int most, const int32_t* row_of_slot, void* stream, const char* name,
                RouteArgs& r) {
   QMV_TRY(check_type(type, name));
   QMV_TRY(check_slots(ntok, top_k, name));
-  QMV_TRY(check_width(K, false, name));
+  QMV_TRY(check_width(K, false, name, most));
   if (row_of_slot == nullptr) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (misaligned(row_of_slot)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   r = RouteArgs();
@@ -134,7 +135,7 @@ int route_args(int type, int ntok, int top_k, int K, const int32_t* row_of_slot,
 int return_rows(int type, const void* ys, bool ys_f32, const float* wide, const float* weights, int ntok, int top_k, int N,
                 const int32_t* row_of_slot, void* y, int64_t ldy, void* stream, const char* name) {
   RouteArgs r;
-  QMV_TRY(route_args(type, ntok, top_k, N, row_of_slot, stream, name, r));
+  QMV_TRY(route_args(type, ntok, top_k, N, QMV_MAX_N, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ldy, N, name));
   if (any_null(ys, weights, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(ys, weights, y)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
@@ -348,7 +349,7 @@ int qmv_moe_dispatch(int32_t type, const void* x, int64_t ldx, int32_t ntok, int
                      const int32_t* row_of_slot, void* xs, void* stream) {
   const char* name = "qmv_moe_dispatch";
   RouteArgs r;
-  QMV_TRY(route_args(type, ntok, top_k, K, row_of_slot, stream, name, r));
+  QMV_TRY(route_args(type, ntok, top_k, K, QMV_MAX_K, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ldx, K, name));
   if (any_null(x, xs)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x, xs)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
@@ -365,7 +366,7 @@ int qmv_moe_dispatch_mx(int32_t fmt, int32_t type, const void* x, int64_t ldx, i
   const char* name = "qmv_moe_dispatch_mx";
   RouteArgs r;
   if (fmt != QMV_MXFP4 && fmt != QMV_MXFP8) return record_error(QMV_EINVAL, "%s: not an MX format: %d", name, fmt);
-  QMV_TRY(route_args(type, ntok, top_k, K, row_of_slot, stream, name, r));
+  QMV_TRY(route_args(type, ntok, top_k, K, QMV_MAX_K, row_of_slot, stream, name, r));
   QMV_TRY(check_width(K, true, name));
   QMV_TRY(check_ld(ldx, K, name));
   if (any_null(x, xq)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
@@ -395,7 +396,7 @@ int qmv_moe_dispatch_grad(int32_t type, const void* dxs, int32_t ntok, int32_t t
                           const int32_t* row_of_slot, void* dx, int64_t ldx, void* stream) {
   const char* name = "qmv_moe_dispatch_grad";
   RouteArgs r;
-  QMV_TRY(route_args(type, ntok, top_k, K, row_of_slot, stream, name, r));
+  QMV_TRY(route_args(type, ntok, top_k, K, QMV_MAX_K, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ldx, K, name));
   if (any_null(dxs, dx)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(dxs, dx)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
@@ -417,7 +418,7 @@ int qmv_moe_return_grad(int32_t type, const void* dy, int64_t ld_dy, const void*
                         void* stream) {
   const char* name = "qmv_moe_return_grad";
   RouteArgs r;
-  QMV_TRY(route_args(type, ntok, top_k, N, row_of_slot, stream, name, r));
+  QMV_TRY(route_args(type, ntok, top_k, N, QMV_MAX_N, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ld_dy, N, name));
   if (any_null(dy, ys, weights, dys, dweights)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(dy, ys, weights, dys, dweights))

@@ -553,7 +553,7 @@ int qmv_moe_dispatch_grad(int32_t type, const void* dxs_dev, int32_t ntok, int32
  *   qmv_moe_return_grad  dys[row_of_slot[t][j]] = weights[t][j] * dy[t],
  *                        dweights[t][j] = <ys[row_of_slot[t][j]], dy[t]>      (fp32; dy rows ld_dy apart)
  * over the slots that are not dropped; a dropped slot's row of dys and its
- * weight's gradient are zero.
+ * weight's gradient are zero. N up to QMV_MAX_N.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ECUDA.
  */
 int qmv_moe_return(int32_t type, const void* ys_dev, const float* weights_dev, int32_t ntok, int32_t top_k, int32_t N,

@@ -115,3 +115,40 @@ def test_products_from_two_host_threads():
     for out, w in zip(outs, work):
         assert np.array_equal(host(out), w[4])
     assert status_clean()
+
+
+@pytest.mark.parametrize("dtype,N", [("bf16", 65600), ("f16", 70001), ("bf16", 1 << 20)])
+def test_return_of_rows_past_65536_columns(dtype, N):
+    """The experts' rows are as wide as a weight matrix may be high."""
+    ntok, top_k, E = 3, 2, 4
+    _, row, _ = sorted_on_gpu(drawn_ids(1, ntok, top_k, E, 0.2), E)
+    r = row.cpu().numpy()
+    flat, valid = np.where(r >= 0, r, ~r), r >= 0
+    ys, weights, dy = dev(randn(2, ntok * top_k, N), dtype), dev(randn(3, ntok, top_k).astype(np.float32)), dev(randn(4, ntok, N), dtype)
+    y, dx = (torch.full((ntok, N), 7.0, dtype=TORCH[dtype], device=DEV) for _ in range(2))
+    qmv.qmv_moe_return(dtype, ys, weights, ntok, top_k, N, row, y, N)
+    terms = np.where(valid[:, None], host(ys)[flat], 0) * host(weights).reshape(-1, 1)
+    terms = terms.reshape(ntok, top_k, N)
+    assert_within(host(y), terms.sum(1), (top_k + 1) * 2.0 ** -24 * np.abs(terms).sum(1), dtype, "y")
+    dys, dw = torch.full_like(ys, 7.0), torch.empty(ntok, top_k, device=DEV)
+    qmv.qmv_moe_return_grad(dtype, dy, N, ys, weights, ntok, top_k, N, row, dys, dw)
+    d = np.repeat(host(dy), top_k, 0)
+    want = np.zeros((ntok * top_k, N))
+    want[flat] = np.where(valid[:, None], host(weights).reshape(-1, 1) * d, 0)
+    assert_within(host(dys), want, np.abs(want) * 2.0 ** -24, dtype, "dys")
+    prod = np.where(valid[:, None], host(ys)[flat], 0) * d
+    # a thread's sum (one of 384 at least), then a tree
+    assert (np.abs(host(dw).reshape(-1) - prod.sum(1)) <= (N / 32 + 16) * 2.0 ** -24 * np.abs(prod).sum(1)).all()
+
+
+def test_layer_past_65536_columns():
+    ntok, top_k, E, K, N, N_down = 3, 2, 2, 32, 32, 65600
+    gu, w_gu, dn, w_dn, x, ids, weights, _ = layer_case("mxfp4", "mxfp8", "bf16", ntok, top_k, E, K, N, N_down, 0.2)
+    ws = buf(qmv.qmv_moe_prefill_layer_workspace_bytes(gu, dn, ntok, top_k))
+    y = torch.full((ntok, N_down), 7.0, dtype=torch.bfloat16, device=DEV)
+    qmv.qmv_moe_prefill_layer(gu, w_gu, dn, w_dn, "bf16", x, K, dev(ids), weights, ntok, top_k, ws, y)
+    _, ys, row = split_layer(gu, w_gu, dn, w_dn, "bf16", x, ids, weights, E, K, N, N_down, "f32")
+    r = row.cpu().numpy().reshape(ntok, top_k)
+    terms = np.where((r >= 0)[..., None], host(ys)[np.where(r >= 0, r, ~r)], 0) * host(weights)[..., None]
+    assert_within(host(y), terms.sum(1), (top_k + 1) * 2.0 ** -24 * np.abs(terms).sum(1), "bf16", "layer")
+    assert status_clean()

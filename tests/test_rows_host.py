@@ -150,3 +150,13 @@ def test_no_rows_is_valid():
                        ("qmv_moe_dispatch_grad", DISPATCH_GRAD), ("qmv_moe_return", RETURN),
                        ("qmv_moe_return_grad", RETURN_GRAD)):
         assert _call(name, good, ntok=0) == 0
+
+
+def test_widths_of_the_routed_rows():
+    """Dispatched rows are a product's input (K), returned ones its output (N): each takes what the product takes."""
+    for name, good, ld in (("qmv_moe_return", RETURN, "ldy"), ("qmv_moe_return_grad", RETURN_GRAD, "ld")):
+        assert _call(name, good, ntok=0, N=1 << 20, **{ld: 1 << 20}) == 0
+        assert _call(name, good, ntok=0, N=(1 << 20) + 1, **{ld: 1 << 21}) == -2
+    for name, good in (("qmv_moe_dispatch", DISPATCH), ("qmv_moe_dispatch_grad", DISPATCH_GRAD)):
+        assert _call(name, good, ntok=0, K=65536, ldx=65536) == 0
+        assert _call(name, good, ntok=0, K=65537, ldx=65537) == -2
