@@ -1,5 +1,7 @@
 // qmv_norm.cu -- root-mean-square norm with the residual's addition and a
 // quantized output, and the microscaled quantizer of activation rows.
+#include <type_traits>
+
 #include "qmv_internal.h"
 #include "qmv_rows.cuh"
 
@@ -14,10 +16,23 @@ namespace qmv {
 // sum. Bound by memory: 2 + 2 bytes in, 2 + 1 + 1/32 out per element for bf16
 // and MXFP8.
 //
+// Squares of numbers past 2^64 or far below 1 leave fp32. Where the mean (with
+// eps) comes out outside [2^-100, infinity), the row's threads take the squares
+// again of numbers scaled by 2^-100 or 2^100.
+//
 // VEC: every row starts on a 16-byte boundary and the width is a multiple of
 // 8. Otherwise (plain output only needs no group of 32) a thread's elements
 // are TPR apart, so that a warp still reads consecutive ones.
 // ---------------------------------------------------------------------------
+constexpr float kMeanLow = 0x1p-100f, kUp = 0x1p100f, kDown = 0x1p-100f;
+
+// Barrier of a row's TPR threads: rows of a CTA may differ in how many they pass.
+template <int TPR, int THREADS>
+__device__ __forceinline__ void row_barrier() {
+  if constexpr (TPR == THREADS) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" :: "r"(1 + (int)threadIdx.x / TPR), "n"(TPR) : "memory");
+}
+
 template <typename T, int OUT, int TPR, int V, bool VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 rms_norm_kernel(NormArgs a) {
@@ -25,7 +40,7 @@ rms_norm_kernel(NormArgs a) {
   constexpr int kRowsPerCta = kThreads / TPR;
   constexpr int kWarps = TPR / 32;
   constexpr bool kCols = VEC || OUT != kNormPlain;   // a thread owns 8 consecutive columns
-  __shared__ float part[kThreads / 32];
+  __shared__ float part[2][kThreads / 32];
   const int tid = threadIdx.x % TPR;
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kRowsPerCta + threadIdx.x / TPR;
@@ -101,17 +116,48 @@ rms_norm_kernel(NormArgs a) {
       }
     }
   }
+  // the row's sum of its threads' parts, the same in all of them; the first is taken by all rows of the CTA together
+  const auto row_sum = [&](float v, auto first) {
+    constexpr int use = decltype(first)::value ? 0 : 1;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-  if constexpr (kWarps > 1) {
-    if (lane == 0) part[threadIdx.x / 32] = sq;
-    __syncthreads();
-    const int w0 = (threadIdx.x / TPR) * kWarps;
-    sq = lane < kWarps ? part[w0 + lane] : 0.0f;
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (kWarps > 1) {
+      if (lane == 0) part[use][threadIdx.x / 32] = v;
+      if constexpr (use == 0) __syncthreads();
+      else row_barrier<TPR, kThreads>();
+      const int w0 = (threadIdx.x / TPR) * kWarps;
+      v = lane < kWarps ? part[use][w0 + lane] : 0.0f;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
+  };
+  const float mean = row_sum(sq, std::true_type()) / (float)K + a.eps;
+  float rs = 1.0f / sqrtf(mean);
+  // fp16's squares stay in the range
+  if (!std::is_same_v<T, __half> && !(mean >= kMeanLow && mean <= 3.402823466e38f)) {   // the same in a row's threads
+    const bool small = mean < kMeanLow;
+    const float f = small ? kUp : kDown;
+    float again = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = s[j][i] * f;
+        again = fmaf(v, v, again);
+      }
+    }
+    rs = 1.0f / sqrtf(row_sum(again, std::false_type()) / (float)K + a.eps * f * f);
+    // Small numbers take the factor first, exactly. Large rows take it last: s * rs is then at most 2^100 sqrt(K),
+    // and the row's small numbers, which the factor would take below the normal ones, keep their places.
+    const float first = small ? f : rs;
+    rs = small ? rs : f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j][i] *= first;
+    }
   }
-  const float rs = 1.0f / sqrtf(sq / (float)K + a.eps);
 
 #pragma unroll
   for (int j = 0; j < V; ++j) {

@@ -473,7 +473,9 @@ int qmv_quantize_act_mx(int32_t fmt, int32_t type, const void* x_dev, int64_t ld
  *   QMV_NORM_MXFP8   an MXFP8 activation buffer (qmv_act_mx_bytes), K % 32 == 0
  *   QMV_NORM_MXFP4   an MXFP4 activation buffer
  *   QMV_NORM_Q8      q8_1 vectors as qmv_quantize_act_q8 makes of an fp32 y
- * The squares are summed in fp32 in an order that depends on K alone.
+ * The squares are summed in fp32, scaled where they would leave its range, in
+ * an order that depends on K, `out` and whether the rows' strides are multiples
+ * of 16 bytes.
  * Errors: QMV_EINVAL (also eps < 0 or NaN), QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
  */
 typedef enum { QMV_NORM_PLAIN = 0, QMV_NORM_MXFP8 = 1, QMV_NORM_MXFP4 = 2, QMV_NORM_Q8 = 3 } qmv_norm_out;

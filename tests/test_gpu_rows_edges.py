@@ -152,3 +152,49 @@ def test_layer_past_65536_columns():
     terms = np.where((r >= 0)[..., None], host(ys)[np.where(r >= 0, r, ~r)], 0) * host(weights)[..., None]
     assert_within(host(y), terms.sum(1), (top_k + 1) * 2.0 ** -24 * np.abs(terms).sum(1), "bf16", "layer")
     assert status_clean()
+
+
+def norm_case(dtype, values, eps, out, ld=None):
+    """(output, kept sum) of the norm of `values` without a residual, gain 1, rows `ld` apart."""
+    rows, K = values.shape
+    x = torch.zeros(rows, ld or K, dtype=TORCH[dtype], device=DEV)
+    x[:, :K] = dev(values, dtype)
+    fmt = out if out.startswith("mx") else None
+    size = {"plain": rows * K * x.element_size(), "q8": qmv.qmv_act_q8_bytes(rows, K)}.get(out) or qmv.qmv_act_mx_bytes(fmt, rows, K)
+    y = buf(size)
+    qmv.qmv_rms_norm(dtype, x, ld or K, None, 0, torch.ones(K, dtype=TORCH[dtype], device=DEV), rows, K, eps, None, out, y)
+    return host(x[:, :K]), y
+
+
+# Magnitudes whose squares leave fp32: above 2^64 and below 2^-64 (eps 0: with eps the smallest rows are ordinary).
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("out", ["plain", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("K,extra", [(32, 0), (256, 0), (544, 0), (2048, 0), (2880, 0), (2880, 3), (7168, 0), (8224, 1), (65536, 0)])
+def test_rms_norm_of_numbers_whose_squares_leave_the_range(dtype, out, K, extra):
+    size = np.array([2.0 ** 64, 1.0, 2.0 ** 121, 2.0 ** -64, 2.0 ** 100, 2.0 ** -100, 3.0, 2.0 ** -118, 2.0 ** 63])
+    s, y = norm_case(dtype, np.clip(randn(K, len(size), K), -60, 60) * size[:, None], 0.0, out, K + extra)
+    want = s / np.sqrt((s ** 2).mean(-1, keepdims=True))
+    err = 1e-5 * np.abs(want)
+    if out == "plain":
+        assert_within(host(y.view(TORCH[dtype]).view(s.shape)), want, err, dtype, "y")
+    else:
+        quantized_close(*unpacked(out, y, *s.shape), want, err, out)
+
+
+@pytest.mark.parametrize("dtype,K", [("bf16", 31), ("f32", 2881), ("bf16", 8191), ("f32", 1025)])
+def test_rms_norm_of_large_numbers_in_odd_widths(dtype, K):
+    size = np.array([1.0, 2.0 ** 100, 2.0 ** 70, 2.0 ** -90])
+    s, y = norm_case(dtype, np.clip(randn(K, len(size), K), -60, 60) * size[:, None], 0.0, "plain")
+    want = s / np.sqrt((s ** 2).mean(-1, keepdims=True))
+    assert_within(host(y.view(TORCH[dtype]).view(s.shape)), want, 1e-5 * np.abs(want), dtype, "y")
+
+
+def test_rms_norm_with_eps_of_numbers_whose_squares_leave_the_range():
+    """eps counts as it stands beside small rows and not beside large ones; a row of zeros without eps is 0 / 0."""
+    size = np.array([2.0 ** 100, 2.0 ** -20, 2.0 ** -70, 0.0])
+    for eps in (1e-5, 1e-30, 4.0, 3e38):
+        s, y = norm_case("f32", np.clip(randn(3, 4, 288), -60, 60) * size[:, None], eps, "plain")
+        want = s / np.sqrt((s ** 2).mean(-1, keepdims=True) + float(np.float32(eps)))
+        assert_within(host(y.view(torch.float32).view(s.shape)), want, 1e-5 * np.abs(want) + 2.0 ** -149, "f32", f"eps {eps}")
+    s, y = norm_case("f32", np.zeros((2, 288)), 0.0, "plain")
+    assert np.isnan(host(y.view(torch.float32))).all()
