@@ -484,20 +484,28 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
   pdl_wait();
   if (warp == 0) {
     constexpr int unit = kCtas * kTileM;
-    int tiles = 0;
+    int tiles = 0, reached = 0;   // before expert e0
     for (int e0 = 0; e0 < p.n_experts; e0 += 32) {
       const int e = e0 + lane;
-      int lo = 0, hi = 0;
+      // Offsets are taken into the call's rows, and none below the ones before it: every row has one expert at most,
+      // whatever the offsets are, and the tiles are as few as the rows allow.
+      int lo = reached, hi = reached;
       if (e < p.n_experts) {
-        lo = p.offsets != nullptr ? p.offsets[e] : 0;
-        hi = p.offsets != nullptr ? p.offsets[e + 1] : (int)p.nrows;
-        // offsets that do not name rows of this call name none
-        lo = max(0, min(lo, (int)p.nrows));
-        hi = max(lo, min(hi, (int)p.nrows));
+        lo = p.offsets != nullptr ? min(p.offsets[e], (int)p.nrows) : 0;
+        hi = p.offsets != nullptr ? min(p.offsets[e + 1], (int)p.nrows) : (int)p.nrows;
+      }
+      if (__any_sync(0xffffffffu, lo < reached || lo > hi)) {   // they do not ascend
+        lo = max(lo, reached);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) lo = max(lo, __shfl_up_sync(0xffffffffu, lo, o));   // its own below lane o
+        hi = max(lo, hi);
+      }
+      reached = __shfl_sync(0xffffffffu, hi, 31);
+      if (e < p.n_experts) {
         first_row[e] = lo;
         if (e == p.n_experts - 1) first_row[e + 1] = hi;
       }
-      int inc = (hi - lo + unit - 1) / unit * p.n_tiles;
+      int inc = e < p.n_experts ? (hi - lo + unit - 1) / unit * p.n_tiles : 0;
       const int own = inc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

@@ -493,7 +493,8 @@ int qmv_rms_norm(int32_t type, const void* x_dev, int64_t ldx, const void* resid
  * grouped by expert: int32 [n_experts + 1], rows offsets[e] .. offsets[e + 1]
  * of x (as qmv_moe_sort orders them) are multiplied by expert e's matrix; rows
  * of no expert are not written. Offsets are read on the device; they must
- * ascend, and are taken into [0, nrows].
+ * ascend, and are taken into [0, nrows]; one below an earlier one counts as it,
+ * so that no row has two experts.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
  */
 int qmv_mx_product(const qmv_wdesc* desc, const void* w_dev, const void* xq_dev, size_t xq_bytes, int32_t nrows,

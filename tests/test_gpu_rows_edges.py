@@ -198,3 +198,36 @@ def test_rms_norm_with_eps_of_numbers_whose_squares_leave_the_range():
         assert_within(host(y.view(torch.float32).view(s.shape)), want, 1e-5 * np.abs(want) + 2.0 ** -149, "f32", f"eps {eps}")
     s, y = norm_case("f32", np.zeros((2, 288)), 0.0, "plain")
     assert np.isnan(host(y.view(torch.float32))).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("offsets,ranges", [
+    ([0, 5, 3, 9], [(0, 5), (5, 5), (5, 9)]), ([-7, 4, 4, 1000], [(0, 4), (4, 4), (4, 9)]),
+    ([6, 6, 6, 6], [(6, 6)] * 3), ([20, 30, 40, 50], [(9, 9)] * 3), ([8, 2, 0, 9], [(8, 8), (8, 8), (8, 9)])])
+def test_rows_of_offsets_that_do_not_ascend(fmt, offsets, ranges):
+    """Each expert's range is taken into [0, nrows] and begins no earlier than those before it end: every row has one expert
+    at most, and rows of none stay as they are."""
+    rows, E, N, K = 9, 3, 40, 64
+    g = qi.rng(4)
+    wc, ws = exact_inputs(g, fmt, (E, N, K))
+    xc, xs = exact_inputs(g, fmt, (rows, K))
+    desc, w = packed_weights(fmt, wc, ws)
+    y = torch.full((rows + 2, N), 7.0, dtype=torch.float32, device=DEV)
+    qmv.qmv_mx_product(desc, w, dev(ref.act_buffer(xc, xs, fmt)), rows, dev(np.array(offsets, dtype=np.int32)), "f32", y)
+    want, xv = np.full((rows + 2, N), 7.0), ref.decode(xc, xs, fmt)
+    for e, (a, b) in enumerate(ranges):
+        want[a:b] = xv[a:b] @ ref.decode(wc[e], ws[e], fmt).T
+    assert np.array_equal(host(y), want) and status_clean()
+
+
+def test_many_descending_offsets():
+    """1024 experts whose offsets fall and rise by turns: only the first pair names rows."""
+    rows, E, N, K = 300, qmv.MAX_SORT_EXPERTS, 24, 32
+    g = qi.rng(5)
+    wc, ws = exact_inputs(g, "mxfp4", (E, N, K))
+    xc, xs = exact_inputs(g, "mxfp4", (rows, K))
+    desc, w = packed_weights("mxfp4", wc, ws)
+    offsets = np.where(np.arange(E + 1) % 2 == 0, 0, rows).astype(np.int32)
+    y = torch.full((rows, N), 7.0, dtype=torch.float32, device=DEV)
+    qmv.qmv_mx_product(desc, w, dev(ref.act_buffer(xc, xs, "mxfp4")), rows, dev(offsets), "f32", y)
+    assert np.array_equal(host(y), ref.decode(xc, xs, "mxfp4") @ ref.decode(wc[0], ws[0], "mxfp4").T) and status_clean()
