@@ -503,7 +503,8 @@ int qmv_mx_product(const qmv_wdesc* desc, const void* w_dev, const void* xq_dev,
 /*
  * Gate and up projections with the SwiGLU between them, over rows:
  *   h[r] = silu(W_gate . x[r]) * (W_up . x[r])
- * with the gate and up sums in fp32 and h quantized, without another rounding,
+ * with the gate and up sums in fp32 and h, within 12 * 2^-24 of that (0 for
+ * gates below -167), quantized without another rounding
  * to the activation buffer hq_dev (h_fmt: an MX format; nrows rows of N
  * columns, N a multiple of 32), the down projection's input. desc describes one
  * projection, w_gate_up_dev is packed by qmv_pack_gate_up; xq, nrows and

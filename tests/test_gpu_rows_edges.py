@@ -231,3 +231,30 @@ def test_many_descending_offsets():
     y = torch.full((rows, N), 7.0, dtype=torch.float32, device=DEV)
     qmv.qmv_mx_product(desc, w, dev(ref.act_buffer(xc, xs, "mxfp4")), rows, dev(offsets), "f32", y)
     assert np.array_equal(host(y), ref.decode(xc, xs, "mxfp4") @ ref.decode(wc[0], ws[0], "mxfp4").T) and status_clean()
+
+
+@pytest.mark.parametrize("h_fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("rows", [40, 700])
+def test_gate_up_swiglu_of_large_negative_gates(h_fmt, rows):
+    """silu(g) of g from -160 to 48 beside up sums so large that the product is an ordinary number: within 12 fp32 roundings
+    (four for the exponential, two for the reciprocal, six sums and products)."""
+    N, K = 224, 32
+    g = qi.rng(rows)
+    gc, gs = np.zeros((1, N, K), dtype=np.uint8), np.full((1, N, 1), 127 + 5, dtype=np.uint8)
+    gc[0, :, 0] = g.choice([12, 13], size=N)                                # -2 and -3, times 32
+    gc[0, 160:, 0] = g.choice([9, 10, 11, 12, 13, 1], size=N - 160)         # groups of every size: -0.5 .. -3 and 0.5
+    uc, us = exact_inputs(g, "mxfp4", (1, N, K))
+    us = np.repeat(g.integers(127 + 90, 127 + 100, size=(1, N // 32, 1)), 32, axis=1).astype(np.uint8)
+    xc, xs = np.zeros((rows, K), dtype=np.uint8), np.full((rows, 1), 127, dtype=np.uint8)
+    xc[:, 0] = g.choice([1, 2, 3], size=rows)                               # 0.5, 1, 1.5
+    desc = qmv.wdesc("mxfp4", N, K, 1)
+    w = dev(qmv.qmv_pack_gate_up(desc, oracle.pack_codes("mxfp4", gc), gs, oracle.pack_codes("mxfp4", uc), us))
+    hq = buf(qmv.qmv_act_mx_bytes(h_fmt, rows, N))
+    qmv.qmv_mx_gate_up_swiglu(desc, w, dev(ref.act_buffer(xc, xs, "mxfp4")), rows, None, h_fmt, hq)
+    xv = ref.decode(xc, xs, "mxfp4")
+    gate, up = xv @ ref.decode(gc[0], gs[0], "mxfp4").T, xv @ ref.decode(uc[0], us[0], "mxfp4").T
+    assert gate.min() < -100 and (np.abs(gate) < 87).any()
+    h = ref.silu(gate) * up
+    codes, scales = unpacked(h_fmt, hq, rows, N)
+    quantized_close(codes, scales, h, 12 * 2.0 ** -24 * np.abs(h) + 2.0 ** -149, h_fmt)
+    assert status_clean()
