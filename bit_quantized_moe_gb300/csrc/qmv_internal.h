@@ -1,6 +1,7 @@
 // qmv_internal.h -- host-side interface between the C ABI and the kernel launchers.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -160,6 +161,32 @@ struct MxGemmArgs {
 };
 cudaError_t launch_mx_gemm(const MxGemmArgs& a);
 uint32_t status_mx_gemm(int clear);
+
+// A number (0 or more) that is asked of each device once, by the first call
+// that needs it there; host threads may ask at the same time.
+class PerDevice {
+ public:
+  // ask(int*) -> cudaError_t: the current device's number. An error is not kept.
+  template <typename F>
+  cudaError_t get(int* value, F&& ask) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    const int known = known_[dev].load(std::memory_order_relaxed);
+    if (known != 0) {
+      *value = known - 1;
+      return cudaSuccess;
+    }
+    e = ask(value);
+    if (e == cudaSuccess) known_[dev].store(*value + 1, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<int> known_[kDevices] = {};   // the number + 1; 0: not asked yet
+};
 
 // Launch with programmatic stream serialization (the kernel begins with
 // griddepcontrol.wait); the legacy default stream has no such edges.

@@ -34,7 +34,6 @@
 //   2      tells warp 1, on the codes' barrier, that a step's scales are there
 // Tiles of an expert follow one another along its rows, so that its weights
 // are read from memory once and again from L2.
-#include <atomic>
 #include <cmath>
 
 #include <cuda.h>
@@ -977,16 +976,14 @@ cudaError_t go(const MxGemmArgs& a) {
   // ends would have its share of the tiles still before it.
   int most = device_sm_count();
   if constexpr (PAIR) {
-    static std::atomic<int> pairs{0};   // per kernel: the same on every device this library is built for
-    most = pairs.load(std::memory_order_relaxed);
-    if (most == 0) {
-      g_launch_stage = "cudaOccupancyMaxActiveClusters";
+    static PerDevice pairs;
+    g_launch_stage = "cudaOccupancyMaxActiveClusters";
+    e = pairs.get(&most, [&cfg](int* n) {
       cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2));
-      e = cudaOccupancyMaxActiveClusters(&most, mx_gemm_kernel<FMT, HFMT, TN, PAIR>, &cfg);
-      if (e != cudaSuccess) return e;
-      if (most < 1) return cudaErrorInvalidConfiguration;
-      pairs.store(most, std::memory_order_relaxed);
-    }
+      return cudaOccupancyMaxActiveClusters(n, mx_gemm_kernel<FMT, HFMT, TN, PAIR>, &cfg);
+    });
+    if (e != cudaSuccess) return e;
+    if (most < 1) return cudaErrorInvalidConfiguration;
   }
   if (grid > most) grid = most;
   g_launch_stage = "launch";

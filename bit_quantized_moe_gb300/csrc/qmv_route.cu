@@ -1,7 +1,6 @@
 // qmv_route.cu -- tokens sorted by expert and back: the stable sort of routed
 // slots, the copies between the tokens' and the experts' row order, the
 // weighted sum, and the gradients of both.
-#include <atomic>
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -195,21 +194,22 @@ cudaError_t launch_moe_sort(const SortArgs& a) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   if (ctas > 8) {
-    static std::atomic<int> wide{-1};   // whether the device places a cluster of 16 with the most shared memory
-    int fit = wide.load(std::memory_order_relaxed);
-    if (fit < 0) {
+    static PerDevice wide;   // clusters of 16 with the most shared memory that the device places
+    int fit = 0;
+    e = wide.get(&fit, [&](int* n) {
       attr[0].val.clusterDim.x = (unsigned)kSortMaxCtas;
       cfg.gridDim = dim3((unsigned)kSortMaxCtas);
       cfg.dynamicSmemBytes = kSortSmemMax;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&fit, moe_sort_kernel, &cfg) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(n, moe_sort_kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();
-        fit = 0;
+        *n = 0;
       }
-      wide.store(fit > 0 ? 1 : 0, std::memory_order_relaxed);
       cfg.dynamicSmemBytes = smem;
-    }
+      return cudaSuccess;
+    });
+    if (e != cudaSuccess) return e;
     if (fit < 1) ctas = 8;
   }
   cfg.gridDim = dim3((unsigned)ctas);
