@@ -94,27 +94,29 @@ class Routed(torch.autograd.Function):
     def forward(ctx, x, row_of_slot, top_k):
         ctx.save_for_backward(row_of_slot)
         ctx.shape = (*x.shape, top_k)
-        xs = empty(x.shape[0] * top_k, x.shape[1])
-        qmv.qmv_moe_dispatch("bf16", x, x.stride(0), x.shape[0], top_k, x.shape[1], row_of_slot, xs)
+        x = x.contiguous()
+        xs = empty(x.shape[0] * top_k, x.shape[1], dtype=x.dtype)
+        qmv.qmv_moe_dispatch(x.dtype, x, x.shape[1], x.shape[0], top_k, x.shape[1], row_of_slot, xs)
         return xs
 
     @staticmethod
     def backward(ctx, dxs):
         (row_of_slot,), (tokens, width, top_k) = ctx.saved_tensors, ctx.shape
-        dx = empty(tokens, width)
-        qmv.qmv_moe_dispatch_grad("bf16", dxs.contiguous(), tokens, top_k, width, row_of_slot, dx, width)
+        dx = empty(tokens, width, dtype=dxs.dtype)
+        qmv.qmv_moe_dispatch_grad(dxs.dtype, dxs.contiguous(), tokens, top_k, width, row_of_slot, dx, width)
         return dx, None, None
 
 
 class Returned(torch.autograd.Function):
-    """The experts' rows back to their tokens, with the router's weights."""
+    """The experts' rows back to their tokens, with the router's weights (fp32)."""
 
     @staticmethod
     def forward(ctx, ys, weights, row_of_slot):
+        ys, weights = ys.contiguous(), weights.contiguous()
         ctx.save_for_backward(ys, weights, row_of_slot)
         tokens, top_k = weights.shape
-        y = empty(tokens, ys.shape[1])
-        qmv.qmv_moe_return("bf16", ys, weights, tokens, top_k, ys.shape[1], row_of_slot, y, ys.shape[1])
+        y = empty(tokens, ys.shape[1], dtype=ys.dtype)
+        qmv.qmv_moe_return(ys.dtype, ys, weights, tokens, top_k, ys.shape[1], row_of_slot, y, ys.shape[1])
         return y
 
     @staticmethod
@@ -122,7 +124,7 @@ class Returned(torch.autograd.Function):
         ys, weights, row_of_slot = ctx.saved_tensors
         tokens, top_k = weights.shape
         dys, dweights = torch.empty_like(ys), torch.empty_like(weights)
-        qmv.qmv_moe_return_grad("bf16", dy.contiguous(), ys.shape[1], ys, weights, tokens, top_k, ys.shape[1], row_of_slot, dys,
+        qmv.qmv_moe_return_grad(ys.dtype, dy.contiguous(), ys.shape[1], ys, weights, tokens, top_k, ys.shape[1], row_of_slot, dys,
                                 dweights)
         return dys, dweights, None
 

@@ -50,3 +50,34 @@ def test_routed_gradients_match_torch():
     assert (y.double() - want).abs().max() <= 2 ** -8 * want.abs().max()
     assert (mine[0].double() - theirs[0].double()).abs().max() <= 2 * 2 ** -8 * theirs[0].double().abs().max()
     assert (mine[1].double() - theirs[1].double()).abs().max() <= 1e-5 * theirs[1].double().abs().max()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_routed_functions_take_strides_and_types_as_they_come(dtype):
+    """Transposed and expanded tokens, rows, weights and gradients, in each type, give what their contiguous copies give."""
+    m = example()
+    tokens, experts, top_k, width = 21, 5, 3, 40
+    g = torch.Generator(device=m.DEV).manual_seed(5)
+    ids = torch.rand(tokens, experts, generator=g, device=m.DEV).topk(top_k).indices
+    slot = torch.argsort(ids.flatten(), stable=True)
+    row = torch.empty_like(slot)
+    row[slot] = torch.arange(len(slot), device=m.DEV)
+    row = row.to(torch.int32)
+
+    def turned(*shape):
+        return torch.randn(*reversed(shape), generator=g, device=m.DEV).to(dtype).T
+
+    x, ys, dxs, dy = turned(tokens, width), turned(tokens * top_k, width), turned(tokens * top_k, width), turned(tokens, width)
+    weights = torch.rand(top_k, tokens, generator=g, device=m.DEV).T
+    one = torch.randn(1, width, generator=g, device=m.DEV).to(dtype).expand(tokens, width)
+
+    def results(x, ys, weights, dxs, dy):
+        x, ys, weights = (t.detach().requires_grad_() for t in (x, ys, weights))
+        xs, y = m.Routed.apply(x, row, top_k), m.Returned.apply(ys, weights, row)
+        return [xs, y, *torch.autograd.grad(xs, x, dxs), *torch.autograd.grad(y, (ys, weights), dy)]
+
+    for tok in (x, one):
+        args = (tok, ys, weights, dxs, dy)
+        got, want = results(*args), results(*(t.contiguous() for t in args))
+        assert all(a.dtype == b.dtype and torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(got[0], tok[slot // top_k])
