@@ -258,3 +258,135 @@ def test_gate_up_swiglu_of_large_negative_gates(h_fmt, rows):
     codes, scales = unpacked(h_fmt, hq, rows, N)
     quantized_close(codes, scales, h, 12 * 2.0 ** -24 * np.abs(h) + 2.0 ** -149, h_fmt)
     assert status_clean()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quantize_special_groups_of_16_bits(fmt, dtype):
+    """Zeros, subnormals, the largest numbers, infinities and NaN in every column of a group, beside ordinary groups."""
+    tiny, big = (2.0 ** -133, 3.3895313892515355e38) if dtype == "bf16" else (2.0 ** -24, 65504.0)
+    special = [0.0, -0.0, tiny, -tiny, 37 * tiny, big, -big, np.inf, -np.inf, np.nan]
+    K = 96
+    v = np.tile(randn(1, 1, K), (32 * len(special), 1))
+    for i, s in enumerate(special):
+        for c in range(32):
+            row = v[32 * i + c]
+            if abs(s) < 1:
+                row[32:64] = 0.0     # a group of nothing else
+            row[32 + c] = s
+    v[-1, 32:64] = np.where(np.arange(32) % 2, np.inf, np.nan)
+    x = dev(v, dtype)
+    rows = len(v)
+    xq = buf(qmv.qmv_act_mx_bytes(fmt, rows, K))
+    qmv.qmv_quantize_act_mx(fmt, dtype, x, K, rows, K, xq)
+    codes, scales = unpacked(fmt, xq, rows, K)
+    want_c, want_s = ref.quantize(host(x), fmt)
+    assert (want_s == 255).sum() == 3 * 32
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("out", ["plain", "mxfp8", "mxfp4", "q8"])
+@pytest.mark.parametrize("K", [96, 2880])
+def test_rms_norm_of_rows_with_infinities_and_nan(dtype, out, K):
+    """An infinity makes its own column NaN and the others 0, a NaN the whole row; the rows beside them stay ordinary."""
+    v = randn(K, 7, K)
+    v[1, 5], v[3, K - 1], v[5, 33] = np.inf, np.nan, -np.inf
+    s, y = norm_case(dtype, v, 1e-5, out)
+    with np.errstate(invalid="ignore"):
+        want = s / np.sqrt((s ** 2).mean(-1, keepdims=True) + 1e-5)
+    bad = np.isnan(want)
+    assert bad[1].sum() == 1 and bad[3].all() and bad[5].sum() == 1
+    err = 1e-5 * np.abs(want)
+    if out == "plain":
+        got = host(y.view(TORCH[dtype]).view(s.shape))
+        assert np.array_equal(np.isnan(got), bad)
+        assert_within(np.where(bad, 0, got), np.where(bad, 0, want), np.where(bad, 0, err), dtype, "y")
+    elif out == "q8":
+        q, d = qmv.qmv_act_q8_unpack(y.cpu().numpy(), *s.shape)
+        d = oracle.f16_bits_to_f64(d)
+        groups = bad.reshape(7, -1, 32).any(-1)
+        assert np.array_equal(np.isnan(d), groups)
+        exact_d = np.abs(np.where(bad, 0, want)).reshape(7, -1, 32).max(-1) / 127
+        assert (np.abs(d - exact_d)[~groups] <= (exact_d * (2.0 ** -11 + 1.1e-5) + 2.0 ** -25)[~groups]).all()
+        q = q.reshape(7, -1, 32)
+        assert not q[1][~groups[1]].any() and not q[5][~groups[5]].any() and q[0].any()
+    else:
+        codes, scales = unpacked(out, y, *s.shape)
+        groups = bad.reshape(7, -1, 32).any(-1)
+        assert np.array_equal(scales == 255, groups) and not codes.reshape(7, -1, 32)[groups].any()
+        keep = [0, 2, 4, 6]
+        quantized_close(codes[keep], scales[keep], want[keep], err[keep], out)
+        assert not scales[1][~groups[1]].any() and not scales[5][~groups[5]].any()
+
+
+@pytest.mark.parametrize("h_fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("rows", [70, 600])
+def test_gate_up_swiglu_of_nan_and_infinite_sums(h_fmt, rows):
+    """A NaN gate or up sum, or an infinite one, makes its group of h NaN; the other groups and rows are as without it."""
+    N, K = 128, 160
+    g = qi.rng(rows)
+    (gc, gs), (uc, us), (xc, xs) = (exact_inputs(g, "mxfp8", s) for s in ((1, N, K), (1, N, K), (rows, K)))
+    gs = (gs - 9).astype(np.uint8)
+    desc = qmv.wdesc("mxfp8", N, K, 1)
+
+    def h_of(gs, us, xs):
+        w = dev(qmv.qmv_pack_gate_up(desc, gc, gs, uc, us))
+        hq = buf(qmv.qmv_act_mx_bytes(h_fmt, rows, N))
+        qmv.qmv_mx_gate_up_swiglu(desc, w, dev(ref.act_buffer(xc, xs, "mxfp8")), rows, None, h_fmt, hq)
+        return unpacked(h_fmt, hq, rows, N)
+
+    codes, scales = h_of(gs, us, xs)
+    assert not (scales == 255).any()
+    bad_gs, bad_us, bad_xs = gs.copy(), us.copy(), xs.copy()
+    bad_gs[0, 3, 1], bad_us[0, 40, 2], bad_us[0, 70], bad_xs[7, 4] = 255, 255, 254, 255   # groups 0, 1 and 2; row 7
+    c, s = h_of(bad_gs, bad_us, bad_xs)
+    over = np.abs(ref.decode(xc, xs, "mxfp8") @ ref.decode(uc[0], bad_us[0], "mxfp8")[70]) >= 2.0 ** 128
+    assert over.sum() > rows // 2
+    assert (s[:, :2] == 255).all() and (s[over, 2] == 255).all() and (s[7] == 255).all()
+    other = np.delete(np.arange(rows), 7)
+    c, codes = c.reshape(rows, -1, 32), codes.reshape(rows, -1, 32)
+    assert np.array_equal(s[other, 3], scales[other, 3]) and np.array_equal(c[other, 3], codes[other, 3])
+    assert not c[other, :2].any() and status_clean()
+
+
+def test_layer_of_tokens_with_infinities_and_nan():
+    """Tokens with an infinity or a NaN are NaN where an expert takes them; the others' outputs are those of a call with
+    ordinary values in those places; a dropped token of NaN is zeros."""
+    ntok, top_k, E, K, N, N_down = 150, 2, 3, 288, 96, 200
+    gu, w_gu, dn, w_dn, x, ids, weights, _ = layer_case("mxfp4", "mxfp8", "bf16", ntok, top_k, E, K, N, N_down, 0.0)
+    bad = [3, 64, 149]
+    ids[64] = -1
+    ws = buf(qmv.qmv_moe_prefill_layer_workspace_bytes(gu, dn, ntok, top_k))
+
+    def run():
+        y = torch.full((ntok, N_down), 7.0, dtype=torch.bfloat16, device=DEV)
+        qmv.qmv_moe_prefill_layer(gu, w_gu, dn, w_dn, "bf16", x, K, dev(ids), weights, ntok, top_k, ws, y)
+        return y
+
+    want = run()
+    x[3, 7], x[64], x[149, K - 1] = float("inf"), float("nan"), float("nan")
+    got = run()
+    keep = [t for t in range(ntok) if t not in bad]
+    assert torch.equal(got[keep], want[keep])
+    assert got[3].isnan().all() and got[149].isnan().all() and not got[64].any() and status_clean()
+
+
+def test_layers_on_two_streams_at_once():
+    """Two layers of different shapes in flight together, each with its own workspace, give what they give alone."""
+    runs = []
+    for args in (("mxfp4", "mxfp4", "bf16", 300, 4, 8, 288, 96, 200, 0.1), ("mxfp8", "mxfp4", "f16", 41, 2, 5, 416, 160, 264, 0.0)):
+        gu, w_gu, dn, w_dn, x, ids, weights, _ = layer_case(*args)
+        dtype, ntok, top_k, K = args[2], args[3], args[4], args[6]
+        y = [torch.empty(ntok, args[8], dtype=TORCH[dtype], device=DEV) for _ in range(2)]
+        ws = buf(qmv.qmv_moe_prefill_layer_workspace_bytes(gu, dn, ntok, top_k))
+        runs.append((y, torch.cuda.Stream(), lambda out, s, a=(gu, w_gu, dn, w_dn, dtype, x, K, dev(ids), weights, ntok, top_k, ws):
+                     qmv.qmv_moe_prefill_layer(*a, out, s)))
+    for y, _, call in runs:
+        call(y[0], None)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for y, s, call in runs:
+            call(y[1], s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(*y) for y, _, _ in runs) and status_clean()
