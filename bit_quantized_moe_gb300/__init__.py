@@ -41,6 +41,7 @@ FORMATS = {"mxfp4": MXFP4, "cb2": CB2, "cb3": CB3, "cb4": CB4, "mxfp8": MXFP8}
 QMV_BF16, QMV_F16, QMV_F32 = 0, 1, 2
 TYPES = {"bf16": QMV_BF16, "f16": QMV_F16, "f32": QMV_F32,
          torch.bfloat16: QMV_BF16, torch.float16: QMV_F16, torch.float32: QMV_F32}
+_BYTES = {k: 4 if v == QMV_F32 else 2 for k, v in TYPES.items()} | {QMV_BF16: 2, QMV_F16: 2, QMV_F32: 4}   # of an element
 QMV_NORM_PLAIN, QMV_NORM_MXFP8, QMV_NORM_MXFP4, QMV_NORM_Q8 = 0, 1, 2, 3
 NORM_OUTS = {"plain": QMV_NORM_PLAIN, "mxfp8": QMV_NORM_MXFP8, "mxfp4": QMV_NORM_MXFP4, "q8": QMV_NORM_Q8}
 MAX_ROWS = 1 << 22
@@ -369,6 +370,7 @@ def qmv_swiglu_bf16(g, u, h, n: int, stream=None) -> None:
 # --- many rows -------------------------------------------------------------------
 # dtype: "bf16", "f16", "f32", the torch dtype or the qmv_type value; strides
 # (ldx, ...) in elements; act buffers are uint8 tensors of qmv_act_mx_bytes.
+# Row and gradient outputs that are too small for the call raise QMV_ESIZE.
 
 def _type(dtype) -> int:
     return TYPES[dtype] if isinstance(dtype, (str, torch.dtype)) else int(dtype)
@@ -376,6 +378,18 @@ def _type(dtype) -> int:
 
 def _fmt(fmt) -> int:
     return FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+
+
+def _short(name: str, what: str, t, need: int) -> None:
+    """Raises QMV_ESIZE where tensor t ends less than `need` bytes past its first element (a view of rows that lie further
+    apart than they are wide may go on past its own elements)."""
+    have = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+    if have < need:
+        raise QmvError(QMV_ESIZE, f"{name}: {what} {have} bytes < {need}")
+
+
+def _span(rows: int, ld: int, width: int) -> int:
+    return (rows - 1) * ld + width if rows > 0 else 0
 
 
 def qmv_act_mx_bytes(fmt, nrows: int, K: int) -> int:
@@ -406,12 +420,16 @@ def qmv_quantize_act_mx(fmt, dtype, x, ldx: int, nrows: int, K: int, xq, stream=
 def qmv_rms_norm(dtype, x, ldx: int, residual, ldr: int, gain, nrows: int, K: int, eps: float, sum_out, out, y,
                  stream=None) -> None:
     """out: "plain", "mxfp8", "mxfp4" or "q8" (QMV_NORM_*); residual and sum_out may be None."""
+    if isinstance(sum_out, torch.Tensor) and sum_out.nbytes < (need := _span(nrows, ldr, K) * _BYTES.get(dtype, 0)):
+        _short("qmv_rms_norm", "sum", sum_out, need)
     _check(lib.qmv_rms_norm(_type(dtype), _ptr(x), ldx, _ptr(residual), ldr, _ptr(gain), nrows, K, eps, _ptr(sum_out),
                             NORM_OUTS[out] if isinstance(out, str) else int(out), _ptr(y), _nbytes(y),
                             _stream(stream)))
 
 
 def qmv_mx_product(desc: WDesc, w, xq, nrows: int, offsets, dtype, y, stream=None) -> None:
+    if isinstance(y, torch.Tensor) and y.nbytes < (need := nrows * desc.N * _BYTES.get(dtype, 0)):
+        _short("qmv_mx_product", "y", y, need)
     _check(lib.qmv_mx_product(ctypes.byref(desc), _ptr(w), _ptr(xq), _nbytes(xq), nrows, _ptr(offsets), _type(dtype),
                               _ptr(y), _stream(stream)))
 
@@ -433,6 +451,8 @@ def qmv_moe_sort(ids, ntok: int, top_k: int, n_experts: int, offsets, row_of_slo
 
 
 def qmv_moe_dispatch(dtype, x, ldx: int, ntok: int, top_k: int, K: int, row_of_slot, xs, stream=None) -> None:
+    if isinstance(xs, torch.Tensor) and xs.nbytes < (need := ntok * top_k * K * _BYTES.get(dtype, 0)):
+        _short("qmv_moe_dispatch", "xs", xs, need)
     _check(lib.qmv_moe_dispatch(_type(dtype), _ptr(x), ldx, ntok, top_k, K, _ptr(row_of_slot), _ptr(xs),
                                 _stream(stream)))
 
@@ -443,17 +463,25 @@ def qmv_moe_dispatch_mx(fmt, dtype, x, ldx: int, ntok: int, top_k: int, K: int, 
 
 
 def qmv_moe_dispatch_grad(dtype, dxs, ntok: int, top_k: int, K: int, row_of_slot, dx, ldx: int, stream=None) -> None:
+    if isinstance(dx, torch.Tensor) and dx.nbytes < (need := _span(ntok, ldx, K) * _BYTES.get(dtype, 0)):
+        _short("qmv_moe_dispatch_grad", "dx", dx, need)
     _check(lib.qmv_moe_dispatch_grad(_type(dtype), _ptr(dxs), ntok, top_k, K, _ptr(row_of_slot), _ptr(dx), ldx,
                                      _stream(stream)))
 
 
 def qmv_moe_return(dtype, ys, weights, ntok: int, top_k: int, N: int, row_of_slot, y, ldy: int, stream=None) -> None:
+    if isinstance(y, torch.Tensor) and y.nbytes < (need := _span(ntok, ldy, N) * _BYTES.get(dtype, 0)):
+        _short("qmv_moe_return", "y", y, need)
     _check(lib.qmv_moe_return(_type(dtype), _ptr(ys), _ptr(weights), ntok, top_k, N, _ptr(row_of_slot), _ptr(y), ldy,
                               _stream(stream)))
 
 
 def qmv_moe_return_grad(dtype, dy, ld_dy: int, ys, weights, ntok: int, top_k: int, N: int, row_of_slot, dys, dweights,
                         stream=None) -> None:
+    if isinstance(dys, torch.Tensor) and dys.nbytes < (need := ntok * top_k * N * _BYTES.get(dtype, 0)):
+        _short("qmv_moe_return_grad", "dys", dys, need)
+    if isinstance(dweights, torch.Tensor) and dweights.nbytes < (need := ntok * top_k * 4):
+        _short("qmv_moe_return_grad", "dweights", dweights, need)
     _check(lib.qmv_moe_return_grad(_type(dtype), _ptr(dy), ld_dy, _ptr(ys), _ptr(weights), ntok, top_k, N,
                                    _ptr(row_of_slot), _ptr(dys), _ptr(dweights), _stream(stream)))
 
@@ -464,6 +492,8 @@ def qmv_moe_prefill_layer_workspace_bytes(gate_up_desc: WDesc, down_desc: WDesc,
 
 def qmv_moe_prefill_layer(gate_up_desc: WDesc, w_gate_up, down_desc: WDesc, w_down, dtype, x, ldx: int, ids, weights,
                           ntok: int, top_k: int, workspace, y, stream=None) -> None:
+    if isinstance(y, torch.Tensor) and y.nbytes < (need := ntok * down_desc.N * _BYTES.get(dtype, 0)):
+        _short("qmv_moe_prefill_layer", "y", y, need)
     _check(lib.qmv_moe_prefill_layer(ctypes.byref(gate_up_desc), _ptr(w_gate_up), ctypes.byref(down_desc),
                                      _ptr(w_down), _type(dtype), _ptr(x), ldx, _ptr(ids), _ptr(weights), ntok, top_k,
                                      _ptr(workspace), _nbytes(workspace), _ptr(y), _stream(stream)))

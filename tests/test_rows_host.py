@@ -160,3 +160,34 @@ def test_widths_of_the_routed_rows():
     for name, good in (("qmv_moe_dispatch", DISPATCH), ("qmv_moe_dispatch_grad", DISPATCH_GRAD)):
         assert _call(name, good, ntok=0, K=65536, ldx=65536) == 0
         assert _call(name, good, ntok=0, K=65537, ldx=65537) == -2
+
+
+def test_output_tensors_that_are_too_small_are_refused():
+    """Rows and gradients whose C call takes no size: the binding compares their tensors with what the call writes."""
+    desc = qmv.wdesc("mxfp4", 64, 64, 4)
+    down = qmv.wdesc("mxfp8", 96, 64, 4)
+    one = torch.zeros(BIG >> 40, dtype=torch.uint8)   # stands for buffers whose size the C call takes
+
+    def f32(n):
+        return torch.zeros(n, dtype=torch.float32)
+
+    calls = [
+        (lambda t: qmv.qmv_rms_norm("f32", P, 64, P, 70, P, 3, 64, 1e-5, t, "plain", one, 0), f32, 2 * 70 + 64, "sum"),
+        (lambda t: qmv.qmv_mx_product(desc, P, one, 3, P, "f32", t, 0), f32, 3 * 64, "y"),
+        (lambda t: qmv.qmv_moe_dispatch("f32", P, 64, 4, 2, 64, P, t, 0), f32, 8 * 64, "xs"),
+        (lambda t: qmv.qmv_moe_dispatch_grad("f32", P, 4, 2, 64, P, t, 70, 0), f32, 3 * 70 + 64, "dx"),
+        (lambda t: qmv.qmv_moe_return("f32", P, P, 4, 2, 64, P, t, 70, 0), f32, 3 * 70 + 64, "y"),
+        (lambda t: qmv.qmv_moe_return_grad("f32", P, 64, P, P, 4, 2, 64, P, t, f32(8), 0), f32, 8 * 64, "dys"),
+        (lambda t: qmv.qmv_moe_return_grad("f32", P, 64, P, P, 4, 2, 64, P, f32(512), t, 0), f32, 8, "dweights"),
+        (lambda t: qmv.qmv_moe_prefill_layer(qmv.wdesc("mxfp4", 64, 96, 4), P, down, P, "bf16", P, 96, P, P, 3, 2, one, t, 0),
+         lambda n: torch.zeros(n, dtype=torch.bfloat16), 3 * 96, "y"),
+    ]
+    for call, new, need, what in calls:
+        with pytest.raises(qmv.QmvError) as e:
+            call(new(need - 1))
+        assert e.value.code == qmv.QMV_ESIZE and f" {what} " in str(e.value)
+    # a view of rows that lie further apart holds what its storage holds from its first element on
+    wide = f32(4 * 70)
+    qmv._short("call", "y", wide.view(4, 70)[:, :64], 4 * (3 * 70 + 64))
+    with pytest.raises(qmv.QmvError):
+        qmv._short("call", "y", wide.view(4, 70)[1:, :64], 4 * (3 * 70 + 64))
