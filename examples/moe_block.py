@@ -6,9 +6,9 @@
    (qmv_rms_norm, qmv_moe_prefill_layer).
 2. Decode: the next token through the same weights (qmv_moe_layer_combine). The two agree to the prompt
    path's quantization of the activations.
-3. Training over frozen experts: a trainable map on the experts' rows between the dispatch and the weighted
+3. A training step's routing: a trainable map in the experts' place between the dispatch and the weighted
    return, its gradient, the router weights' and the input's (qmv_moe_sort, qmv_moe_dispatch,
-   qmv_moe_return and their gradients).
+   qmv_moe_return and their gradients; the experts' own input gradients are not among the calls).
 """
 import argparse
 import os
