@@ -36,10 +36,9 @@
 // are read from memory once and again from L2.
 #include <cmath>
 
-#include <cuda.h>
-
 #include "qmv_internal.h"
 #include "qmv_rows.cuh"
+#include "qmv_tc.cuh"
 
 namespace qmv {
 
@@ -104,39 +103,6 @@ struct GemmParams {
   int K, n_experts, out_n, out_type, n_tiles;
 };
 
-// PAIR: `bar` is the leader's barrier, as an address of the cluster.
-template <bool PAIR>
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
-        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-  }
-}
-template <bool PAIR>
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int r, int t, int c, int e,
-                                            uint32_t bar) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        :: "r"(dst), "l"(map), "r"(x), "r"(r), "r"(t), "r"(c), "r"(e), "r"(bar) : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        :: "r"(dst), "l"(map), "r"(x), "r"(r), "r"(t), "r"(c), "r"(e), "r"(bar) : "memory");
-  }
-}
-
-// K-major operand in shared memory, rows of 128 bytes with the 128-byte
-// swizzle, eight rows every 1024 bytes.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
 // Scales in shared memory: 32 rows of 16 bytes, eight every 128 bytes, no swizzle.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
@@ -178,103 +144,6 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
   if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
   else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
 }
-// Arrives when this thread's earlier MMAs and copies are complete; PAIR: at the
-// same barrier of both CTAs.
-template <bool PAIR>
-__device__ __forceinline__ void mma_commit_to(uint32_t bar) {
-  if constexpr (PAIR) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(bar), "h"((uint16_t)3) : "memory");
-  } else {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
-  }
-}
-// The address of `addr` in the cluster's CTA 0.
-__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-  return r;
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// As mbar_wait_bounded, for a barrier that the other CTA arrives at.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
-  unsigned long long t0 = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
-        : "memory");
-    if (ok != 0) return true;
-    const unsigned long long now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > limit_ns) return false;
-  }
-}
-template <bool PAIR>
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
-  if constexpr (PAIR) return mbar_wait_cluster(bar, parity, kWaitLimitNs);
-  else return mbar_wait_bounded(bar, parity, kWaitLimitNs);
-}
-// Whether a phase is already complete; does not wait.
-__device__ __forceinline__ bool peek(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 accumulator columns of this thread's row.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// Waits for this warp's tensor memory loads; r is not used before it.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :: "memory");
-  asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                    "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                    "+r"(r[30]), "+r"(r[31]) :: "memory");
-}
-
-// One lane of a converged warp, as the compiler knows it: the operands of the
-// instructions it guards stay in uniform registers. (With lane == 0 in its
-// place each tcgen05 instruction took about 100 cycles to issue, and the
-// 8192 x 7168 x 7168 MXFP4 product 295 us.)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
 // The 4 x 4 bytes of four words, transposed.
 __device__ __forceinline__ void transpose4(const uint32_t (&a)[4], uint32_t (&t)[4]) {
   const uint32_t p = prmt(a[0], a[1], 0x5140), q = prmt(a[2], a[3], 0x5140);
@@ -503,38 +372,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
   pdl_wait();
   if (warp == 0) {
     constexpr int unit = kCtas * kTileM;
-    int tiles = 0, reached = 0;   // before expert e0
-    for (int e0 = 0; e0 < p.n_experts; e0 += 32) {
-      const int e = e0 + lane;
-      // Offsets are taken into the call's rows, and none below the ones before it: every row has one expert at most,
-      // whatever the offsets are, and the tiles are as few as the rows allow.
-      int lo = reached, hi = reached;
-      if (e < p.n_experts) {
-        lo = p.offsets != nullptr ? min(p.offsets[e], (int)p.nrows) : 0;
-        hi = p.offsets != nullptr ? min(p.offsets[e + 1], (int)p.nrows) : (int)p.nrows;
-      }
-      if (__any_sync(0xffffffffu, lo < reached || lo > hi)) {   // they do not ascend
-        lo = max(lo, reached);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) lo = max(lo, __shfl_up_sync(0xffffffffu, lo, o));   // its own below lane o
-        hi = max(lo, hi);
-      }
-      reached = __shfl_sync(0xffffffffu, hi, 31);
-      if (e < p.n_experts) {
-        first_row[e] = lo;
-        if (e == p.n_experts - 1) first_row[e + 1] = hi;
-      }
-      int inc = e < p.n_experts ? (hi - lo + unit - 1) / unit * p.n_tiles : 0;
-      const int own = inc;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        inc += lane >= o ? v : 0;
-      }
-      if (e < p.n_experts) first_tile[e] = tiles + inc - own;
-      tiles += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) first_tile[p.n_experts] = tiles;
+    expert_tiles(p.offsets, (int)p.nrows, p.n_experts, unit, p.n_tiles, lane, first_row, first_tile);
   }
   tc_before_sync();
   __syncthreads();
@@ -870,32 +708,6 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
 QMV_DEFINE_STATUS_ACCESSOR(status_mx_gemm)
 
 namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult st;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st) != cudaSuccess ||
-        st != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
-bool encode(CUtensorMap* map, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
-  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box,
-                     one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int FMT, int HFMT, int TN, bool PAIR>
 cudaError_t go(const MxGemmArgs& a) {
