@@ -44,6 +44,8 @@ TYPES = {"bf16": QMV_BF16, "f16": QMV_F16, "f32": QMV_F32,
 _BYTES = {k: 4 if v == QMV_F32 else 2 for k, v in TYPES.items()} | {QMV_BF16: 2, QMV_F16: 2, QMV_F32: 4}   # of an element
 QMV_NORM_PLAIN, QMV_NORM_MXFP8, QMV_NORM_MXFP4, QMV_NORM_Q8 = 0, 1, 2, 3
 NORM_OUTS = {"plain": QMV_NORM_PLAIN, "mxfp8": QMV_NORM_MXFP8, "mxfp4": QMV_NORM_MXFP4, "q8": QMV_NORM_Q8}
+QMV_SCORE_SOFTMAX, QMV_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": QMV_SCORE_SOFTMAX, "sigmoid": QMV_SCORE_SIGMOID}
 MAX_ROWS = 1 << 22
 MAX_SORT_EXPERTS = 1024
 MAX_NTOK = 16
@@ -67,6 +69,10 @@ EXPORTS = (
     "qmv_mx_product", "qmv_mx_gate_up_swiglu", "qmv_moe_sort_workspace_bytes", "qmv_moe_sort", "qmv_moe_dispatch",
     "qmv_moe_dispatch_mx", "qmv_moe_dispatch_grad", "qmv_moe_return", "qmv_moe_return_grad",
     "qmv_moe_prefill_layer_workspace_bytes", "qmv_moe_prefill_layer",
+    "qmv_moe_router", "qmv_moe_balance_workspace_bytes", "qmv_moe_balance", "qmv_moe_router_grad",
+    "qmv_act_b128_bytes", "qmv_act_b128_scale_offset", "qmv_act_b128_unpack", "qmv_quantize_act_b128",
+    "qmv_quantize_weights_b128", "qmv_b128_product", "qmv_b128_linear_workspace_bytes", "qmv_b128_linear",
+    "qmv_b128_grad_x", "qmv_b128_grad_w",
 )
 
 
@@ -155,6 +161,21 @@ def _load() -> ctypes.CDLL:
         "qmv_moe_return_grad": (ctypes.c_int, [I32, P, I64, P, P, I32, I32, I32, P, P, P, P]),
         "qmv_moe_prefill_layer_workspace_bytes": (SZ, [D, D, I32, I32]),
         "qmv_moe_prefill_layer": (ctypes.c_int, [D, P, D, P, I32, P, I64, P, P, I32, I32, P, SZ, P, P]),
+        "qmv_moe_router": (ctypes.c_int, [I32, P, I64, P, I32, I32, I32, I32, I32, ctypes.c_float, P, P, P]),
+        "qmv_moe_balance_workspace_bytes": (SZ, [I32, I32]),
+        "qmv_moe_balance": (ctypes.c_int, [I32, P, I64, P, P, I32, I32, I32, I32, P, P, P, P, SZ, P]),
+        "qmv_moe_router_grad": (ctypes.c_int, [I32, P, I64, P, P, P, P, P, I32, I32, I32, I32, I32, ctypes.c_float, P,
+                                               I64, P]),
+        "qmv_act_b128_bytes": (SZ, [I32, I32]),
+        "qmv_act_b128_scale_offset": (SZ, [I32, I32]),
+        "qmv_act_b128_unpack": (ctypes.c_int, [P, I32, I32, P, P]),
+        "qmv_quantize_act_b128": (ctypes.c_int, [I32, P, I64, I32, I32, P, SZ, P]),
+        "qmv_quantize_weights_b128": (ctypes.c_int, [I32, P, I32, I32, I32, P, P, P]),
+        "qmv_b128_product": (ctypes.c_int, [P, P, I32, I32, I32, P, SZ, I32, P, I32, P, P]),
+        "qmv_b128_linear_workspace_bytes": (SZ, [I32, I32]),
+        "qmv_b128_linear": (ctypes.c_int, [P, P, I32, I32, I32, I32, P, I64, I32, P, P, SZ, P, P]),
+        "qmv_b128_grad_x": (ctypes.c_int, [P, P, I32, I32, I32, P, SZ, I32, P, I32, P, P]),
+        "qmv_b128_grad_w": (ctypes.c_int, [I32, P, I64, P, I64, I32, I32, I32, I32, P, I32, P, P]),
         "qmv_last_error": (ctypes.c_char_p, []),
         "qmv_version": (ctypes.c_char_p, []),
     }
@@ -497,6 +518,109 @@ def qmv_moe_prefill_layer(gate_up_desc: WDesc, w_gate_up, down_desc: WDesc, w_do
     _check(lib.qmv_moe_prefill_layer(ctypes.byref(gate_up_desc), _ptr(w_gate_up), ctypes.byref(down_desc),
                                      _ptr(w_down), _type(dtype), _ptr(x), ldx, _ptr(ids), _ptr(weights), ntok, top_k,
                                      _ptr(workspace), _nbytes(workspace), _ptr(y), _stream(stream)))
+
+
+# --- the router, its balance loss and their gradient ---------------------------------
+# score: "softmax", "sigmoid" or QMV_SCORE_*; live: None or one byte (bool, uint8) a token.
+
+def _score(score) -> int:
+    return SCORES[score] if isinstance(score, str) else int(score)
+
+
+def _need(name: str, what: str, t, need: int) -> None:
+    """Refuses an output tensor that is too small (the C call takes no size of it)."""
+    if isinstance(t, torch.Tensor) and t.nbytes < need:
+        _short(name, what, t, need)
+
+
+def qmv_moe_router(dtype, logits, ldl: int, live, ntok: int, n_experts: int, top_k: int, score, renorm: bool, scale: float,
+                   ids, weights, stream=None) -> None:
+    _need("qmv_moe_router", "ids", ids, ntok * top_k * 4)
+    _need("qmv_moe_router", "weights", weights, ntok * top_k * 4)
+    _check(lib.qmv_moe_router(_type(dtype), _ptr(logits), ldl, _ptr(live), ntok, n_experts, top_k, _score(score), int(renorm),
+                              scale, _ptr(ids), _ptr(weights), _stream(stream)))
+
+
+def qmv_moe_balance_workspace_bytes(ntok: int, n_experts: int) -> int:
+    return lib.qmv_moe_balance_workspace_bytes(ntok, n_experts)
+
+
+def qmv_moe_balance(dtype, logits, ldl: int, live, ids, ntok: int, n_experts: int, top_k: int, score, counts, means, loss,
+                    workspace, stream=None) -> None:
+    _need("qmv_moe_balance", "counts", counts, (n_experts + 1) * 4)
+    _need("qmv_moe_balance", "means", means, n_experts * 4)
+    _need("qmv_moe_balance", "loss", loss, 4)
+    _check(lib.qmv_moe_balance(_type(dtype), _ptr(logits), ldl, _ptr(live), _ptr(ids), ntok, n_experts, top_k, _score(score),
+                               _ptr(counts), _ptr(means), _ptr(loss), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def qmv_moe_router_grad(dtype, logits, ldl: int, live, ids, dweights, counts, dloss, ntok: int, n_experts: int, top_k: int,
+                        score, renorm: bool, scale: float, dlogits, ldd: int, stream=None) -> None:
+    _need("qmv_moe_router_grad", "dlogits", dlogits, _span(ntok, ldd, n_experts) * _BYTES.get(dtype, 0))
+    _check(lib.qmv_moe_router_grad(_type(dtype), _ptr(logits), ldl, _ptr(live), _ptr(ids), _ptr(dweights), _ptr(counts),
+                                   _ptr(dloss), ntok, n_experts, top_k, _score(score), int(renorm), scale, _ptr(dlogits), ldd,
+                                   _stream(stream)))
+
+
+# --- E4M3 with a scale for each block of 128 ------------------------------------------
+# w: codes [n_experts][N][K], w_scales fp32 [n_experts][ceil(N / 128)][ceil(K / 128)].
+
+def qmv_act_b128_bytes(nrows: int, K: int) -> int:
+    return lib.qmv_act_b128_bytes(nrows, K)
+
+
+def qmv_act_b128_scale_offset(nrows: int, K: int) -> int:
+    return lib.qmv_act_b128_scale_offset(nrows, K)
+
+
+def qmv_act_b128_unpack(xq_host: np.ndarray, nrows: int, K: int):
+    """(codes [nrows][K], scales [nrows][ceil(K / 128)]) of a host copy of an activation buffer."""
+    xq_host = np.ascontiguousarray(xq_host, dtype=np.uint8)
+    if xq_host.nbytes < qmv_act_b128_bytes(nrows, K):
+        raise ValueError("activation buffer is smaller than qmv_act_b128_bytes")
+    codes, scales = np.empty((nrows, K), dtype=np.uint8), np.empty((nrows, -(-K // 128)), dtype=np.float32)
+    _check(lib.qmv_act_b128_unpack(xq_host.ctypes.data, nrows, K, codes.ctypes.data, scales.ctypes.data))
+    return codes, scales
+
+
+def qmv_quantize_act_b128(dtype, x, ldx: int, nrows: int, K: int, xq, stream=None) -> None:
+    _check(lib.qmv_quantize_act_b128(_type(dtype), _ptr(x), ldx, nrows, K, _ptr(xq), _nbytes(xq), _stream(stream)))
+
+
+def qmv_quantize_weights_b128(dtype, w, n_experts: int, N: int, K: int, codes, scales, stream=None) -> None:
+    _need("qmv_quantize_weights_b128", "codes", codes, n_experts * N * K)
+    _need("qmv_quantize_weights_b128", "scales", scales, n_experts * -(-N // 128) * -(-K // 128) * 4)
+    _check(lib.qmv_quantize_weights_b128(_type(dtype), _ptr(w), n_experts, N, K, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def qmv_b128_product(w, w_scales, n_experts: int, N: int, K: int, xq, nrows: int, offsets, dtype, y, stream=None) -> None:
+    _need("qmv_b128_product", "y", y, nrows * N * _BYTES.get(dtype, 0))
+    _check(lib.qmv_b128_product(_ptr(w), _ptr(w_scales), n_experts, N, K, _ptr(xq), _nbytes(xq), nrows, _ptr(offsets),
+                                _type(dtype), _ptr(y), _stream(stream)))
+
+
+def qmv_b128_linear_workspace_bytes(nrows: int, K: int) -> int:
+    return lib.qmv_b128_linear_workspace_bytes(nrows, K)
+
+
+def qmv_b128_linear(w, w_scales, n_experts: int, N: int, K: int, dtype, x, ldx: int, nrows: int, offsets, workspace, y,
+                    stream=None) -> None:
+    _need("qmv_b128_linear", "y", y, nrows * N * _BYTES.get(dtype, 0))
+    _check(lib.qmv_b128_linear(_ptr(w), _ptr(w_scales), n_experts, N, K, _type(dtype), _ptr(x), ldx, nrows, _ptr(offsets),
+                               _ptr(workspace), _nbytes(workspace), _ptr(y), _stream(stream)))
+
+
+def qmv_b128_grad_x(w, w_scales, n_experts: int, N: int, K: int, dyq, nrows: int, offsets, dtype, dx, stream=None) -> None:
+    _need("qmv_b128_grad_x", "dx", dx, nrows * K * _BYTES.get(dtype, 0))
+    _check(lib.qmv_b128_grad_x(_ptr(w), _ptr(w_scales), n_experts, N, K, _ptr(dyq), _nbytes(dyq), nrows, _ptr(offsets),
+                               _type(dtype), _ptr(dx), _stream(stream)))
+
+
+def qmv_b128_grad_w(dtype, dy, ld_dy: int, x, ldx: int, n_experts: int, N: int, K: int, nrows: int, offsets, out_dtype, dw,
+                    stream=None) -> None:
+    _need("qmv_b128_grad_w", "dw", dw, n_experts * N * K * _BYTES.get(out_dtype, 0))
+    _check(lib.qmv_b128_grad_w(_type(dtype), _ptr(dy), ld_dy, _ptr(x), ldx, n_experts, N, K, nrows, _ptr(offsets),
+                               _type(out_dtype), _ptr(dw), _stream(stream)))
 
 
 def qmv_debug_block_sums(desc: WDesc, w, x, per_slot_x: int, ids, ntok: int, top_k: int, y, sums,

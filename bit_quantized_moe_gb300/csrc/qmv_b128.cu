@@ -1,0 +1,165 @@
+// qmv_b128.cu -- quantization to E4M3 with one fp32 scale per 128 columns of a
+// row (activations, gradients) or per block of 128 x 128 (weights).
+#include "qmv_internal.h"
+#include "qmv_rows.cuh"
+
+namespace qmv {
+
+// ---------------------------------------------------------------------------
+//   a = max(largest |x| of the block, 2^-116),  scale = a / 448,
+//   code = E4M3(x * (448 / a)),
+// both quotients IEEE divisions, the product rounded to fp32 and then to
+// nearest even. 2^-116 keeps 448 / a finite and the scale a normal number; a
+// block of zeros has codes of 0. A block with an infinity or a NaN has the scale
+// NaN and codes of 0, so that it shows in every product it enters.
+// ---------------------------------------------------------------------------
+constexpr float kB128Floor = 0x1p-116f;
+
+struct BlockScale {
+  float scale, inverse;
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax) {
+  const bool bad = amax >= 0x7f800000u;
+  const float a = fmaxf(__uint_as_float(bad ? 0u : amax), kB128Floor);
+  BlockScale s;
+  s.scale = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(a, 448.0f);
+  s.inverse = bad ? 0.0f : __fdiv_rn(448.0f, a);
+  return s;
+}
+
+// Codes of eight elements; inverse 0 stands for a block without numbers.
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Raw8<T>& r, float inverse) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = inverse == 0.0f ? 0.0f : __fmul_rn(to_f32(r.e[4 * h + i]), inverse);
+    asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n"
+        " mov.b32 %0, {a, b};\n}"
+        : "=r"(w[h])
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight elements from column c on, those past the last as zeros.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_to(const T* row, int c, int K, Raw8<T>& r) {
+  if (VEC && c + 8 <= K) {
+    load_raw8<T, true>(row + c, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.e[i] = c + i < K ? row[c + i] : from_f32<T>(0.0f);
+  }
+}
+
+// Rows: eight lanes take a block of 128 columns, 16 columns each, whose 16
+// codes are one store. Bound by memory: 2 bytes in, 1 + 1/32 out (bf16).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_b128_kernel(B128QuantArgs a) {
+  const int blocks = b128_blocks(a.K);
+  const int64_t unit = (int64_t)blockIdx.x * 32 + threadIdx.x / 8;   // a block of 128 columns
+  const int64_t r = unit / blocks;
+  const int kb = (int)(unit - r * blocks);
+  const bool live = r < a.nrows;
+  const int c = kb * kB128 + (int)(threadIdx.x & 7) * 16;
+  pdl_wait();
+  Raw8<T> raw[2];
+  const T* row = static_cast<const T*>(a.x) + (live ? r : 0) * a.ldx;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_to<T, VEC>(row, c + 8 * i, live ? a.K : 0, raw[i]);
+  uint32_t m = max(amax_bits8(raw[0]), amax_bits8(raw[1]));
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const BlockScale s = block_scale(m);
+  if (live) {
+    uint8_t* out = static_cast<uint8_t*>(a.xq);
+    if (c < a.K) {   // the row's last 16 codes may go past K: they are 0
+      const uint2 lo = codes8<T>(raw[0], s.inverse), hi = codes8<T>(raw[1], s.inverse);
+      *reinterpret_cast<uint4*>(out + (uint64_t)r * b128_row_bytes(a.K) + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+    if ((threadIdx.x & 7) == 0) {
+      reinterpret_cast<float*>(out + b128_scale_offset(a.nrows, a.K))[(int64_t)kb * a.nrows + r] = s.scale;
+    }
+  }
+  pdl_launch_dependents();
+}
+
+// Weights: a CTA takes a block; 16 threads a row, eight columns each.
+template <typename T>
+__global__ void __launch_bounds__(256)
+quantize_weights_b128_kernel(const T* w, int N, int K, int n_blocks, int k_blocks, uint8_t* codes, float* scales) {
+  __shared__ uint32_t part[8];
+  const int64_t block = blockIdx.x;
+  const int kb = (int)(block % k_blocks);
+  const int nb = (int)(block / k_blocks % n_blocks);
+  const int64_t e = block / k_blocks / n_blocks;
+  const int c = kb * kB128 + (int)(threadIdx.x & 15) * 8;
+  const int r0 = nb * kB128 + (int)threadIdx.x / 16;
+  const int64_t base = e * N * K;
+  pdl_wait();
+  Raw8<T> raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {   // K is a multiple of 16
+    const int r = r0 + 16 * i;
+    if (r < N && c < K) load_raw8<T, true>(w + base + (int64_t)r * K + c, raw[i]);
+    else clear_raw8(raw[i]);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, amax_bits8(raw[i]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+  const BlockScale s = block_scale(m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    if (r < N && c < K) *reinterpret_cast<uint2*>(codes + base + (int64_t)r * K + c) = codes8<T>(raw[i], s.inverse);
+  }
+  if (threadIdx.x == 0) scales[block] = s.scale;
+  pdl_launch_dependents();
+}
+
+namespace {
+
+template <typename T>
+cudaError_t quant_b128(const B128QuantArgs& a) {
+  const int64_t units = a.nrows * b128_blocks(a.K);
+  const dim3 grid((unsigned)((units + 31) / 32)), block(256);
+  const bool vec = a.ldx % (16 / (int)sizeof(T)) == 0;
+  return vec ? launch_pdl(quantize_b128_kernel<T, true>, grid, block, 0, a.stream, a)
+             : launch_pdl(quantize_b128_kernel<T, false>, grid, block, 0, a.stream, a);
+}
+
+template <typename T>
+cudaError_t quant_weights(const void* w, int n_experts, int N, int K, void* codes, float* scales, cudaStream_t s) {
+  const int nb = b128_blocks(N), kb = b128_blocks(K);
+  return launch_pdl(quantize_weights_b128_kernel<T>, dim3((unsigned)((int64_t)n_experts * nb * kb)), dim3(256), 0, s,
+                    static_cast<const T*>(w), N, K, nb, kb, static_cast<uint8_t*>(codes), scales);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_b128(const B128QuantArgs& a) {
+  switch (a.type) {
+    case QMV_BF16: return quant_b128<__nv_bfloat16>(a);
+    case QMV_F16: return quant_b128<__half>(a);
+    default: return quant_b128<float>(a);
+  }
+}
+
+cudaError_t launch_quantize_weights_b128(int type, const void* w, int n_experts, int N, int K, void* codes, float* scales,
+                                         cudaStream_t s) {
+  switch (type) {
+    case QMV_BF16: return quant_weights<__nv_bfloat16>(w, n_experts, N, K, codes, scales, s);
+    case QMV_F16: return quant_weights<__half>(w, n_experts, N, K, codes, scales, s);
+    default: return quant_weights<float>(w, n_experts, N, K, codes, scales, s);
+  }
+}
+
+}  // namespace qmv

@@ -162,6 +162,103 @@ struct MxGemmArgs {
 cudaError_t launch_mx_gemm(const MxGemmArgs& a);
 uint32_t status_mx_gemm(int clear);
 
+// The router of a MoE layer (qmv_router.cu). live: null, or 0 for a token that is not there.
+struct RouterArgs {
+  int type = 0, score = 0;      // qmv_type of the logits, qmv_score
+  const void* logits = nullptr;
+  int64_t ldl = 0;
+  const uint8_t* live = nullptr;
+  int64_t ntok = 0;
+  int n_experts = 0, top_k = 1;
+  bool renorm = false;
+  float scale = 1.0f;
+  int32_t* ids = nullptr;
+  float* weights = nullptr;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_router(const RouterArgs& a);
+
+struct BalanceArgs {
+  int type = 0, score = 0;
+  const void* logits = nullptr;
+  int64_t ldl = 0;
+  const uint8_t* live = nullptr;
+  const int32_t* ids = nullptr;
+  int64_t ntok = 0;
+  int n_experts = 0, top_k = 1;
+  int32_t* counts = nullptr;    // [E + 1]
+  float *means = nullptr, *loss = nullptr;
+  int parts = 1;                // CTAs of the first launch: rows of partial sums
+  float* part_sums = nullptr;   // [parts][E]
+  int32_t* part_counts = nullptr;   // [parts][E + 1]
+  cudaStream_t stream = nullptr;
+};
+int balance_parts(int64_t ntok);
+cudaError_t launch_balance(const BalanceArgs& a);
+
+struct RouterGradArgs {
+  int type = 0, score = 0;
+  const void* logits = nullptr;
+  int64_t ldl = 0;
+  const uint8_t* live = nullptr;
+  const int32_t* ids = nullptr;
+  const float* dweights = nullptr;   // null: no gradient of the weights
+  const int32_t* counts = nullptr;   // null: none of the balance loss
+  const float* dloss = nullptr;
+  int64_t ntok = 0;
+  int n_experts = 0, top_k = 1;
+  bool renorm = false;
+  float scale = 1.0f;
+  void* dlogits = nullptr;
+  int64_t ldd = 0;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_router_grad(const RouterGradArgs& a);
+
+// E4M3 with fp32 scales of 128 columns of a row, or of 128 x 128 (qmv_b128.cu).
+struct B128QuantArgs {
+  int type = 0;
+  const void* x = nullptr;
+  int64_t ldx = 0;
+  int64_t nrows = 0;
+  int K = 0;
+  void* xq = nullptr;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_quantize_b128(const B128QuantArgs& a);
+cudaError_t launch_quantize_weights_b128(int type, const void* w, int n_experts, int N, int K, void* codes, float* scales,
+                                         cudaStream_t s);
+
+// Products of such operands (qmv_b128_gemm.cu).
+struct B128GemmArgs {
+  int n_experts = 1, N = 0, K = 0;
+  const void* w = nullptr;            // codes [E][N][K]
+  const float* w_scales = nullptr;    // [E][ceil(N / 128)][ceil(K / 128)]
+  const void* xq = nullptr;           // activation buffer of K (y) or N (dx) columns
+  int64_t nrows = 0;
+  const int32_t* offsets = nullptr;   // [E + 1]; null: every row, expert 0
+  int out_type = 0;
+  void* y = nullptr;                  // [nrows][N], or dx [nrows][K]
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_b128_product(const B128GemmArgs& a);
+cudaError_t launch_b128_grad_x(const B128GemmArgs& a);
+
+struct B128GradWArgs {
+  int type = 0;                       // of dy and x, 16 bits
+  const void* dy = nullptr;
+  int64_t ld_dy = 0;
+  const void* x = nullptr;
+  int64_t ldx = 0;
+  int n_experts = 1, N = 0, K = 0;
+  int64_t nrows = 0;
+  const int32_t* offsets = nullptr;
+  int out_type = 0;
+  void* dw = nullptr;                 // [E][N][K]
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_b128_grad_w(const B128GradWArgs& a);
+
 // A number (0 or more) that is asked of each device once, by the first call
 // that needs it there; host threads may ask at the same time.
 class PerDevice {

@@ -4,75 +4,18 @@
 #include <cmath>
 #include <cstring>
 
-#include <cuda_runtime.h>
-
 #include "../../include/qmv.h"
+#include "qmv_checks.h"
 #include "qmv_internal.h"
 #include "qmv_layout.h"
 
 namespace qmv {
 namespace {
 
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-template <typename... P>
-bool any_null(const P*... p) {
-  return ((p == nullptr) || ...);
-}
-template <typename... P>
-bool any_misaligned(const P*... p) {
-  return (misaligned(p) || ...);
-}
-
-int launched(cudaError_t e, const char* name) {
-  if (e == cudaSuccess) return record_error(QMV_OK, "%s", "");
-  cudaGetLastError();   // clear a non-sticky error so later calls start clean
-  return record_error(QMV_ECUDA, "%s: %s failed: %s (%s)", name, g_launch_stage, cudaGetErrorName(e),
-                      cudaGetErrorString(e));
-}
-int done() { return record_error(QMV_OK, "%s", ""); }
-
 bool mx_shape(int fmt, int64_t nrows, int K) {
   return (fmt == QMV_MXFP4 || fmt == QMV_MXFP8) && nrows >= 0 && nrows <= QMV_MAX_ROWS && K >= 32 && K <= QMV_MAX_K &&
          K % 32 == 0;
 }
-
-int check_type(int type, const char* name) {
-  if (type < QMV_BF16 || type > QMV_F32) return record_error(QMV_EINVAL, "%s: unknown element type %d", name, type);
-  return QMV_OK;
-}
-
-int check_width(int K, bool groups, const char* name, int most = QMV_MAX_K) {
-  if (K < 1 || K > most) return record_error(QMV_ESHAPE, "%s: %d columns outside [1, %d]", name, K, most);
-  if (groups && K % 32) return record_error(QMV_ESHAPE, "%s: %d columns are not a multiple of 32", name, K);
-  return QMV_OK;
-}
-
-int check_ld(int64_t ld, int K, const char* name) {
-  if (ld < K || ld > (int64_t)1 << 40)
-    return record_error(QMV_ESHAPE, "%s: row stride %lld for %d columns", name, (long long)ld, K);
-  return QMV_OK;
-}
-
-int check_rows(int nrows, const char* name) {
-  if (nrows < 0 || nrows > QMV_MAX_ROWS)
-    return record_error(QMV_EINVAL, "%s: %d rows outside [0, %d]", name, nrows, QMV_MAX_ROWS);
-  return QMV_OK;
-}
-
-int check_slots(int ntok, int top_k, const char* name) {
-  if (top_k < 1 || top_k > QMV_MAX_TOPK)
-    return record_error(QMV_EINVAL, "%s: top_k=%d outside [1, %d]", name, top_k, QMV_MAX_TOPK);
-  if (ntok < 0 || (int64_t)ntok * top_k > QMV_MAX_ROWS)
-    return record_error(QMV_EINVAL, "%s: ntok=%d with top_k=%d: at most %d slots", name, ntok, top_k, QMV_MAX_ROWS);
-  return QMV_OK;
-}
-
-#define QMV_TRY(call)             \
-  do {                            \
-    const int rc_ = (call);       \
-    if (rc_ != QMV_OK) return rc_; \
-  } while (0)
 
 // Common checks of the two products; fills `g`.
 int product_args(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq_bytes, int nrows, const int32_t* offsets,
@@ -149,8 +92,6 @@ int return_rows(int type, const void* ys, bool ys_f32, const float* wide, const 
   g_launch_stage = "launch";
   return launched(launch_return(r), name);
 }
-
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The experts' rows between the down product and the weighted sum are kept in
 // fp32 where that is at most this many bytes, so that the layer's output is

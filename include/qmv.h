@@ -590,6 +590,140 @@ int qmv_moe_prefill_layer(const qmv_wdesc* gate_up_desc, const void* w_gate_up_d
                           void* workspace_dev, size_t workspace_bytes, void* y_dev, void* stream);
 
 /*
+ * The router of a MoE layer: the top_k experts of each token by logit, and
+ * their weights. logits [ntok][n_experts] of element type `type`, rows ldl
+ * elements apart (float32 logits keep the order that 16-bit ones may round away).
+ *   score QMV_SCORE_SOFTMAX  s = softmax over all experts
+ *         QMV_SCORE_SIGMOID  s = 1 / (1 + exp(-logit)), each expert its own
+ *   ids [ntok][top_k]        largest logit first, of equal ones the lowest expert
+ *   weights [ntok][top_k]    fp32: scale * s, or with renorm != 0 scale * s over
+ *                            the sum of the chosen s
+ * ids and weights are what the calls above take. live_dev (may be NULL): one
+ * byte a token, 0 for padding, whose ids are -1 and weights 0 (dropped slots).
+ * A logit of -infinity is an expert that is not there; slots for which none is
+ * left have id -1 and weight 0. A row with a NaN (softmax: or +infinity) gets the
+ * experts 0 .. top_k - 1 with weights of NaN. top_k at most n_experts, n_experts at most
+ * QMV_MAX_SORT_EXPERTS. One launch.
+ * Errors: QMV_EINVAL (also a scale that is not finite), QMV_ESHAPE, QMV_EALIGN, QMV_ECUDA.
+ */
+typedef enum { QMV_SCORE_SOFTMAX = 0, QMV_SCORE_SIGMOID = 1 } qmv_score;
+int qmv_moe_router(int32_t type, const void* logits_dev, int64_t ldl, const uint8_t* live_dev, int32_t ntok,
+                   int32_t n_experts, int32_t top_k, int32_t score, int32_t renorm, float scale, int32_t* ids_dev,
+                   float* weights_dev, void* stream);
+
+/*
+ * The balance loss of a batch, and the slots of each expert. With T the live
+ * tokens (those with a logit above -infinity, and not padding), n_e their slots
+ * with id e (ids [ntok][top_k]; ids outside [0, n_experts) count nowhere) and
+ * p_te the token's scores as shares of their sum (softmax as it is),
+ *   loss = n_experts * sum_e f_e P_e,   f_e = n_e / (top_k T),   P_e = 1/T sum_t p_te
+ * (1 for slots and shares spread evenly; 0 without a live token).
+ *   counts [n_experts + 1]   int32: n_e, and T in the last
+ *   means [n_experts]        fp32: P_e
+ *   loss [1]                 fp32
+ * Sums are fp32 in a fixed order. A call without tokens writes zeros.
+ * workspace: qmv_moe_balance_workspace_bytes(...) bytes of device scratch; calls that
+ * share one must be ordered on one stream. Two launches.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+size_t qmv_moe_balance_workspace_bytes(int32_t ntok, int32_t n_experts);
+int qmv_moe_balance(int32_t type, const void* logits_dev, int64_t ldl, const uint8_t* live_dev, const int32_t* ids_dev,
+                    int32_t ntok, int32_t n_experts, int32_t top_k, int32_t score, int32_t* counts_dev, float* means_dev,
+                    float* loss_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of both with respect to the logits:
+ *   dlogits [ntok][n_experts] (`type`, rows ldd apart) =
+ *       sum_j dweights[t][j] * d weights[t][j] / d logits + dloss * d loss / d logits
+ * The choice of experts (ids as qmv_moe_router gave them) and the fractions f_e
+ * are constants; slots whose id is outside [0, n_experts) take no part, an expert
+ * that is named twice takes both slots'. dweights_dev fp32 [ntok][top_k], or NULL for the loss
+ * alone; counts_dev as qmv_moe_balance gave them and dloss_dev fp32 [1], or both
+ * NULL for the weights alone. Padding's rows are zero; a row with a NaN (softmax:
+ * or +infinity) among its logits is NaN. live, score, renorm and scale as in
+ * the calls above. fp32 until it is stored; one launch.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ECUDA.
+ */
+int qmv_moe_router_grad(int32_t type, const void* logits_dev, int64_t ldl, const uint8_t* live_dev, const int32_t* ids_dev,
+                        const float* dweights_dev, const int32_t* counts_dev, const float* dloss_dev, int32_t ntok,
+                        int32_t n_experts, int32_t top_k, int32_t score, int32_t renorm, float scale, void* dlogits_dev,
+                        int64_t ldd, void* stream);
+
+/*
+ * E4M3 with one fp32 scale for each block of 128, the other 8-bit form that
+ * checkpoints come in: weights with a scale per 128 x 128, activations with one
+ * per row and 128 columns. Quantization, in fp32, of a block with the largest magnitude m:
+ *   a = max(m, 2^-116),   scale = a / 448,   code = E4M3(x * (448 / a)),
+ * each operation rounded to nearest even. A block with an infinity or a NaN has
+ * the scale NaN and codes 0, so that its products are NaN.
+ *
+ * Weights need no packer: codes [n_experts][N][K], scales fp32
+ * [n_experts][ceil(N / 128)][ceil(K / 128)], row-major as they are stored. K a
+ * multiple of 16, N any; the last blocks may be smaller.
+ * Activation buffer: the codes, row after row, each row padded to a multiple of
+ * 16 bytes with zeros; at qmv_act_b128_scale_offset bytes the scales, fp32
+ * [ceil(K / 128)][nrows]. K any, up to QMV_MAX_N.
+ * The size functions return 0 for an invalid shape.
+ */
+size_t qmv_act_b128_bytes(int32_t nrows, int32_t K);
+size_t qmv_act_b128_scale_offset(int32_t nrows, int32_t K);
+
+/* Host helper: split such a buffer (host copy) into codes [nrows][K] and scales [nrows][ceil(K / 128)]. */
+int qmv_act_b128_unpack(const void* xq_host, int32_t nrows, int32_t K, uint8_t* codes_host, float* scales_host);
+
+/*
+ * Quantize rows x_dev [nrows][K] (`type`, ldx apart) to such a buffer, and
+ * weights w_dev [n_experts][N][K] (`type`, contiguous) to codes and scales.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+int qmv_quantize_act_b128(int32_t type, const void* x_dev, int64_t ldx, int32_t nrows, int32_t K, void* xq_dev,
+                          size_t xq_bytes, void* stream);
+int qmv_quantize_weights_b128(int32_t type, const void* w_dev, int32_t n_experts, int32_t N, int32_t K, void* codes_dev,
+                              float* scales_dev, void* stream);
+
+/*
+ * Product of such operands on the tensor cores:
+ *   y[r][n] = sum_b sx[r][b] * sw[n / 128][b] * sum_{k in block b} q[r][k] * w[n][k]
+ * The sum over a block of 128 is the tensor cores' (fp32, truncating); blocks are scaled
+ * and added in fp32. xq_dev: an activation buffer of K columns (xq_bytes: its size).
+ * y_dev: out_type [nrows][N]. offsets_dev as in qmv_mx_product: NULL for a dense
+ * product (n_experts 1), or int32 [n_experts + 1] for rows grouped by expert; rows
+ * of no expert are not written. Any number of rows, from a decode token on.
+ * Scales may be any fp32; where the product of two leaves fp32's range, so do y's terms.
+ *
+ * qmv_b128_linear quantizes rows x (`type`, ldx apart) and multiplies: y has the
+ * type of x. workspace: qmv_b128_linear_workspace_bytes(...) bytes of device
+ * scratch; calls that share one must be ordered on one stream.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+int qmv_b128_product(const void* w_dev, const float* w_scales_dev, int32_t n_experts, int32_t N, int32_t K,
+                     const void* xq_dev, size_t xq_bytes, int32_t nrows, const int32_t* offsets_dev, int32_t out_type,
+                     void* y_dev, void* stream);
+size_t qmv_b128_linear_workspace_bytes(int32_t nrows, int32_t K);
+int qmv_b128_linear(const void* w_dev, const float* w_scales_dev, int32_t n_experts, int32_t N, int32_t K, int32_t type,
+                    const void* x_dev, int64_t ldx, int32_t nrows, const int32_t* offsets_dev, void* workspace_dev,
+                    size_t workspace_bytes, void* y_dev, void* stream);
+
+/*
+ * Gradients of the product, the quantizations taken as they are (straight through):
+ *   qmv_b128_grad_x  dx[r][k] = sum_n Q(dy)[r][n] * W[n][k], from the same weights; dyq_dev an
+ *                    activation buffer of N columns (qmv_quantize_act_b128 of dy);
+ *                    dx out_type [nrows][K]; rows of no expert are not written
+ *   qmv_b128_grad_w  dW[e][n][k] = sum over e's rows r of dy[r][n] * x[r][k], of the
+ *                    16-bit dy and x themselves (`type`: bf16 or fp16; rows ld_dy and ldx
+ *                    apart, multiples of 8 elements): dw out_type [n_experts][N][K]. The
+ *                    matrix of an expert without rows is zero.
+ * offsets_dev as above. Sums are fp32.
+ * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
+ */
+int qmv_b128_grad_x(const void* w_dev, const float* w_scales_dev, int32_t n_experts, int32_t N, int32_t K,
+                    const void* dyq_dev, size_t dyq_bytes, int32_t nrows, const int32_t* offsets_dev, int32_t out_type,
+                    void* dx_dev, void* stream);
+int qmv_b128_grad_w(int32_t type, const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ldx, int32_t n_experts,
+                    int32_t N, int32_t K, int32_t nrows, const int32_t* offsets_dev, int32_t out_type, void* dw_dev,
+                    void* stream);
+
+/*
  * SwiGLU between the gate/up and down gathers of a gpt-oss-style MoE layer:
  * h[i] = silu(g[i]) * u[i], silu(z) = z / (1 + exp(-z)), bf16 in and out,
  * fp32 arithmetic, n elements ("perf(rocm): add an mxfp4 arm ...", "Problem /
