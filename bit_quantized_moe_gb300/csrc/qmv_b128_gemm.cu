@@ -1,139 +1,640 @@
 // qmv_b128_gemm.cu -- products of E4M3 operands with fp32 scales of 128 columns
-// (rows) and blocks of 128 x 128 (weights), and their gradients:
+// (rows) and blocks of 128 x 128 (weights), and their gradients, over many rows
+// on the tcgen05 tensor cores:
 //
 //   y[r][n]     = sum_b sx[r][b] sw[n / 128][b] sum_{k in b} q[r][k] w[n][k]
 //   dx[r][k]    = sum_b sd[r][b] sw[b][k / 128] sum_{n in b} d[r][n] w[n][k]
 //   dW[e][n][k] = sum over e's rows r of dy[r][n] x[r][k]
 //
-// One CTA an output tile of 64 x 64, its operands decoded to fp32 in shared
-// memory, a thread 4 x 4 outputs.
+// A pair of CTAs on two SMs takes an output tile of 256 x 256: each holds 128
+// rows of one operand and half of the other in shared memory, 128 bytes of
+// depth a step (128 codes, a block; 64 of the 16-bit numbers of dW), and 128 x
+// 256 sums in its tensor memory. A step's MMAs start from zero, so that its sum
+// can take its scales: the epilogue's threads, a row and 128 columns each, read
+// it from tensor memory (two steps fit) and add it, scaled, to fp32 sums in
+// registers. The scale is one number for a thread's 128 columns: its row's
+// times its block's. dW takes the same way with a scale of 1: no sum in the
+// tensor cores, which truncate where they add, is longer than 64 rows.
+//
+// Operands whose depth is contiguous (rows in y and dx, weights in y) lie in shared
+// memory as rows of 128 bytes, swizzled; the others (weights in dx, both in dW)
+// as 128 bytes of outputs at each depth, which the tensor core reads transposed:
+// no operand is transposed in memory, and one copy of the weights serves both products.
+//
+// Warps: 0 issues the TMA copies, 1 (of the pair's first CTA) the MMAs, 2 clears
+// the rows behind an expert's last one (dW), 4..11 are the epilogue.
+#include <cmath>
+
 #include "qmv_internal.h"
 #include "qmv_rows.cuh"
+#include "qmv_tc.cuh"
 
 namespace qmv {
 
-constexpr int kTile = 64, kDepth = 16;
+enum : int { kModeY = 0, kModeDx = 1, kModeDw = 2 };
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
-  uint32_t h[2];
-  e4m3x4_to_f16x2(c, h);
-  return __half2float(__ushort_as_half((unsigned short)(h[0] & 0xffffu)));
+constexpr int kHalf = 128;             // rows, and columns of the other operand, of one CTA
+constexpr int kPairTile = 2 * kHalf;
+constexpr int kPairThreads = 384;
+constexpr int kPairStages = 6;
+constexpr uint32_t kOperandBytes = kHalf * 128;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr int kEpiWarps = 8;           // a CTA's
+constexpr int kParkCols16 = 16;        // columns that a warp turns round at once, where rows are not of whole 16 bytes
+constexpr uint32_t kParkBytes = kEpiWarps * 32 * (kParkCols16 + 1) * 4;
+constexpr size_t pair_smem(int n_experts) {
+  return 1024 + (size_t)kPairStages * kStageBytes + kParkBytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
+}
+static_assert(pair_smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
+// Registers of an epilogue thread and of the others: 256 * 216 + 128 * 72 = 384 * 168, what the launch gives.
+#define QMV_EPI_REGS 216
+#define QMV_OTHER_REGS 72
+
+struct PairParams {
+  const float* sx;            // scales of the rows [blocks of depth][nrows]
+  const float* sw;            // scales of the weights [E][ceil(N / 128)][ceil(K / 128)]
+  const int32_t* offsets;
+  void* y;
+  int64_t nrows;
+  int n_experts, N, K;
+  int out_n;                  // columns of the output
+  int out_type, store_bytes;  // widest store that the output's rows allow: 32, 16, or 0
+  int steps;                  // y, dx: of depth
+  int n_tiles, m_tiles;       // column tiles; dW: row tiles of a matrix
+};
+
+template <int MODE, bool F16>
+__device__ __forceinline__ constexpr uint32_t pair_idesc() {
+  return (1u << 4) | (MODE == kModeDw && !F16 ? (1u << 7) | (1u << 10) : 0u) | (MODE == kModeDw ? 1u << 15 : 0u) |
+         (MODE != kModeY ? 1u << 16 : 0u) | ((uint32_t)(kPairTile >> 3) << 17) | ((uint32_t)(kPairTile >> 4) << 24);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_one(void* y, int64_t at, float v) {
-  static_cast<T*>(y)[at] = from_f32<T>(v);
-}
-__device__ __forceinline__ void store_as(int type, void* y, int64_t at, float v) {
-  if (type == QMV_BF16) store_one<__nv_bfloat16>(y, at, v);
-  else if (type == QMV_F16) store_one<__half>(y, at, v);
-  else store_one<float>(y, at, v);
+// Operand read transposed: 128 bytes of outputs at each depth, swizzled, eight
+// depths every 1024 bytes; the next 128 bytes of outputs `panel` bytes on.
+__device__ __forceinline__ uint64_t transposed_desc(uint32_t addr, uint32_t panel) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Rows of expert e of the call; an offset below an earlier one counts as it.
-__device__ __forceinline__ void expert_rows(const int32_t* offsets, int nrows, int e, int& lo, int& hi) {
-  if (offsets == nullptr) {
-    lo = 0;
-    hi = nrows;
-    return;
+template <int MODE>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (MODE == kModeDw) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+  } else {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
   }
-  lo = 0;
-  for (int i = 0; i <= e; ++i) lo = max(lo, min(offsets[i], nrows));
-  hi = max(lo, min(offsets[e + 1], nrows));
 }
 
-// A: [M][D] and B: [C][D] as functions of (row, depth); out of (row, column).
-template <typename A, typename B, typename O>
-__device__ __forceinline__ void tile_product(int m0, int M, int c0, int C, int D, A&& fa, B&& fb, O&& out) {
-  __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-  float acc[4][4] = {};
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  for (int d0 = 0; d0 < D; d0 += kDepth) {
-    for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-      const int d = i % kDepth, r = i / kDepth;
-      sa[d][r] = m0 + r < M && d0 + d < D ? fa(m0 + r, d0 + d) : 0.0f;
-      sb[d][r] = c0 + r < C && d0 + d < D ? fb(c0 + r, d0 + d) : 0.0f;
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+// An arrival, with bytes to wait for, at a barrier of the cluster.
+__device__ __forceinline__ void mbar_expect_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// 16 accumulator columns of this thread's row; not used before tmem_ld_wait16.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
+}
+
+// Two fp32 sums in one register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Two numbers of 16 bits in a word.
+template <typename T>
+__device__ __forceinline__ uint32_t two16(float a, float b) {
+  const T lo = from_f32<T>(a), hi = from_f32<T>(b);
+  return (uint32_t) * reinterpret_cast<const unsigned short*>(&lo) | (uint32_t) * reinterpret_cast<const unsigned short*>(&hi) << 16;
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8], int bytes) {
+  if (bytes == 32) {
+    store32(p, w);
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// 16 columns of a row from n0 on, where the row's stores may be `bytes` wide
+// and its columns end on such a boundary.
+__device__ __forceinline__ void store16(const PairParams& p, int64_t row, int n0, const float (&v)[16]) {
+  const int64_t at = row * p.out_n + n0;
+  if (p.out_type == QMV_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (n0 + 8 * h >= p.out_n) break;
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+      float* out = static_cast<float*>(p.y) + at + 8 * h;
+      if (n0 + 8 * h + 8 <= p.out_n) store_words(out, w, p.store_bytes);
+      else *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);   // half a piece: 16-byte rows
     }
-    __syncthreads();
+  } else {
+    uint32_t w[8];
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
+    for (int i = 0; i < 8; ++i) {
+      w[i] = p.out_type == QMV_BF16 ? two16<__nv_bfloat16>(v[2 * i], v[2 * i + 1]) : two16<__half>(v[2 * i], v[2 * i + 1]);
+    }
+    uint16_t* out = static_cast<uint16_t*>(p.y) + at;
+    if (n0 + 16 <= p.out_n) store_words(out, w, p.store_bytes);
+    else *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Sixteen columns of a warp's 32 rows, turned round in shared memory, so that
+// neighbouring lanes store neighbouring elements: rows that start anywhere.
+__device__ __forceinline__ void store_turned(const PairParams& p, float* park, int64_t row0, int rows, int n0, int lane,
+                                             const float (&v)[16]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 16; ++i) park[lane * (kParkCols16 + 1) + i] = v[i];
+  __syncwarp();
+  const int c = lane & 15;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + lane / 16;
+    if (r < rows && n0 + c < p.out_n) {
+      const float x = park[r * (kParkCols16 + 1) + c];
+      const int64_t at = (row0 + r) * p.out_n + n0 + c;
+      if (p.out_type == QMV_BF16) static_cast<__nv_bfloat16*>(p.y)[at] = from_f32<__nv_bfloat16>(x);
+      else if (p.out_type == QMV_F16) static_cast<__half*>(p.y)[at] = from_f32<__half>(x);
+      else static_cast<float*>(p.y)[at] = x;
+    }
+  }
+  __syncwarp();
+}
+
+// What a CTA does of one output tile.
+struct PairTile {
+  int expert;
+  int row0, rows;    // y, dx: its first row, and rows from there on; dW: the expert's
+  int m, n;          // dW: first row of the matrix; first column of the pair
+  int steps;
+};
+
+template <int MODE>
+__device__ __forceinline__ PairTile pair_tile(int t, const PairParams& p, const int* first_tile, const int* first_row, int rank) {
+  PairTile r;
+  if constexpr (MODE == kModeDw) {
+    const int each = p.m_tiles * p.n_tiles;
+    r.expert = t / each;
+    const int i = t - r.expert * each;
+    r.n = i / p.m_tiles;
+    r.m = (i - r.n * p.m_tiles) * kPairTile + rank * kHalf;
+    r.n *= kPairTile;
+    r.row0 = first_row[r.expert];
+    r.rows = first_row[r.expert + 1] - r.row0;
+    r.steps = (r.rows + 63) / 64;
+  } else {
+    int lo = 0, hi = p.n_experts - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (first_tile[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    const int rows = first_row[lo + 1] - first_row[lo];
+    const int mt = (rows + kPairTile - 1) / kPairTile;
+    const int i = t - first_tile[lo];
+    r.expert = lo;
+    r.n = i / mt;
+    const int m = (i - r.n * mt) * kPairTile + rank * kHalf;
+    r.n *= kPairTile;
+    r.m = 0;
+    r.row0 = first_row[lo] + m;
+    r.rows = rows - m;
+    r.steps = p.steps;
+  }
+  return r;
+}
+
+template <int MODE, bool F16>
+__global__ void __launch_bounds__(kPairThreads, 1)
+b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ PairParams p) {
+  constexpr int kStages = kPairStages;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+  float* park = reinterpret_cast<float*>(stages + kStages * kStageBytes);
+  int* first_tile = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(park) + kParkBytes);   // [n_experts + 1]
+  int* first_row = first_tile + p.n_experts + 1;                                             // [n_experts + 1]
+  // Barriers. full (the first CTA's): a step's copies of both CTAs have arrived; empty: its MMAs are complete;
+  // acc_full, acc_empty (the first CTA's): a sum in tensor memory is there, has been read by both CTAs; tail: dW, this
+  // CTA's copies of a step that is an expert's last, ragged one.
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], tail[kStages], done;
+  __shared__ uint32_t tmem_base;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&full[i]), 2);
+      mbar_init(smem_addr(&empty[i]), 1);
+      mbar_init(smem_addr(&tail[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&acc_full[i]), 1);
+      mbar_init(smem_addr(&acc_empty[i]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_addr(&done), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(&tmem_base)),
+                 "r"(2u * kPairTile) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  pdl_wait();
+  if (warp == 0) expert_tiles(p.offsets, (int)p.nrows, p.n_experts, kPairTile, p.n_tiles, lane, first_row, first_tile);
+  tc_before_sync();
+  __syncthreads();
+  cluster_sync_all();   // both CTAs' barriers exist
+  tc_after_sync();
+  const uint32_t tmem = tmem_base;
+  const int tiles = MODE == kModeDw ? p.n_experts * p.m_tiles * p.n_tiles : first_tile[p.n_experts];
+  const int t0 = (int)blockIdx.x / 2, dt = (int)gridDim.x / 2;
+  bool ok = true;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(QMV_OTHER_REGS));
+    const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
+    const auto tile_of = [&](int t) {   // the same in all lanes, and known to be
+      PairTile r = pair_tile<MODE>(t, p, first_tile, first_row, rank);
+      r.expert = __shfl_sync(0xffffffffu, r.expert, 0);
+      r.row0 = __shfl_sync(0xffffffffu, r.row0, 0);
+      r.rows = __shfl_sync(0xffffffffu, r.rows, 0);
+      r.m = __shfl_sync(0xffffffffu, r.m, 0);
+      r.n = __shfl_sync(0xffffffffu, r.n, 0);
+      r.steps = __shfl_sync(0xffffffffu, r.steps, 0);
+      return r;
+    };
+    if (warp == 0) {
+      // ---- copies
+      const uint32_t data0 = smem_addr(stages);
+      int it = 0, st = 0;
+      for (int i = 0; i < my_tiles && ok; ++i) {
+        const PairTile tile = tile_of(t0 + i * dt);
+        // boxes of 64 rows that have a live one; rows that are not copied keep what the stage held, and are not stored
+        const int copies = max(0, min(tile.rows, kHalf) + 63) / 64;
+        for (int s = 0; s < tile.steps; ++s, ++it) {
+          if (it >= kStages && !__all_sync(0xffffffffu, wait_for<true>(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1))) {
+            ok = false;
+            break;
+          }
+          const uint32_t a = data0 + (uint32_t)st * kStageBytes, b = a + kOperandBytes;
+          const uint32_t lead = leader_addr(smem_addr(&full[st]));
+          if (elect_one()) {
+            if constexpr (MODE == kModeDw) {
+              // two panels of 64 outputs x 64 rows each
+              const int row = tile.row0 + 64 * s, x0 = (tile.m) * 2, y0 = (tile.n + rank * kHalf) * 2;
+              if (tile.rows - 64 * s >= 64) {
+                mbar_expect_cluster(lead, kStageBytes);
+                tma_load_2d<true>(a, &map_a, x0, row, lead);
+                tma_load_2d<true>(a + kOperandBytes / 2, &map_a, x0 + 128, row, lead);
+                tma_load_2d<true>(b, &map_b, y0, row, lead);
+                tma_load_2d<true>(b + kOperandBytes / 2, &map_b, y0 + 128, row, lead);
+              } else {   // rows of the next expert come too: warp 2 clears them, then arrives
+                const uint32_t mine = smem_addr(&tail[st]);
+                mbar_arrive_expect_tx(mine, kStageBytes);
+                tma_load_2d<false>(a, &map_a, x0, row, mine);
+                tma_load_2d<false>(a + kOperandBytes / 2, &map_a, x0 + 128, row, mine);
+                tma_load_2d<false>(b, &map_b, y0, row, mine);
+                tma_load_2d<false>(b + kOperandBytes / 2, &map_b, y0 + 128, row, mine);
+              }
+            } else {
+              mbar_expect_cluster(lead, (uint32_t)copies * 64 * 128 + kOperandBytes);
+              for (int c = 0; c < copies; ++c) tma_load_2d<true>(a + c * 64 * 128, &map_a, s * 128, tile.row0 + 64 * c, lead);
+              if constexpr (MODE == kModeY) tma_load_3d_pair(b, &map_b, s * 128, tile.n + rank * kHalf, tile.expert, lead);
+              else tma_load_3d_pair(b, &map_b, tile.n + rank * kHalf, s * 128, tile.expert, lead);
+            }
+          }
+          __syncwarp();
+          if (++st == kStages) st = 0;
+        }
+      }
+      if (!ok) {   // leave no copy in flight: they report to the first CTA, so give them their time
+        const unsigned long long from = global_timer_ns();
+        while (global_timer_ns() - from < kDrainLimitNs) {}
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---- products; the same in all lanes, one issues
+      const uint32_t data0 = smem_addr(stages);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      constexpr uint32_t idesc = pair_idesc<MODE, F16>();
+      int it = 0, st = 0;
+      uint32_t st_phase = 0;
+      for (int i = 0; i < my_tiles && ok; ++i) {
+        const int steps = tile_of(t0 + i * dt).steps;
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int acc = it & 1;
+          if (!__all_sync(0xffffffffu, wait_for<true>(smem_addr(&acc_empty[acc]), ((it >> 1) & 1) ^ 1)) ||
+              !__all_sync(0xffffffffu, wait_for<true>(smem_addr(&full[st]), st_phase))) {
+            ok = false;
+            break;
+          }
+          tc_after_sync();
+          const uint32_t a = data0 + (uint32_t)st * kStageBytes, b = a + kOperandBytes;
+          const uint32_t d = tm + (uint32_t)(acc * kPairTile);
+          if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[d][ty * 4 + i], sb[d][tx * 4 + j], acc[i][j]);
+            for (int j = 0; j < 4; ++j) {   // 32 bytes of depth each; transposed: 32 or 16 depths
+              uint64_t da, db;
+              if constexpr (MODE == kModeDw) {
+                da = transposed_desc(a + j * 16 * 128, kOperandBytes / 2);
+                db = transposed_desc(b + j * 16 * 128, kOperandBytes / 2);
+              } else {
+                da = operand_desc(a + j * 32);
+                db = MODE == kModeY ? operand_desc(b + j * 32) : transposed_desc(b + j * 32 * 128, 1024);
+              }
+              pair_mma<MODE>(d, da, db, idesc, j > 0 ? 1u : 0u);
+            }
+            mma_commit_to<true>(smem_addr(&empty[st]));
+            mma_commit_to<true>(smem_addr(&acc_full[acc]));
+          }
+          __syncwarp();
+          if (++st == kStages) {
+            st = 0;
+            st_phase ^= 1;
+          }
+        }
+      }
+      if (elect_one()) mma_commit_to<true>(smem_addr(&done));
+      __syncwarp();
+      if (!wait_for<true>(smem_addr(&done), 0)) ok = false;
+    } else if (warp == 2 && MODE == kModeDw) {
+      // ---- the rows behind an expert's last one, cleared in both operands (0 times a NaN is one)
+      int it = 0;
+      uint32_t phases = 0;   // bit st: of tail[st]
+      for (int i = 0; i < my_tiles && ok; ++i) {
+        const PairTile tile = tile_of(t0 + i * dt);
+        it += tile.steps;
+        const int valid = tile.rows - 64 * (tile.steps - 1);
+        if (tile.steps == 0 || valid == 64) continue;
+        const int st = (it - 1) % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&tail[st]), (phases >> st) & 1, kWaitLimitNs))) {
+          ok = false;
+          break;
+        }
+        phases ^= 1u << st;
+        uint8_t* at = stages + (uint32_t)st * kStageBytes;
+        // four panels of 64 rows of 128 bytes
+        for (int j = lane; j < 4 * (64 - valid) * 8; j += 32) {
+          const int piece = j & 7, r = j / 8;
+          const int panel = r / (64 - valid), row = valid + r - panel * (64 - valid);
+          reinterpret_cast<uint4*>(at + panel * (kOperandBytes / 2) + row * 128)[piece] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_addr(smem_addr(&full[st])));
       }
     }
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i) {
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, c = c0 + tx * 4 + j;
-      if (m < M && c < C) out(m, c, acc[i][j]);
+  } else {
+    // ---- epilogue: thread = row 32 (warp % 4) + lane, columns 128 * half on
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(QMV_EPI_REGS));
+    const int quad = warp % 4, half = (warp - 4) / 4;
+    const int r = quad * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    float* my_park = park + (warp - 4) * 32 * (kParkCols16 + 1);
+    const int k_blocks = b128_blocks(p.K), n_blocks = b128_blocks(p.N);
+    int it = 0;
+    for (int t = t0; t < tiles && ok; t += dt) {
+      const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
+      const int n0 = tile.n + half * kHalf;   // first column of this thread
+      // the scales: one of the row and one of the weights' block a step, asked for a step ahead
+      const float* sx = nullptr;
+      const float* sw = nullptr;
+      int64_t sw_stride = 0;
+      float next_x = 1.0f, next_w = 1.0f;
+      if constexpr (MODE != kModeDw) {
+        const int64_t row = min((int64_t)tile.row0 + r, p.nrows - 1);
+        sx = p.sx + row;
+        const float* base = p.sw + (int64_t)tile.expert * n_blocks * k_blocks;
+        const int block = min(n0 / kB128, (MODE == kModeY ? n_blocks : k_blocks) - 1);
+        sw = MODE == kModeY ? base + (int64_t)block * k_blocks : base + block;
+        sw_stride = MODE == kModeY ? 1 : k_blocks;
+        next_x = *sx;
+        next_w = *sw;
+      }
+      uint64_t sum[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) sum[i] = 0;
+      for (int s = 0; s < tile.steps; ++s, ++it) {
+        const int acc = it & 1;
+        const float scale = next_x * next_w;
+        if constexpr (MODE != kModeDw) {
+          if (s + 1 < tile.steps) {
+            next_x = sx[(int64_t)(s + 1) * p.nrows];
+            next_w = sw[(s + 1) * sw_stride];
+          }
+        }
+        if (!__all_sync(0xffffffffu, wait_for<true>(smem_addr(&acc_full[acc]), (it >> 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_after_sync();
+        const uint64_t scale2 = pack2(scale, scale);
+        const uint32_t d = tmem + (uint32_t)(acc * kPairTile + half * kHalf) + lanes;
+        // one load under way while the one before is added
+        uint32_t v[2][16];
+        tmem_ld16(d, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          tmem_ld_wait16(v[c & 1]);
+          if (c < 7) tmem_ld16(d + 16 * (c + 1), v[(c + 1) & 1]);
+          if (c == 7) {   // read
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_addr(smem_addr(&acc_empty[acc])));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t part = pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
+            if constexpr (MODE == kModeDw) sum[8 * c + i] = add2(sum[8 * c + i], part);
+            else sum[8 * c + i] = fma2(part, scale2, sum[8 * c + i]);
+          }
+        }
+      }
+      if (!ok) break;
+      const int64_t row0 = MODE == kModeDw ? (int64_t)tile.expert * p.N + tile.m : (int64_t)tile.row0;   // of the CTA
+      const int rows = MODE == kModeDw ? p.N - tile.m : tile.rows;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int n = n0 + 16 * c;
+        if (n >= p.out_n) break;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) unpack2(sum[8 * c + i], v[2 * i], v[2 * i + 1]);
+        if (p.store_bytes != 0) {
+          if (r < rows) store16(p, row0 + r, n, v);
+        } else {
+          store_turned(p, my_park, row0 + quad * 32, rows - quad * 32, n, lane, v);
+        }
+      }
     }
+    // the first CTA's last arrivals have reached this one before it may exit
+    if (ok && !wait_for<true>(smem_addr(&done), 0)) ok = false;
+  }
+  if (!ok && lane == 0) set_status(kStatusWaitTile);
+  __syncwarp();
+  pdl_launch_dependents();
+  tc_before_sync();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA's memory is in use by the other any more
+  if (warp == 1) {
+    tc_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(2u * kPairTile));
   }
 }
 
-template <bool GRAD>
-__global__ void __launch_bounds__(256) b128_product_kernel(B128GemmArgs a) {
-  pdl_wait();
-  const int D = GRAD ? a.N : a.K, C = GRAD ? a.K : a.N;
-  const int e = blockIdx.z;
-  int lo, hi;
-  expert_rows(a.offsets, (int)a.nrows, e, lo, hi);
-  const int m0 = blockIdx.y * kTile;
-  if (m0 < hi - lo) {
-    const uint8_t* q = static_cast<const uint8_t*>(a.xq);
-    const float* sx = reinterpret_cast<const float*>(q + b128_scale_offset(a.nrows, D));
-    const uint64_t row = b128_row_bytes(D);
-    const uint8_t* w = static_cast<const uint8_t*>(a.w) + (int64_t)e * a.N * a.K;
-    const int kb = b128_blocks(a.K);
-    const float* sw = a.w_scales + (int64_t)e * b128_blocks(a.N) * kb;
-    tile_product(
-        m0, hi - lo, blockIdx.x * kTile, C, D,
-        [&](int r, int d) { return e4m3_to_f32(q[(uint64_t)(lo + r) * row + d]) * sx[(int64_t)(d / kB128) * a.nrows + lo + r]; },
-        [&](int c, int d) {
-          const int n = GRAD ? d : c, k = GRAD ? c : d;
-          return e4m3_to_f32(w[(int64_t)n * a.K + k]) * sw[n / kB128 * kb + k / kB128];
-        },
-        [&](int r, int c, float v) { store_as(a.out_type, a.y, (int64_t)(lo + r) * C + c, v); });
-  }
-  pdl_launch_dependents();
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) b128_grad_w_kernel(B128GradWArgs a) {
-  pdl_wait();
-  const int e = blockIdx.z;
-  int lo, hi;
-  expert_rows(a.offsets, (int)a.nrows, e, lo, hi);
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* x = static_cast<const T*>(a.x);
-  tile_product(
-      blockIdx.y * kTile, a.N, blockIdx.x * kTile, a.K, hi - lo,
-      [&](int n, int r) { return to_f32(dy[(int64_t)(lo + r) * a.ld_dy + n]); },
-      [&](int k, int r) { return to_f32(x[(int64_t)(lo + r) * a.ldx + k]); },
-      [&](int n, int k, float v) { store_as(a.out_type, a.dw, ((int64_t)e * a.N + n) * a.K + k, v); });
-  pdl_launch_dependents();
-}
+QMV_DEFINE_STATUS_ACCESSOR(status_b128_gemm)
 
 namespace {
 
-unsigned tiles_of(int64_t n) { return (unsigned)((n + kTile - 1) / kTile); }
+template <int MODE, bool F16>
+cudaError_t pair_go(PairParams& p, int64_t tiles, const void* a, uint64_t a_bytes, uint64_t a_stride, const void* b,
+                    uint64_t b_bytes, uint64_t b_stride, cudaStream_t stream) {
+  auto* kernel = b128_pair_kernel<MODE, F16>;
+  // The most that any call asks for (the attribute is the function's), and before the tensor maps: it makes the device's
+  // context current on a host thread whose first CUDA call this is.
+  g_launch_stage = "cudaFuncSetAttribute";
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem(QMV_MAX_SORT_EXPERTS));
+  if (e != cudaSuccess) return e;
+  g_launch_stage = "cuTensorMapEncodeTiled";
+  if (encode_fn() == nullptr) return cudaErrorNotSupported;
+  CUtensorMap ma, mb;
+  {
+    const cuuint64_t dims[2] = {a_bytes, (cuuint64_t)p.nrows}, strides[1] = {a_stride};
+    const cuuint32_t box[2] = {128, 64};
+    if (!encode(&ma, 2, a, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  if constexpr (MODE == kModeDw) {
+    const cuuint64_t dims[2] = {b_bytes, (cuuint64_t)p.nrows}, strides[1] = {b_stride};
+    const cuuint32_t box[2] = {128, 64};
+    if (!encode(&mb, 2, b, dims, strides, box)) return cudaErrorInvalidValue;
+  } else {
+    const cuuint64_t dims[3] = {b_bytes, (cuuint64_t)p.N, (cuuint64_t)p.n_experts};
+    const cuuint64_t strides[2] = {b_stride, b_stride * (cuuint64_t)p.N};
+    const cuuint32_t box[3] = {128, 128, 1};
+    if (!encode(&mb, 3, b, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  const uint64_t row = (uint64_t)p.out_n * (p.out_type == QMV_F32 ? 4 : 2), at = reinterpret_cast<uintptr_t>(p.y);
+  p.store_bytes = (row | at) % 32 == 0 ? 32 : (row % 16 == 0 ? 16 : 0);
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = pair_smem(p.n_experts);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // no more pairs than run at once
+  static PerDevice pairs;
+  int most = 0;
+  g_launch_stage = "cudaOccupancyMaxActiveClusters";
+  e = pairs.get(&most, [&](int* n) {
+    cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2));
+    return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  });
+  if (e != cudaSuccess) return e;
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  g_launch_stage = "launch";
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < most ? tiles : most)));
+  cfg.numAttrs = stream != nullptr ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+}
+
+template <int MODE>
+cudaError_t product_go(const B128GemmArgs& a) {
+  const int depth = MODE == kModeY ? a.K : a.N;
+  PairParams p = {};
+  p.sx = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.xq) + b128_scale_offset(a.nrows, depth));
+  p.sw = a.w_scales;
+  p.offsets = a.offsets;
+  p.y = a.y;
+  p.nrows = a.nrows;
+  p.n_experts = a.n_experts;
+  p.N = a.N;
+  p.K = a.K;
+  p.out_n = MODE == kModeY ? a.N : a.K;
+  p.out_type = a.out_type;
+  p.steps = b128_blocks(depth);
+  p.n_tiles = (p.out_n + kPairTile - 1) / kPairTile;
+  // no more pairs than tiles there can be: every expert has at most one partial row tile
+  const int64_t row_tiles = a.nrows / kPairTile + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);
+  return pair_go<MODE, false>(p, row_tiles * p.n_tiles, a.xq, b128_row_bytes(depth), b128_row_bytes(depth), a.w,
+                              (uint64_t)a.K, (uint64_t)a.K, a.stream);
+}
 
 }  // namespace
 
-cudaError_t launch_b128_product(const B128GemmArgs& a) {
-  return launch_pdl(b128_product_kernel<false>, dim3(tiles_of(a.N), tiles_of(a.nrows), a.n_experts), dim3(256), 0, a.stream, a);
-}
-
-cudaError_t launch_b128_grad_x(const B128GemmArgs& a) {
-  return launch_pdl(b128_product_kernel<true>, dim3(tiles_of(a.K), tiles_of(a.nrows), a.n_experts), dim3(256), 0, a.stream, a);
-}
+cudaError_t launch_b128_product(const B128GemmArgs& a) { return product_go<kModeY>(a); }
+cudaError_t launch_b128_grad_x(const B128GemmArgs& a) { return product_go<kModeDx>(a); }
 
 cudaError_t launch_b128_grad_w(const B128GradWArgs& a) {
-  const dim3 grid(tiles_of(a.K), tiles_of(a.N), a.n_experts);
-  if (a.type == QMV_BF16) return launch_pdl(b128_grad_w_kernel<__nv_bfloat16>, grid, dim3(256), 0, a.stream, a);
-  return launch_pdl(b128_grad_w_kernel<__half>, grid, dim3(256), 0, a.stream, a);
+  PairParams p = {};
+  p.offsets = a.offsets;
+  p.y = a.dw;
+  p.nrows = a.nrows;
+  p.n_experts = a.n_experts;
+  p.N = a.N;
+  p.K = a.K;
+  p.out_n = a.K;
+  p.out_type = a.out_type;
+  p.m_tiles = (a.N + kPairTile - 1) / kPairTile;
+  p.n_tiles = (a.K + kPairTile - 1) / kPairTile;
+  const int64_t tiles = (int64_t)a.n_experts * p.m_tiles * p.n_tiles;
+  const uint64_t ld_dy = (uint64_t)a.ld_dy * 2, ldx = (uint64_t)a.ldx * 2;
+  if (a.type == QMV_F16) {
+    return pair_go<kModeDw, true>(p, tiles, a.dy, (uint64_t)a.N * 2, ld_dy, a.x, (uint64_t)a.K * 2, ldx, a.stream);
+  }
+  return pair_go<kModeDw, false>(p, tiles, a.dy, (uint64_t)a.N * 2, ld_dy, a.x, (uint64_t)a.K * 2, ldx, a.stream);
 }
 
 }  // namespace qmv

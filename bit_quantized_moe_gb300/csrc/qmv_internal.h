@@ -161,6 +161,7 @@ struct MxGemmArgs {
 };
 cudaError_t launch_mx_gemm(const MxGemmArgs& a);
 uint32_t status_mx_gemm(int clear);
+uint32_t status_b128_gemm(int clear);
 
 // The router of a MoE layer (qmv_router.cu). live: null, or 0 for a token that is not there.
 struct RouterArgs {
