@@ -94,9 +94,15 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];"
       :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
-// An arrival, with bytes to wait for, at a barrier of the cluster.
-__device__ __forceinline__ void mbar_expect_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+// Arrivals at a barrier of the cluster that hand over no memory written by
+// threads (copies and tensor memory have their own order): releasing and
+// acquiring at the cluster's scope at every step made the steps four times as
+// long (8192 x 7168 x 7168: 693 us).
+__device__ __forceinline__ void mbar_expect_pair(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 accumulator columns of this thread's row; not used before tmem_ld_wait16.
@@ -318,7 +324,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         // boxes of 64 rows that have a live one; rows that are not copied keep what the stage held, and are not stored
         const int copies = max(0, min(tile.rows, kHalf) + 63) / 64;
         for (int s = 0; s < tile.steps; ++s, ++it) {
-          if (it >= kStages && !__all_sync(0xffffffffu, wait_for<true>(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1))) {
+          if (it >= kStages && !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1))) {
             ok = false;
             break;
           }
@@ -329,7 +335,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
               // two panels of 64 outputs x 64 rows each
               const int row = tile.row0 + 64 * s, x0 = (tile.m) * 2, y0 = (tile.n + rank * kHalf) * 2;
               if (tile.rows - 64 * s >= 64) {
-                mbar_expect_cluster(lead, kStageBytes);
+                mbar_expect_pair(lead, kStageBytes);
                 tma_load_2d<true>(a, &map_a, x0, row, lead);
                 tma_load_2d<true>(a + kOperandBytes / 2, &map_a, x0 + 128, row, lead);
                 tma_load_2d<true>(b, &map_b, y0, row, lead);
@@ -343,7 +349,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 tma_load_2d<false>(b + kOperandBytes / 2, &map_b, y0 + 128, row, mine);
               }
             } else {
-              mbar_expect_cluster(lead, (uint32_t)copies * 64 * 128 + kOperandBytes);
+              mbar_expect_pair(lead, (uint32_t)copies * 64 * 128 + kOperandBytes);
               for (int c = 0; c < copies; ++c) tma_load_2d<true>(a + c * 64 * 128, &map_a, s * 128, tile.row0 + 64 * c, lead);
               if constexpr (MODE == kModeY) tma_load_3d_pair(b, &map_b, s * 128, tile.n + rank * kHalf, tile.expert, lead);
               else tma_load_3d_pair(b, &map_b, tile.n + rank * kHalf, s * 128, tile.expert, lead);
@@ -368,11 +374,13 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         const int steps = tile_of(t0 + i * dt).steps;
         for (int s = 0; s < steps; ++s, ++it) {
           const int acc = it & 1;
-          if (!__all_sync(0xffffffffu, wait_for<true>(smem_addr(&acc_empty[acc]), ((it >> 1) & 1) ^ 1)) ||
-              !__all_sync(0xffffffffu, wait_for<true>(smem_addr(&full[st]), st_phase))) {
+          if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_empty[acc]), ((it >> 1) & 1) ^ 1)) ||
+              !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&full[st]), st_phase))) {
             ok = false;
             break;
           }
+          // what warp 2 of both CTAs cleared
+          if (MODE == kModeDw && s == steps - 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
           tc_after_sync();
           const uint32_t a = data0 + (uint32_t)st * kStageBytes, b = a + kOperandBytes;
           const uint32_t d = tm + (uint32_t)(acc * kPairTile);
@@ -401,7 +409,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       }
       if (elect_one()) mma_commit_to<true>(smem_addr(&done));
       __syncwarp();
-      if (!wait_for<true>(smem_addr(&done), 0)) ok = false;
+      if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
     } else if (warp == 2 && MODE == kModeDw) {
       // ---- the rows behind an expert's last one, cleared in both operands (0 times a NaN is one)
       int it = 0;
@@ -468,7 +476,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             next_w = sw[(s + 1) * sw_stride];
           }
         }
-        if (!__all_sync(0xffffffffu, wait_for<true>(smem_addr(&acc_full[acc]), (it >> 1) & 1))) {
+        if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_full[acc]), (it >> 1) & 1))) {
           ok = false;
           break;
         }
@@ -485,7 +493,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           if (c == 7) {   // read
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_addr(smem_addr(&acc_empty[acc])));
+            if (lane == 0) mbar_arrive_pair(leader_addr(smem_addr(&acc_empty[acc])));
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -513,7 +521,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       }
     }
     // the first CTA's last arrivals have reached this one before it may exit
-    if (ok && !wait_for<true>(smem_addr(&done), 0)) ok = false;
+    if (ok && !wait_for<false>(smem_addr(&done), 0)) ok = false;
   }
   if (!ok && lane == 0) set_status(kStatusWaitTile);
   __syncwarp();
