@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) quantize_b128_kernel(B128QuantArgs a) {
       *reinterpret_cast<uint4*>(out + (uint64_t)r * b128_row_bytes(a.K) + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
     if ((threadIdx.x & 7) == 0) {
-      reinterpret_cast<float*>(out + b128_scale_offset(a.nrows, a.K))[(int64_t)kb * a.nrows + r] = s.scale;
+      reinterpret_cast<float*>(out + b128_scale_offset(a.nrows, a.K))[r * b128_scale_row(a.K) + kb] = s.scale;
     }
   }
   pdl_launch_dependents();

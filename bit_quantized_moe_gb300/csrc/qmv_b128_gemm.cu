@@ -13,8 +13,7 @@
 // can take its scales: the epilogue's threads, a row and 128 columns each, read
 // it from tensor memory (two steps fit) and add it, scaled, to fp32 sums in
 // registers. The scale is one number for a thread's 128 columns: its row's
-// times its block's. dW takes the same way with a scale of 1: no sum in the
-// tensor cores, which truncate where they add, is longer than 64 rows.
+// times its block's. dW goes the same way without scales, 512 rows at a time.
 //
 // Operands whose depth is contiguous (rows in y and dx, weights in y) lie in shared
 // memory as rows of 128 bytes, swizzled; the others (weights in dx, both in dW)
@@ -23,7 +22,7 @@
 //
 // Warps: 0 issues the TMA copies, 1 (of the pair's first CTA) the MMAs, 2 clears
 // the rows behind an expert's last one (dW), 4..11 are the epilogue.
-#include <cmath>
+#include <type_traits>
 
 #include "qmv_internal.h"
 #include "qmv_rows.cuh"
@@ -33,33 +32,47 @@ namespace qmv {
 
 enum : int { kModeY = 0, kModeDx = 1, kModeDw = 2 };
 
+// Steps whose MMAs add to one sum in tensor memory. y and dx: one, whose scales follow. dW has none: 512 rows, so that the
+// tensor cores' truncating additions stay few (8 steps: within 1e-6 of the sum of magnitudes) and the epilogue seldom.
+template <int MODE>
+constexpr int kGroup = MODE == kModeDw ? 8 : 1;
+
 constexpr int kHalf = 128;             // rows, and columns of the other operand, of one CTA
 constexpr int kPairTile = 2 * kHalf;
 constexpr int kPairThreads = 384;
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
+constexpr int kBand = 8;               // row tiles that follow one another (see pair_tile)
 constexpr uint32_t kOperandBytes = kHalf * 128;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kEpiWarps = 8;           // a CTA's
-constexpr int kParkCols16 = 16;        // columns that a warp turns round at once, where rows are not of whole 16 bytes
-constexpr uint32_t kParkBytes = kEpiWarps * 32 * (kParkCols16 + 1) * 4;
+// Bytes of a row that its thread parks in shared memory before its warp stores
+// them, and the pitch of a row there (an odd number of 16 bytes: no bank conflicts).
+constexpr int kParkRow = 128, kParkPitch = kParkRow + 16;
+constexpr uint32_t kParkBytes = kEpiWarps * 32 * kParkPitch;
 constexpr size_t pair_smem(int n_experts) {
   return 1024 + (size_t)kPairStages * kStageBytes + kParkBytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
 }
 static_assert(pair_smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
 // Registers of an epilogue thread and of the others: 256 * 216 + 128 * 72 = 384 * 168, what the launch gives.
-#define QMV_EPI_REGS 216
-#define QMV_OTHER_REGS 72
+template <int MODE>
+struct PairRegs {
+  static constexpr int epilogue = 232, other = 40;
+  static_assert(256 * epilogue + 128 * other <= kPairThreads * 168, "what the launch gives");
+};
 
 struct PairParams {
-  const float* sx;            // scales of the rows [blocks of depth][nrows]
+  const float4* sx;           // scales of the rows [nrows][blocks of depth, rounded up to 4]
   const float* sw;            // scales of the weights [E][ceil(N / 128)][ceil(K / 128)]
   const int32_t* offsets;
   void* y;
   int64_t nrows;
   int n_experts, N, K;
   int out_n;                  // columns of the output
-  int out_type, store_bytes;  // widest store that the output's rows allow: 32, 16, or 0
+  int out_type;
+  bool whole16;               // the output's rows are of whole 16 bytes
   int steps;                  // y, dx: of depth
+  int x_quads;                // fours of a row's scales
+  int k_blocks, n_blocks;     // of the weights' scales
   int n_tiles, m_tiles;       // column tiles; dW: row tiles of a matrix
 };
 
@@ -102,7 +115,7 @@ __device__ __forceinline__ void mbar_expect_pair(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 accumulator columns of this thread's row; not used before tmem_ld_wait16.
@@ -120,6 +133,22 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                :: "memory");
 }
 
+// As mbar_wait_bounded, without a hint to sleep.
+__device__ __forceinline__ bool wait_brisk(uint32_t bar, uint32_t parity) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (ok != 0) return true;
+    if (i % 1024 == 0) {
+      const unsigned long long now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+
 // Two fp32 sums in one register pair.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t v;
@@ -132,77 +161,83 @@ __device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
   return v;
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
+__device__ __forceinline__ void fma2(uint64_t& sum, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(a), "l"(b));
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
+__device__ __forceinline__ void add2(uint64_t& sum, uint64_t a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(a)); }
 
 // Two numbers of 16 bits in a word.
 template <typename T>
 __device__ __forceinline__ uint32_t two16(float a, float b) {
-  const T lo = from_f32<T>(a), hi = from_f32<T>(b);
-  return (uint32_t) * reinterpret_cast<const unsigned short*>(&lo) | (uint32_t) * reinterpret_cast<const unsigned short*>(&hi) << 16;
-}
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8], int bytes) {
-  if (bytes == 32) {
-    store32(p, w);
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
-// 16 columns of a row from n0 on, where the row's stores may be `bytes` wide
-// and its columns end on such a boundary.
-__device__ __forceinline__ void store16(const PairParams& p, int64_t row, int n0, const float (&v)[16]) {
-  const int64_t at = row * p.out_n + n0;
-  if (p.out_type == QMV_F32) {
+// The 128 columns from n0 on of a warp's 32 rows, as T: parked 128 bytes a row
+// at a time and stored four rows by 128 bytes an instruction. (As 32-byte stores of
+// 32 rows at once: 8192 x 7168 x 7168 396 us; as bulk copies of 128 bytes: 347 us,
+// but dW of 32 experts of 2880 627.) Rows are of whole 16 bytes.
+template <typename T>
+__device__ __forceinline__ void store_rows(const PairParams& p, uint8_t* park, int64_t row0, int rows, int n0, int lane,
+                                           const uint64_t (&sum)[64]) {
+  constexpr int cols = kParkRow / (int)sizeof(T);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (n0 + 8 * h >= p.out_n) break;
-      uint32_t w[8];
+  for (int c = 0; c < kHalf; c += cols) {
+    const int vecs = min(cols, p.out_n - n0 - c) * (int)sizeof(T) / 16;
+    if (vecs <= 0) break;
+    uint8_t* mine = park + lane * kParkPitch;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
-      float* out = static_cast<float*>(p.y) + at + 8 * h;
-      if (n0 + 8 * h + 8 <= p.out_n) store_words(out, w, p.store_bytes);
-      else *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);   // half a piece: 16-byte rows
+    for (int i = 0; i < kParkRow / 16; ++i) {
+      uint4 w;
+      if constexpr (sizeof(T) == 4) {
+        const uint64_t a = sum[(c + 4 * i) / 2], b = sum[(c + 4 * i) / 2 + 1];
+        w = make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
+      } else {
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float lo, hi;
+          unpack2(sum[(c + 8 * i) / 2 + k], lo, hi);
+          h[k] = two16<T>(lo, hi);
+        }
+        w = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      reinterpret_cast<uint4*>(mine)[i] = w;
     }
-  } else {
-    uint32_t w[8];
+    __syncwarp();
+    uint8_t* out = static_cast<uint8_t*>(p.y) + ((row0 + lane / 8) * p.out_n + n0 + c) * (int64_t)sizeof(T) + (lane & 7) * 16;
+    const uint8_t* src = park + (lane / 8) * kParkPitch + (lane & 7) * 16;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      w[i] = p.out_type == QMV_BF16 ? two16<__nv_bfloat16>(v[2 * i], v[2 * i + 1]) : two16<__half>(v[2 * i], v[2 * i + 1]);
+      if (4 * i + lane / 8 < rows && (lane & 7) < vecs) {
+        *reinterpret_cast<uint4*>(out + (int64_t)(4 * i) * p.out_n * sizeof(T)) =
+            *reinterpret_cast<const uint4*>(src + 4 * i * kParkPitch);
+      }
     }
-    uint16_t* out = static_cast<uint16_t*>(p.y) + at;
-    if (n0 + 16 <= p.out_n) store_words(out, w, p.store_bytes);
-    else *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    __syncwarp();
   }
 }
 
 // Sixteen columns of a warp's 32 rows, turned round in shared memory, so that
 // neighbouring lanes store neighbouring elements: rows that start anywhere.
 __device__ __forceinline__ void store_turned(const PairParams& p, float* park, int64_t row0, int rows, int n0, int lane,
-                                             const float (&v)[16]) {
+                                             const uint64_t* sum) {
+  constexpr int pitch = 17;
+  static_assert(pitch * 4 <= kParkPitch, "a row's place");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) park[lane * (kParkCols16 + 1) + i] = v[i];
+  for (int i = 0; i < 8; ++i) unpack2(sum[i], park[lane * pitch + 2 * i], park[lane * pitch + 2 * i + 1]);
   __syncwarp();
   const int c = lane & 15;
 #pragma unroll 4
   for (int i = 0; i < 16; ++i) {
     const int r = 2 * i + lane / 16;
     if (r < rows && n0 + c < p.out_n) {
-      const float x = park[r * (kParkCols16 + 1) + c];
+      const float x = park[r * pitch + c];
       const int64_t at = (row0 + r) * p.out_n + n0 + c;
       if (p.out_type == QMV_BF16) static_cast<__nv_bfloat16*>(p.y)[at] = from_f32<__nv_bfloat16>(x);
       else if (p.out_type == QMV_F16) static_cast<__half*>(p.y)[at] = from_f32<__half>(x);
@@ -220,6 +255,9 @@ struct PairTile {
   int steps;
 };
 
+// Output tile t: experts in order; of an expert, bands of up to kBand row tiles,
+// column by column, so that the tiles that run at once share their rows and their
+// columns alike.
 template <int MODE>
 __device__ __forceinline__ PairTile pair_tile(int t, const PairParams& p, const int* first_tile, const int* first_row, int rank) {
   PairTile r;
@@ -227,8 +265,9 @@ __device__ __forceinline__ PairTile pair_tile(int t, const PairParams& p, const 
     const int each = p.m_tiles * p.n_tiles;
     r.expert = t / each;
     const int i = t - r.expert * each;
-    r.n = i / p.m_tiles;
-    r.m = (i - r.n * p.m_tiles) * kPairTile + rank * kHalf;
+    const int band = i / (kBand * p.n_tiles), in = i - band * kBand * p.n_tiles, tall = min(kBand, p.m_tiles - band * kBand);
+    r.n = in / tall;
+    r.m = (band * kBand + in - r.n * tall) * kPairTile + rank * kHalf;
     r.n *= kPairTile;
     r.row0 = first_row[r.expert];
     r.rows = first_row[r.expert + 1] - r.row0;
@@ -244,8 +283,9 @@ __device__ __forceinline__ PairTile pair_tile(int t, const PairParams& p, const 
     const int mt = (rows + kPairTile - 1) / kPairTile;
     const int i = t - first_tile[lo];
     r.expert = lo;
-    r.n = i / mt;
-    const int m = (i - r.n * mt) * kPairTile + rank * kHalf;
+    const int band = i / (kBand * p.n_tiles), in = i - band * kBand * p.n_tiles, tall = min(kBand, mt - band * kBand);
+    r.n = in / tall;
+    const int m = (band * kBand + in - r.n * tall) * kPairTile + rank * kHalf;
     r.n *= kPairTile;
     r.m = 0;
     r.row0 = first_row[lo] + m;
@@ -262,9 +302,9 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   constexpr int kStages = kPairStages;
   extern __shared__ uint8_t dyn[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
-  float* park = reinterpret_cast<float*>(stages + kStages * kStageBytes);
-  int* first_tile = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(park) + kParkBytes);   // [n_experts + 1]
-  int* first_row = first_tile + p.n_experts + 1;                                             // [n_experts + 1]
+  uint8_t* park = stages + kStages * kStageBytes;
+  int* first_tile = reinterpret_cast<int*>(park + kParkBytes);   // [n_experts + 1]
+  int* first_row = first_tile + p.n_experts + 1;                 // [n_experts + 1]
   // Barriers. full (the first CTA's): a step's copies of both CTAs have arrived; empty: its MMAs are complete;
   // acc_full, acc_empty (the first CTA's): a sum in tensor memory is there, has been read by both CTAs; tail: dW, this
   // CTA's copies of a step that is an expert's last, ragged one.
@@ -303,7 +343,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   bool ok = true;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(QMV_OTHER_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PairRegs<MODE>::other));
     const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
     const auto tile_of = [&](int t) {   // the same in all lanes, and known to be
       PairTile r = pair_tile<MODE>(t, p, first_tile, first_row, rank);
@@ -324,7 +364,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         // boxes of 64 rows that have a live one; rows that are not copied keep what the stage held, and are not stored
         const int copies = max(0, min(tile.rows, kHalf) + 63) / 64;
         for (int s = 0; s < tile.steps; ++s, ++it) {
-          if (it >= kStages && !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1))) {
+          if (it >= kStages && !__all_sync(0xffffffffu, wait_brisk(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1))) {
             ok = false;
             break;
           }
@@ -368,14 +408,14 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       const uint32_t data0 = smem_addr(stages);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t idesc = pair_idesc<MODE, F16>();
-      int it = 0, st = 0;
+      int st = 0, sums = 0;
       uint32_t st_phase = 0;
       for (int i = 0; i < my_tiles && ok; ++i) {
         const int steps = tile_of(t0 + i * dt).steps;
-        for (int s = 0; s < steps; ++s, ++it) {
-          const int acc = it & 1;
-          if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_empty[acc]), ((it >> 1) & 1) ^ 1)) ||
-              !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&full[st]), st_phase))) {
+        for (int s = 0; s < steps; ++s) {
+          const int acc = sums & 1;
+          if ((s % kGroup<MODE> == 0 && !__all_sync(0xffffffffu, wait_brisk(smem_addr(&acc_empty[acc]), ((sums >> 1) & 1) ^ 1))) ||
+              !__all_sync(0xffffffffu, wait_brisk(smem_addr(&full[st]), st_phase))) {
             ok = false;
             break;
           }
@@ -384,6 +424,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           tc_after_sync();
           const uint32_t a = data0 + (uint32_t)st * kStageBytes, b = a + kOperandBytes;
           const uint32_t d = tm + (uint32_t)(acc * kPairTile);
+          const bool last = s % kGroup<MODE> == kGroup<MODE> - 1 || s == steps - 1;   // of the sum
           if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {   // 32 bytes of depth each; transposed: 32 or 16 depths
@@ -395,12 +436,13 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 da = operand_desc(a + j * 32);
                 db = MODE == kModeY ? operand_desc(b + j * 32) : transposed_desc(b + j * 32 * 128, 1024);
               }
-              pair_mma<MODE>(d, da, db, idesc, j > 0 ? 1u : 0u);
+              pair_mma<MODE>(d, da, db, idesc, s % kGroup<MODE> > 0 || j > 0 ? 1u : 0u);
             }
             mma_commit_to<true>(smem_addr(&empty[st]));
-            mma_commit_to<true>(smem_addr(&acc_full[acc]));
+            if (last) mma_commit_to<true>(smem_addr(&acc_full[acc]));
           }
           __syncwarp();
+          sums += last;
           if (++st == kStages) {
             st = 0;
             st_phase ^= 1;
@@ -409,7 +451,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       }
       if (elect_one()) mma_commit_to<true>(smem_addr(&done));
       __syncwarp();
-      if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
+      if (!wait_brisk(smem_addr(&done), 0)) ok = false;
     } else if (warp == 2 && MODE == kModeDw) {
       // ---- the rows behind an expert's last one, cleared in both operands (0 times a NaN is one)
       int it = 0;
@@ -439,89 +481,103 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
   } else {
     // ---- epilogue: thread = row 32 (warp % 4) + lane, columns 128 * half on
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(QMV_EPI_REGS));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PairRegs<MODE>::epilogue));
     const int quad = warp % 4, half = (warp - 4) / 4;
     const int r = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    float* my_park = park + (warp - 4) * 32 * (kParkCols16 + 1);
-    const int k_blocks = b128_blocks(p.K), n_blocks = b128_blocks(p.N);
+    uint8_t* warp_park = park + (uint32_t)(warp - 4) * 32 * kParkPitch;
     int it = 0;
     for (int t = t0; t < tiles && ok; t += dt) {
-      const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
-      const int n0 = tile.n + half * kHalf;   // first column of this thread
-      // the scales: one of the row and one of the weights' block a step, asked for a step ahead
-      const float* sx = nullptr;
+      // The scales: the row's four steps at a time, a load ahead; the weights' blocks' 32 steps at a time, a lane each.
+      // (A thread's loads under way are waited for with its next load of tensor memory: two loads a step, 8192 x 7168 x
+      // 7168 334 us.)
+      int steps;
+      const float4* sx = nullptr;
       const float* sw = nullptr;
-      int64_t sw_stride = 0;
-      float next_x = 1.0f, next_w = 1.0f;
-      if constexpr (MODE != kModeDw) {
-        const int64_t row = min((int64_t)tile.row0 + r, p.nrows - 1);
-        sx = p.sx + row;
-        const float* base = p.sw + (int64_t)tile.expert * n_blocks * k_blocks;
-        const int block = min(n0 / kB128, (MODE == kModeY ? n_blocks : k_blocks) - 1);
-        sw = MODE == kModeY ? base + (int64_t)block * k_blocks : base + block;
-        sw_stride = MODE == kModeY ? 1 : k_blocks;
-        next_x = *sx;
-        next_w = *sw;
+      float4 x4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f), next4 = x4;
+      float w32 = 1.0f;
+      {
+        const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
+        steps = (tile.steps + kGroup<MODE> - 1) / kGroup<MODE>;
+        if constexpr (MODE != kModeDw) {
+          sx = p.sx + min((int64_t)tile.row0 + r, p.nrows - 1) * p.x_quads;
+          const int block = min((tile.n + half * kHalf) / kB128, (MODE == kModeY ? p.n_blocks : p.k_blocks) - 1);
+          sw = p.sw + (int64_t)tile.expert * p.n_blocks * p.k_blocks + (MODE == kModeY ? (int64_t)block * p.k_blocks : block);
+          next4 = *sx;
+        }
       }
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      for (int s = 0; s < tile.steps; ++s, ++it) {
+      for (int s = 0; s < steps; ++s, ++it) {
         const int acc = it & 1;
-        const float scale = next_x * next_w;
+        float scale = 1.0f;
         if constexpr (MODE != kModeDw) {
-          if (s + 1 < tile.steps) {
-            next_x = sx[(int64_t)(s + 1) * p.nrows];
-            next_w = sw[(s + 1) * sw_stride];
+          if (s % 4 == 0) {
+            x4 = next4;
+            if (s + 4 < steps) next4 = sx[s / 4 + 1];
+            if (s % 32 == 0) {
+              const int at = min(s + lane, steps - 1);
+              w32 = sw[MODE == kModeY ? (int64_t)at : (int64_t)at * p.k_blocks];
+            }
           }
+          const float x = (s & 2) ? ((s & 1) ? x4.w : x4.z) : ((s & 1) ? x4.y : x4.x);
+          scale = x * __shfl_sync(0xffffffffu, w32, s & 31);
         }
-        if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_full[acc]), (it >> 1) & 1))) {
+        if (!__all_sync(0xffffffffu, wait_brisk(smem_addr(&acc_full[acc]), (it >> 1) & 1))) {
           ok = false;
           break;
         }
         tc_after_sync();
         const uint64_t scale2 = pack2(scale, scale);
         const uint32_t d = tmem + (uint32_t)(acc * kPairTile + half * kHalf) + lanes;
-        // one load under way while the one before is added
-        uint32_t v[2][16];
-        tmem_ld16(d, v[0]);
+        // Two loads of 32 columns are out before the first is added, and the other two while the first two are: the sum
+        // has been read when half of it has been added. (One load after the other: 8192 x 7168 x 7168 345 us.)
+        uint32_t v[2][32];
+        const auto add = [&](int c) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          tmem_ld_wait16(v[c & 1]);
-          if (c < 7) tmem_ld16(d + 16 * (c + 1), v[(c + 1) & 1]);
-          if (c == 7) {   // read
-            tc_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(leader_addr(smem_addr(&acc_empty[acc])));
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t two = pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
+            if constexpr (MODE == kModeDw) add2(sum[16 * c + i], two);
+            else fma2(sum[16 * c + i], two, scale2);
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t part = pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
-            if constexpr (MODE == kModeDw) sum[8 * c + i] = add2(sum[8 * c + i], part);
-            else sum[8 * c + i] = fma2(part, scale2, sum[8 * c + i]);
-          }
-        }
+        };
+        tmem_ld32(d, v[0]);
+        tmem_ld32(d + 32, v[1]);
+        tmem_ld_wait(v[0]);
+        tmem_ld_wait(v[1]);
+        add(0);
+        tmem_ld32(d + 64, v[0]);
+        add(1);
+        tmem_ld32(d + 96, v[1]);
+        tmem_ld_wait(v[0]);
+        tmem_ld_wait(v[1]);
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(leader_addr(smem_addr(&acc_empty[acc])));   // read
+        add(2);
+        add(3);
       }
       if (!ok) break;
+      asm volatile("" : "+r"(t));   // the tile's place is worked out again, not kept in registers over the steps
+      const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
+      const int n0 = tile.n + half * kHalf;   // first column of this thread
       const int64_t row0 = MODE == kModeDw ? (int64_t)tile.expert * p.N + tile.m : (int64_t)tile.row0;   // of the CTA
       const int rows = MODE == kModeDw ? p.N - tile.m : tile.rows;
+      if (p.whole16) {
+        if (p.out_type == QMV_BF16) store_rows<__nv_bfloat16>(p, warp_park, row0 + quad * 32, rows - quad * 32, n0, lane, sum);
+        else if (p.out_type == QMV_F16) store_rows<__half>(p, warp_park, row0 + quad * 32, rows - quad * 32, n0, lane, sum);
+        else store_rows<float>(p, warp_park, row0 + quad * 32, rows - quad * 32, n0, lane, sum);
+      } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int n = n0 + 16 * c;
-        if (n >= p.out_n) break;
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) unpack2(sum[8 * c + i], v[2 * i], v[2 * i + 1]);
-        if (p.store_bytes != 0) {
-          if (r < rows) store16(p, row0 + r, n, v);
-        } else {
-          store_turned(p, my_park, row0 + quad * 32, rows - quad * 32, n, lane, v);
+        for (int c = 0; c < 8; ++c) {
+          if (n0 + 16 * c >= p.out_n) break;
+          store_turned(p, reinterpret_cast<float*>(warp_park), row0 + quad * 32, rows - quad * 32, n0 + 16 * c, lane, sum + 8 * c);
         }
       }
     }
     // the first CTA's last arrivals have reached this one before it may exit
-    if (ok && !wait_for<false>(smem_addr(&done), 0)) ok = false;
+    if (ok && !wait_brisk(smem_addr(&done), 0)) ok = false;
   }
   if (!ok && lane == 0) set_status(kStatusWaitTile);
   __syncwarp();
@@ -566,8 +622,9 @@ cudaError_t pair_go(PairParams& p, int64_t tiles, const void* a, uint64_t a_byte
     const cuuint32_t box[3] = {128, 128, 1};
     if (!encode(&mb, 3, b, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const uint64_t row = (uint64_t)p.out_n * (p.out_type == QMV_F32 ? 4 : 2), at = reinterpret_cast<uintptr_t>(p.y);
-  p.store_bytes = (row | at) % 32 == 0 ? 32 : (row % 16 == 0 ? 16 : 0);
+  p.k_blocks = b128_blocks(p.K);
+  p.n_blocks = b128_blocks(p.N);
+  p.whole16 = (uint64_t)p.out_n * (p.out_type == QMV_F32 ? 4 : 2) % 16 == 0;
 
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kPairThreads);
@@ -602,7 +659,8 @@ template <int MODE>
 cudaError_t product_go(const B128GemmArgs& a) {
   const int depth = MODE == kModeY ? a.K : a.N;
   PairParams p = {};
-  p.sx = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.xq) + b128_scale_offset(a.nrows, depth));
+  p.sx = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(a.xq) + b128_scale_offset(a.nrows, depth));
+  p.x_quads = b128_scale_row(depth) / 4;
   p.sw = a.w_scales;
   p.offsets = a.offsets;
   p.y = a.y;

@@ -202,15 +202,17 @@ QMV_HD inline uint64_t mx_act_bytes(int f, int64_t nrows, int K) {
 
 // Activations in E4M3 with one fp32 scale per row and 128 columns: the codes
 // row after row, rows padded to 16 bytes with codes of 0 (a tensor map's rows),
-// then the scales [ceil(K / 128)][nrows].
+// then the scales, row after row, a row padded to a multiple of four (16 bytes:
+// a thread of a product takes its row's four at a time).
 constexpr int kB128 = 128;
 QMV_HD inline uint64_t b128_row_bytes(int K) { return ((uint64_t)K + 15) / 16 * 16; }
 QMV_HD inline int b128_blocks(int K) { return (K + kB128 - 1) / kB128; }
+QMV_HD inline int b128_scale_row(int K) { return (b128_blocks(K) + 3) / 4 * 4; }
 QMV_HD inline uint64_t b128_scale_offset(int64_t nrows, int K) {
   return ((uint64_t)nrows * b128_row_bytes(K) + 127) / 128 * 128;
 }
 QMV_HD inline uint64_t b128_act_bytes(int64_t nrows, int K) {
-  return b128_scale_offset(nrows, K) + ((uint64_t)nrows * b128_blocks(K) * 4 + 15) / 16 * 16;
+  return b128_scale_offset(nrows, K) + (uint64_t)nrows * b128_scale_row(K) * 4;
 }
 
 }  // namespace qmv

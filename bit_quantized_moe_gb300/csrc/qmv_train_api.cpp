@@ -201,7 +201,7 @@ int qmv_act_b128_unpack(const void* xq, int32_t nrows, int32_t K, uint8_t* codes
   const size_t blocks = (size_t)b128_blocks(K);
   for (size_t r = 0; r < (size_t)nrows; ++r) {
     std::memcpy(codes + r * K, src + r * b128_row_bytes(K), (size_t)K);
-    for (size_t b = 0; b < blocks; ++b) std::memcpy(scales + r * blocks + b, words + (b * (size_t)nrows + r) * 4, 4);
+    for (size_t b = 0; b < blocks; ++b) std::memcpy(scales + r * blocks + b, words + (r * (size_t)b128_scale_row(K) + b) * 4, 4);
   }
   return done();
 }

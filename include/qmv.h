@@ -661,8 +661,8 @@ int qmv_moe_router_grad(int32_t type, const void* logits_dev, int64_t ldl, const
  * [n_experts][ceil(N / 128)][ceil(K / 128)], row-major as they are stored. K a
  * multiple of 16, N any; the last blocks may be smaller.
  * Activation buffer: the codes, row after row, each row padded to a multiple of
- * 16 bytes with zeros; at qmv_act_b128_scale_offset bytes the scales, fp32
- * [ceil(K / 128)][nrows]. K any, up to QMV_MAX_N.
+ * 16 bytes with zeros; at qmv_act_b128_scale_offset bytes the scales, fp32, row after
+ * row, each of ceil(K / 128) padded to a multiple of four. K any, up to QMV_MAX_N.
  * The size functions return 0 for an invalid shape.
  */
 size_t qmv_act_b128_bytes(int32_t nrows, int32_t K);

@@ -141,15 +141,15 @@ TOKENS = [(dict(type=3), -1), (dict(ntok=-1), -1), (dict(ntok=1 << 22), -1), (di
                                             (dict(dlogits=ODD), -3), (dict(scale=float("-inf")), -1)]),
     ("qmv_quantize_act_b128", QUANT, [(dict(type=3), -1), (dict(nrows=-1), -1), (dict(nrows=1 << 23), -1), (dict(K=0), -2),
                                       (dict(K=(1 << 20) + 1, ldx=1 << 21), -2), (dict(ldx=63), -2), (dict(x=None), -1),
-                                      (dict(xq=None), -1), (dict(x=ODD), -3), (dict(xq=ODD), -3), (dict(xq_bytes=3 * 64 + 11), -4)]),
+                                      (dict(xq=None), -1), (dict(x=ODD), -3), (dict(xq=ODD), -3), (dict(xq_bytes=256 + 47), -4)]),
     ("qmv_quantize_weights_b128", QUANT_W, MATRIX + [(dict(type=-1), -1), (dict(w=None), -1), (dict(codes=ODD), -3), (dict(scales=None), -1),
                                                      (dict(n=1024, N=1 << 20, K=65536), -2)]),
     ("qmv_b128_product", PRODUCT, MATRIX + ROWS + [(dict(out_type=3), -1), (dict(w=None), -1), (dict(ws=None), -1), (dict(y=None), -1),
-                                                   (dict(ws=ODD), -3), (dict(xq=ODD), -3), (dict(xq_bytes=3 * 64 + 11), -4)]),
+                                                   (dict(ws=ODD), -3), (dict(xq=ODD), -3), (dict(xq_bytes=256 + 47), -4)]),
     ("qmv_b128_grad_x", PRODUCT, MATRIX + ROWS + [(dict(out_type=-1), -1), (dict(xq=None), -1), (dict(y=ODD), -3),
-                                                  (dict(xq_bytes=3 * 64 + 11), -4), (dict(N=600, xq_bytes=3 * 600), -4)]),
+                                                  (dict(xq_bytes=256 + 47), -4), (dict(N=600, xq_bytes=3 * 600), -4)]),
     ("qmv_b128_linear", LINEAR, MATRIX + ROWS + [(dict(type=3), -1), (dict(x=None), -1), (dict(x=ODD), -3), (dict(ldx=63), -2),
-                                                 (dict(space=None), -1), (dict(space_bytes=3 * 64 + 11), -4), (dict(y=None), -1)]),
+                                                 (dict(space=None), -1), (dict(space_bytes=256 + 47), -4), (dict(y=None), -1)]),
     ("qmv_b128_grad_w", GRAD_W, MATRIX + ROWS + [(dict(type=2), -1), (dict(out_type=3), -1), (dict(ld_dy=63), -2), (dict(ldx=56), -2),
                                                  (dict(ld_dy=68), -2), (dict(ldx=70), -2), (dict(dy=None), -1), (dict(dw=None), -1),
                                                  (dict(x=ODD), -3), (dict(dw=ODD), -3)]),

@@ -161,8 +161,9 @@ def act_buffer(codes, scales):
     wide = -(-K // 16) * 16
     body = np.pad(codes, ((0, 0), (0, wide - K))).reshape(-1)
     at = -(-body.size // 128) * 128
-    tail = np.ascontiguousarray(scales.astype(np.float32).T).view(np.uint8).reshape(-1)
-    out = np.zeros(at + -(-tail.size // 16) * 16, dtype=np.uint8)
+    blocks = scales.shape[1]
+    tail = np.pad(scales.astype(np.float32), ((0, 0), (0, -blocks % 4))).view(np.uint8).reshape(-1)
+    out = np.zeros(at + tail.size, dtype=np.uint8)
     out[:body.size] = body
     out[at:at + tail.size] = tail
     return out
