@@ -672,7 +672,7 @@ int qmv_device_status(uint32_t* flags, int32_t clear) {
   if (!flags) return fail(QMV_EINVAL, "qmv_device_status: NULL pointer");
   uint32_t v = 0;
   const uint32_t parts[] = {status_mxfp4(clear), status_cb2(clear), status_cb3(clear),     status_cb4(clear),     status_mxfp8(clear),
-                            status_verify(clear), status_act(clear), status_mx_gemm(clear), status_b128_gemm(clear)};
+                            status_verify(clear), status_act(clear), status_mx_gemm(clear), status_b128_gemm(clear), status_b128_few(clear)};
   for (uint32_t p : parts) {
     if (p == 0xffffffffu) return cuda_fail(cudaGetLastError(), "qmv_device_status");
     v |= p;

@@ -1,0 +1,448 @@
+// qmv_b128_few.cu -- the products of E4M3 operands with scales of blocks of 128
+// (qmv_b128_gemm.cu) where an expert has few rows: a decode token, a decode
+// batch over the experts, the end of a prompt.
+//
+// Bound by reading the weights once. The weights take the tensor cores' 128
+// rows, the activations' rows their columns (BN of them), so that a step moves
+// 16 KB of weights and 2 or 4 KB of rows. Two CTAs an SM keep a ring of 5 or 4
+// steps under way each. (64 columns, one CTA an SM: slower from 32 rows to 128, by
+// up to a third over experts.) Where there are fewer tiles than
+// SMs, a cluster of CTAs shares a tile's depth and adds its parts in shared
+// memory in the order of the ranks: no workspace, the same bits every run.
+//
+// A step's sum starts from zero and is added in fp32 registers, scaled by its
+// row's scale (one a column here) times its block's, as in qmv_b128_gemm.cu.
+//
+// Warps: 0 issues the TMA copies, 1 the MMAs, 4..7 are the epilogue, thread =
+// row of the weights.
+#include "qmv_internal.h"
+#include "qmv_rows.cuh"
+#include "qmv_tc.cuh"
+
+namespace qmv {
+
+constexpr int kFewThreads = 256;
+constexpr int kFewAccs = 4;
+constexpr int kFewSplits = 8;          // CTAs of a cluster, at most
+constexpr uint32_t kFewW = 128 * 128;  // bytes of weights of a step
+
+template <int BN>
+struct Few {
+  static constexpr int ctas = 2;   // of an SM
+  static constexpr int stages = BN == 16 ? 5 : 4;
+  static constexpr uint32_t x_bytes = BN * 128;
+  static constexpr uint32_t stage_bytes = kFewW + x_bytes;
+  static constexpr uint32_t join_bytes = BN * 128 * 4;
+  static constexpr uint32_t scale_bytes = 4 * BN * 4;   // a warp's scales of a step
+  static constexpr uint32_t tmem_cols = kFewAccs * BN;
+  static constexpr size_t smem(int n_experts) {
+    return 1024 + (size_t)stages * stage_bytes + join_bytes + scale_bytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
+  }
+  static_assert(ctas * (smem(256) + 1536) <= 228 * 1024 && smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
+};
+
+struct FewParams {
+  const float4* sx;           // scales of the rows [nrows][blocks of depth, rounded up to 4]
+  const float* sw;            // scales of the weights [E][ceil(N / 128)][ceil(K / 128)]
+  const int32_t* offsets;
+  void* y;
+  int64_t nrows;
+  int n_experts, out_n, out_type;
+  int x_quads, k_blocks, n_blocks;
+  int steps, per_split;       // of depth, and of one rank of the cluster
+  int n_tiles;                // tiles of 128 outputs
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      " tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+struct FewTile {
+  int expert, row0, rows, n;   // first row of the tile, and rows from there on; first output
+};
+template <int BN>
+__device__ __forceinline__ FewTile few_tile(int t, const FewParams& p, const int* first_tile, const int* first_row) {
+  int lo = 0, hi = p.n_experts - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (first_tile[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const int rows = first_row[lo + 1] - first_row[lo];
+  const int mt = (rows + BN - 1) / BN;   // row tiles of a tile of outputs follow one another: its weights come from L2 again
+  const int i = t - first_tile[lo];
+  FewTile r;
+  r.expert = lo;
+  r.n = i / mt * 128;
+  const int m = (i % mt) * BN;
+  r.row0 = first_row[lo] + m;
+  r.rows = rows - m;
+  return r;
+}
+
+__device__ __forceinline__ void few_store(const FewParams& p, int64_t at, float v) {
+  if (p.out_type == QMV_BF16) static_cast<__nv_bfloat16*>(p.y)[at] = from_f32<__nv_bfloat16>(v);
+  else if (p.out_type == QMV_F16) static_cast<__half*>(p.y)[at] = from_f32<__half>(v);
+  else static_cast<float*>(p.y)[at] = v;
+}
+
+// DX: the weights' outputs are their columns, read transposed.
+template <int BN, bool DX>
+__global__ void __launch_bounds__(kFewThreads, Few<BN>::ctas)
+b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                const __grid_constant__ FewParams p) {
+  using F = Few<BN>;
+  constexpr int kStages = F::stages;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+  float* join = reinterpret_cast<float*>(stages + kStages * F::stage_bytes);   // [BN][128] this CTA's sums
+  float* scales = join + BN * 128;                                            // [4 warps][BN]
+  int* first_tile = reinterpret_cast<int*>(scales + 4 * BN);
+  int* first_row = first_tile + p.n_experts + 1;
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kFewAccs], acc_empty[kFewAccs], joined, joint_read, done;
+  __shared__ uint32_t tmem_base;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), splits = cluster_size();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&full[i]), 1);
+      mbar_init(smem_addr(&empty[i]), 1);
+    }
+    for (int i = 0; i < kFewAccs; ++i) {
+      mbar_init(smem_addr(&acc_full[i]), 1);
+      mbar_init(smem_addr(&acc_empty[i]), 4);
+    }
+    mbar_init(smem_addr(&joined), 4 * splits);
+    mbar_init(smem_addr(&joint_read), 4 * splits);
+    mbar_init(smem_addr(&done), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_addr(&tmem_base)),
+                 "r"(F::tmem_cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  if (warp == 0) expert_tiles(p.offsets, (int)p.nrows, p.n_experts, BN, p.n_tiles, lane, first_row, first_tile);
+  tc_before_sync();
+  __syncthreads();
+  if (splits > 1) cluster_sync_all();   // every CTA's barriers exist
+  tc_after_sync();
+  const uint32_t tmem = tmem_base;
+  const int tiles = first_tile[p.n_experts];
+  const int t0 = (int)blockIdx.x / splits, dt = (int)gridDim.x / splits;
+  const int s0 = min(rank * p.per_split, p.steps), s1 = min(s0 + p.per_split, p.steps);   // this rank's steps
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---- copies
+    int it = 0, st = 0;
+    for (int t = t0; t < tiles && ok; t += dt) {
+      FewTile tile = few_tile<BN>(t, p, first_tile, first_row);
+      tile.expert = __shfl_sync(0xffffffffu, tile.expert, 0);
+      tile.row0 = __shfl_sync(0xffffffffu, tile.row0, 0);
+      tile.n = __shfl_sync(0xffffffffu, tile.n, 0);
+      for (int s = s0; s < s1; ++s, ++it) {
+        if (it >= kStages && !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&empty[st]), ((it / kStages) & 1) ^ 1))) {
+          ok = false;
+          break;
+        }
+        const uint32_t w = smem_addr(stages) + (uint32_t)st * F::stage_bytes, bar = smem_addr(&full[st]);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, F::stage_bytes);
+          if constexpr (DX) tma_load_3d(w, &map_w, tile.n, s * 128, tile.expert, bar);
+          else tma_load_3d(w, &map_w, s * 128, tile.n, tile.expert, bar);
+          tma_load_2d<false>(w + kFewW, &map_x, s * 128, tile.row0, bar);
+        }
+        __syncwarp();
+        if (++st == kStages) st = 0;
+      }
+    }
+    if (!ok) {   // leave no copy in flight
+      for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
+        if (!mbar_wait_bounded(smem_addr(&full[i % kStages]), (i / kStages) & 1, kDrainLimitNs) && lane == 0) {
+          set_status(kStatusDrain);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- products; the same in all lanes, one issues
+    constexpr uint32_t idesc = (1u << 4) | (DX ? 1u << 15 : 0u) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
+    const int total = my_tiles * (s1 - s0);
+    int st = 0;
+    uint32_t st_phase = 0;
+    for (int it = 0; it < total; ++it) {
+      const int acc = it % kFewAccs;
+      if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_empty[acc]), ((it / kFewAccs) & 1) ^ 1)) ||
+          !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&full[st]), st_phase))) {
+        ok = false;
+        break;
+      }
+      tc_after_sync();
+      const uint32_t w = smem_addr(stages) + (uint32_t)st * F::stage_bytes, x = w + kFewW;
+      const uint32_t d = tm + (uint32_t)(acc * BN);
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t a = DX ? transposed_desc(w + j * 32 * 128, 1024) : operand_desc(w + j * 32);
+          asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+                       :: "r"(d), "l"(a), "l"(operand_desc(x + j * 32)), "r"(idesc), "r"(j > 0 ? 1u : 0u) : "memory");
+        }
+        mma_commit_to<false>(smem_addr(&empty[st]));
+        mma_commit_to<false>(smem_addr(&acc_full[acc]));
+      }
+      __syncwarp();
+      if (++st == kStages) {
+        st = 0;
+        st_phase ^= 1;
+      }
+    }
+    if (elect_one()) mma_commit_to<false>(smem_addr(&done));
+    __syncwarp();
+    if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
+  } else if (warp >= 4) {
+    // ---- epilogue: thread = row of the weights 32 (warp % 4) + lane; the tile's rows are its columns
+    constexpr int kEach = (BN + 31) / 32;   // rows whose scales a lane loads
+    const int quad = warp % 4;
+    float* mine = scales + quad * BN;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    int it = 0;
+    uint32_t phase = 0;   // of the joins
+    for (int t = t0; t < tiles && ok; t += dt) {
+      const FewTile tile = few_tile<BN>(t, p, first_tile, first_row);
+      const int block = tile.n / kB128;
+      const float* sw = p.sw + (int64_t)tile.expert * p.n_blocks * p.k_blocks + (DX ? block : (int64_t)block * p.k_blocks);
+      const int64_t sw_stride = DX ? p.k_blocks : 1;
+      // the rows' scales four steps at a time, a load ahead; the block's 32 steps at a time, a lane each (a thread's loads
+      // under way are waited for with its next load of tensor memory)
+      float4 x4[kEach], next4[kEach];
+      float w32 = 0.0f;
+      const float4* sx[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        sx[i] = p.sx + min((int64_t)tile.row0 + lane + 32 * i, p.nrows - 1) * p.x_quads;
+        next4[i] = s0 < s1 ? sx[i][s0 / 4] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        x4[i] = next4[i];
+      }
+      float sum[BN];
+#pragma unroll
+      for (float& v : sum) v = 0.0f;
+      for (int s = s0; s < s1; ++s, ++it) {
+        const int acc = it % kFewAccs;
+        if (s == s0 || s % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            x4[i] = next4[i];
+            if (s / 4 * 4 + 4 < s1) next4[i] = sx[i][s / 4 + 1];
+          }
+        }
+        if ((s - s0) % 32 == 0) w32 = sw[min(s + lane, s1 - 1) * sw_stride];
+        const float w = __shfl_sync(0xffffffffu, w32, (s - s0) & 31);
+        __syncwarp();   // the step before has been read
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const float x = (s & 2) ? ((s & 1) ? x4[i].w : x4[i].z) : ((s & 1) ? x4[i].y : x4[i].x);
+          if (BN >= 32 || lane < BN) mine[lane + 32 * i] = x * w;
+        }
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_full[acc]), (it / kFewAccs) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_after_sync();
+#pragma unroll
+        for (int c = 0; c < BN; c += 16) {
+          uint32_t v[16];
+          tmem_ld16_now(tmem + (uint32_t)(acc * BN + c) + lanes, v);
+          if (c + 16 >= BN) {   // read
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_one(smem_addr(&acc_empty[acc]));
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(mine + c + i);
+            sum[c + i] = fmaf(__uint_as_float(v[i]), f.x, sum[c + i]);
+            sum[c + i + 1] = fmaf(__uint_as_float(v[i + 1]), f.y, sum[c + i + 1]);
+            sum[c + i + 2] = fmaf(__uint_as_float(v[i + 2]), f.z, sum[c + i + 2]);
+            sum[c + i + 3] = fmaf(__uint_as_float(v[i + 3]), f.w, sum[c + i + 3]);
+          }
+        }
+      }
+      if (!ok) break;
+      const int n = tile.n + quad * 32 + lane;
+      if (splits == 1) {
+#pragma unroll
+        for (int c = 0; c < BN; ++c) {
+          if (c < tile.rows && n < p.out_n) few_store(p, ((int64_t)tile.row0 + c) * p.out_n + n, sum[c]);
+        }
+      } else {
+        // every rank's sums lie in its own shared memory; each adds up the rows that are its share
+        const int rows = min(tile.rows, BN);
+#pragma unroll
+        for (int c = 0; c < BN; ++c) {
+          if (c < rows) join[c * 128 + quad * 32 + lane] = sum[c];
+        }
+        __syncwarp();
+        if (lane < splits) mbar_arrive_cluster(peer_addr(smem_addr(&joined), lane));
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_addr(&joined), phase, kWaitLimitNs))) {
+          ok = false;
+          break;
+        }
+        for (int c = rank; c < rows; c += splits) {
+          const uint32_t at = smem_addr(join + c * 128 + quad * 32 + lane);
+          float part[kFewSplits];
+#pragma unroll
+          for (int i = 0; i < kFewSplits; ++i) part[i] = i < splits ? ld_cluster(peer_addr(at, i)) : 0.0f;
+          float v = part[0];
+#pragma unroll
+          for (int i = 1; i < kFewSplits; ++i) v += part[i];
+          if (n < p.out_n) few_store(p, ((int64_t)tile.row0 + c) * p.out_n + n, v);
+        }
+        if (t + dt < tiles) {   // the next tile's sums take the same place
+          __syncwarp();
+          if (lane < splits) mbar_arrive_cluster(peer_addr(smem_addr(&joint_read), lane));
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_addr(&joint_read), phase, kWaitLimitNs))) {
+            ok = false;
+            break;
+          }
+        }
+        phase ^= 1;
+      }
+    }
+  }
+  if (!ok && lane == 0) set_status(kStatusWaitTile);
+  __syncwarp();
+  pdl_launch_dependents();
+  tc_before_sync();
+  __syncthreads();
+  if (splits > 1) cluster_sync_all();   // no CTA's sums are being read any more
+  if (warp == 1) {
+    tc_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(F::tmem_cols));
+  }
+}
+
+QMV_DEFINE_STATUS_ACCESSOR(status_b128_few)
+
+namespace {
+
+template <int BN, bool DX>
+cudaError_t few_go(const B128GemmArgs& a) {
+  using F = Few<BN>;
+  auto* kernel = b128_few_kernel<BN, DX>;
+  const int depth = DX ? a.N : a.K;
+  FewParams p = {};
+  p.sx = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(a.xq) + b128_scale_offset(a.nrows, depth));
+  p.sw = a.w_scales;
+  p.offsets = a.offsets;
+  p.y = a.y;
+  p.nrows = a.nrows;
+  p.n_experts = a.n_experts;
+  p.out_n = DX ? a.K : a.N;
+  p.out_type = a.out_type;
+  p.x_quads = b128_scale_row(depth) / 4;
+  p.k_blocks = b128_blocks(a.K);
+  p.n_blocks = b128_blocks(a.N);
+  p.steps = b128_blocks(depth);
+  p.n_tiles = b128_blocks(p.out_n);
+  g_launch_stage = "cudaFuncSetAttribute";
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::smem(QMV_MAX_SORT_EXPERTS));
+  if (e != cudaSuccess) return e;
+  g_launch_stage = "cuTensorMapEncodeTiled";
+  if (encode_fn() == nullptr) return cudaErrorNotSupported;
+  CUtensorMap mw, mx;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.n_experts};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.K, (cuuint64_t)a.K * (cuuint64_t)a.N};
+    const cuuint32_t box[3] = {128, 128, 1};
+    if (!encode(&mw, 3, a.w, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t row = b128_row_bytes(depth);
+    const cuuint64_t dims[2] = {row, (cuuint64_t)a.nrows}, strides[1] = {row};
+    const cuuint32_t box[2] = {128, BN};
+    if (!encode(&mx, 2, a.xq, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  // tiles that there can be: every expert has at most one partial row tile
+  const int64_t row_tiles = a.nrows / BN + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);
+  const int64_t tiles = (a.n_experts == 1 ? (a.nrows + BN - 1) / BN : row_tiles) * p.n_tiles;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = F::smem(a.n_experts);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // Ranks of a tile: as many as there is room for on the SMs, each with two steps at least, while every tile has a
+  // cluster of its own (1 x 7168 x 7168, 56 tiles: one rank 20.8 us, two 14.3, three 13.3, five 12.6; clusters that take
+  // a second tile 16.7 and more). The occupancy query counts one CTA an SM; two run (the fives above are 280 CTAs).
+  static PerDevice clusters[kFewSplits + 1];   // of each size that run at once
+  int splits = 1, most = 0;
+  while (splits < kFewSplits && (splits + 1) * tiles <= F::ctas * device_sm_count() && (splits + 1) * 2 <= p.steps) ++splits;
+  for (;; --splits) {
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    g_launch_stage = "cudaOccupancyMaxActiveClusters";
+    e = clusters[splits].get(&most, [&](int* n) {
+      cfg.gridDim = dim3((unsigned)(device_sm_count() / splits * splits));
+      return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+    });
+    if (e != cudaSuccess) return e;
+    most *= F::ctas;
+    if (splits == 1 || most >= tiles) break;
+  }
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  p.per_split = (p.steps + splits - 1) / splits;
+  g_launch_stage = "launch";
+  cfg.gridDim = dim3((unsigned)(splits * (tiles < most ? tiles : most)));
+  cfg.numAttrs = a.stream != nullptr ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mx, p);
+}
+
+template <bool DX>
+cudaError_t few_by_rows(const B128GemmArgs& a) {
+  const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
+  return a.nrows <= 16 * hit ? few_go<16, DX>(a) : few_go<32, DX>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_b128_few(const B128GemmArgs& a, bool dx) { return dx ? few_by_rows<true>(a) : few_by_rows<false>(a); }
+
+}  // namespace qmv

@@ -22,6 +22,7 @@
 //
 // Warps: 0 issues the TMA copies, 1 (of the pair's first CTA) the MMAs, 2 clears
 // the rows behind an expert's last one (dW), 4..11 are the epilogue.
+#include <cmath>
 #include <type_traits>
 
 #include "qmv_internal.h"
@@ -80,13 +81,6 @@ template <int MODE, bool F16>
 __device__ __forceinline__ constexpr uint32_t pair_idesc() {
   return (1u << 4) | (MODE == kModeDw && !F16 ? (1u << 7) | (1u << 10) : 0u) | (MODE == kModeDw ? 1u << 15 : 0u) |
          (MODE != kModeY ? 1u << 16 : 0u) | ((uint32_t)(kPairTile >> 3) << 17) | ((uint32_t)(kPairTile >> 4) << 24);
-}
-
-// Operand read transposed: 128 bytes of outputs at each depth, swizzled, eight
-// depths every 1024 bytes; the next 128 bytes of outputs `panel` bytes on.
-__device__ __forceinline__ uint64_t transposed_desc(uint32_t addr, uint32_t panel) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
 template <int MODE>
@@ -678,10 +672,28 @@ cudaError_t product_go(const B128GemmArgs& a) {
                               (uint64_t)a.K, (uint64_t)a.K, a.stream);
 }
 
+// Whether a product takes the kernel for few rows (32 a tile). Its time goes by the tiles' steps, 2 ns each over the whole
+// device, or by reading the weights, at about 4.5 TB/s; a pair's by the tiles that each pair has to take, 0.41 us a
+// step; both as fitted to GB300. Experts are taken as equally full, with half a tile more each. Measured (few / pairs, us):
+//   1 x 2880 x 2880 6.1 / 13.8, 16 x 7168 x 7168 14.3 / 28.7, 128 x 7168 x 7168 28.3 / 30.2, 256 x 7168 x 7168 54 / 30.0
+//   over 32 experts of 2880 x 2880: 1024 rows 53 / 79, 2048 rows 80 / 80, 4096 rows 160 / 82
+bool few_rows(const B128GemmArgs& a, int depth, int out_n) {
+  const double hit = a.nrows < a.n_experts ? (double)a.nrows : (double)a.n_experts;
+  const auto row_tiles = [&](int rows) {
+    const double each = a.nrows / hit / rows;
+    return a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
+  };
+  const double steps = b128_blocks(depth);
+  const double tile_us = row_tiles(32) * b128_blocks(out_n) * steps * 2e-3, read_us = hit * a.N * a.K / 4.5e6;
+  const double pair_tiles = row_tiles(kPairTile) * ((out_n + kPairTile - 1) / kPairTile);
+  const double pair_us = ceil(pair_tiles / (device_sm_count() / 2)) * steps * 0.41;
+  return 4.0 + (tile_us > read_us ? tile_us : read_us) < 7.0 + (pair_us > read_us ? pair_us : read_us);
+}
+
 }  // namespace
 
-cudaError_t launch_b128_product(const B128GemmArgs& a) { return product_go<kModeY>(a); }
-cudaError_t launch_b128_grad_x(const B128GemmArgs& a) { return product_go<kModeDx>(a); }
+cudaError_t launch_b128_product(const B128GemmArgs& a) { return few_rows(a, a.K, a.N) ? launch_b128_few(a, false) : product_go<kModeY>(a); }
+cudaError_t launch_b128_grad_x(const B128GemmArgs& a) { return few_rows(a, a.N, a.K) ? launch_b128_few(a, true) : product_go<kModeDx>(a); }
 
 cudaError_t launch_b128_grad_w(const B128GradWArgs& a) {
   PairParams p = {};

@@ -162,6 +162,7 @@ struct MxGemmArgs {
 cudaError_t launch_mx_gemm(const MxGemmArgs& a);
 uint32_t status_mx_gemm(int clear);
 uint32_t status_b128_gemm(int clear);
+uint32_t status_b128_few(int clear);
 
 // The router of a MoE layer (qmv_router.cu). live: null, or 0 for a token that is not there.
 struct RouterArgs {
@@ -244,6 +245,8 @@ struct B128GemmArgs {
 };
 cudaError_t launch_b128_product(const B128GemmArgs& a);
 cudaError_t launch_b128_grad_x(const B128GemmArgs& a);
+// Few rows of an expert (qmv_b128_few.cu); dx: grad_x.
+cudaError_t launch_b128_few(const B128GemmArgs& a, bool dx);
 
 struct B128GradWArgs {
   int type = 0;                       // of dy and x, 16 bits

@@ -42,6 +42,13 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
+// Operand read transposed: 128 bytes of outputs at each depth, swizzled, eight
+// depths every 1024 bytes; the next 128 bytes of outputs `panel` bytes on.
+__device__ __forceinline__ uint64_t transposed_desc(uint32_t addr, uint32_t panel) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
 // Arrives when this thread's earlier MMAs and copies are complete; PAIR: at the
 // same barrier of both CTAs.
 template <bool PAIR>
