@@ -3,8 +3,12 @@
 // gradient of both.
 #include <type_traits>
 
+#include <cooperative_groups.h>
+
 #include "qmv_internal.h"
 #include "qmv_rows.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace qmv {
 
@@ -17,8 +21,11 @@ namespace qmv {
 // softmax: exp(l - max) over its sum. sigmoid: with u = e^min(l,0) / (1 + e^-|l|)
 // = 1 / (1 + e^-l); quotients of sigmoids are taken of
 // t = e^(min(l,0) - top) / (1 + e^-|l|), top the largest min(l,0) of the row, which
-// is in range where u is not. expf and its sums are fp32; a row of E terms is
-// within (E / 32 + 12) * 2^-24 or so of exact.
+// is in range where u is not. Exponentials are the special functions' 2^x of
+// x log2 e, whose rounding costs |x| * 2^-24 as the argument's own does; sums
+// are fp32, and a row divides by its sum once, by multiplying with the
+// reciprocal. (With expf and a division an expert the gradient of 16,384 x 256
+// took 16.7 us.)
 //
 // A logit of -infinity is an expert that is not there. A row with a NaN
 // (softmax: or +infinity) has no scores: its weights and its gradient are NaN.
@@ -26,6 +33,7 @@ namespace qmv {
 constexpr int kRouterThreads = 256;
 constexpr int kRouterWarps = kRouterThreads / 32;
 
+__device__ __forceinline__ float exp_of(float x) { return __expf(x); }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -52,9 +60,9 @@ __device__ __forceinline__ void load_logits(const T* row, int n_experts, int lan
 }
 
 // 1 / (1 + e^-l)
-__device__ __forceinline__ float sigmoid(float l) { return expf(fminf(l, 0.0f)) / (1.0f + expf(-fabsf(l))); }
+__device__ __forceinline__ float sigmoid(float l) { return exp_of(fminf(l, 0.0f)) / (1.0f + exp_of(-fabsf(l))); }
 __device__ __forceinline__ float sigmoid_scaled(float l, float top) {
-  return l == neg_inf() ? 0.0f : expf(fminf(l, 0.0f) - top) / (1.0f + expf(-fabsf(l)));
+  return l == neg_inf() ? 0.0f : exp_of(fminf(l, 0.0f) - top) / (1.0f + exp_of(-fabsf(l)));
 }
 
 // Whether the row has no scores: a NaN, or for softmax +infinity.
@@ -78,13 +86,14 @@ __device__ __forceinline__ bool row_shares(const float (&l)[V], float (&p)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if constexpr (SIGMOID) p[i] = sigmoid_scaled(l[i], top);
-    else p[i] = l[i] == neg_inf() ? 0.0f : expf(l[i] - top);
+    else p[i] = l[i] == neg_inf() ? 0.0f : exp_of(l[i] - top);
     sum += p[i];
   }
   sum = warp_sum(sum);
   if (sum == 0.0f) return false;
+  const float inverse = 1.0f / sum;
 #pragma unroll
-  for (int i = 0; i < V; ++i) p[i] /= sum;
+  for (int i = 0; i < V; ++i) p[i] *= inverse;
   return true;
 }
 
@@ -116,18 +125,15 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(RouterArgs a) {
     float chosen = neg_inf();   // and its logit
     float first = neg_inf();    // the largest
     for (int j = 0; j < a.top_k; ++j) {
-      uint32_t best = 0;
-      int at = 0;
+      uint32_t best = key[0];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (key[i] > best) {
-          best = key[i];
-          at = i;
-        }
-      }
+      for (int i = 1; i < V; ++i) best = max(best, key[i]);
       const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-      const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
       if (m == 0u) break;   // no logit above -infinity is left
+      uint32_t at = 0xffffffffu;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) at = key[i] == m ? (uint32_t)(lane + 32 * i) : at;
+      const int e = (int)__reduce_min_sync(0xffffffffu, at);
       if (j == 0) first = key_value(m);
       if (lane == j) {
         id = e;
@@ -138,15 +144,15 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(RouterArgs a) {
     }
     float w;
     if (a.renorm) {
-      const float v = id < 0 ? 0.0f : (SIGMOID ? sigmoid_scaled(chosen, fminf(first, 0.0f)) : expf(chosen - first));
+      const float v = id < 0 ? 0.0f : (SIGMOID ? sigmoid_scaled(chosen, fminf(first, 0.0f)) : exp_of(chosen - first));
       w = v / warp_sum(v);
     } else if constexpr (SIGMOID) {
       w = sigmoid(chosen);
     } else {
       float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += l[i] == neg_inf() ? 0.0f : expf(l[i] - first);
-      w = expf(chosen - first) / warp_sum(sum);
+      for (int i = 0; i < V; ++i) sum += l[i] == neg_inf() ? 0.0f : exp_of(l[i] - first);
+      w = exp_of(chosen - first) / warp_sum(sum);
     }
     w = id < 0 ? 0.0f : w * a.scale;
     if (bad) {
@@ -166,15 +172,30 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(RouterArgs a) {
 //   L = E sum_e f_e P_e,   f_e = n_e / (top_k T),   P_e = 1/T sum_t p_te.
 //
 // A warp adds up its tokens' shares in registers, a CTA its warps' and writes a
-// row of partial sums; the second launch adds the rows in order. Slots and
-// tokens are counted in integers, so that every sum is the same every run.
+// row of partial sums; the second launch, 128 experts a CTA, adds the rows in
+// order, and its CTAs (a cluster) their parts of the loss. A batch that one CTA
+// takes needs no second launch. Slots and tokens are counted in integers, so
+// that every sum is the same every run.
 // ---------------------------------------------------------------------------
 constexpr int kBalanceThreads = 512;
 constexpr int kBalanceWarps = kBalanceThreads / 32;
+constexpr int kBalanceAlone = 64;      // tokens that one CTA takes alone
+constexpr int kBalanceParts = 304;     // CTAs of the first launch at most: two an SM
+constexpr int kFinishCols = 128, kFinishGroups = 8;
+
+// Sum over the CTA's threads, in all of them; scratch: one number a warp.
+__device__ __forceinline__ float block_sum(float v, float* scratch) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = v;
+  __syncthreads();
+  const int warps = (int)blockDim.x / 32, lane = threadIdx.x & 31;
+  return warp_sum(lane < warps ? scratch[lane] : 0.0f);
+}
 
 template <typename T, bool SIGMOID, int V>
 __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceArgs a) {
   extern __shared__ float sums[];   // [warps][E], then counts [E + 1]
+  __shared__ float scratch[kBalanceWarps];
   const int E = a.n_experts;
   int* counts = reinterpret_cast<int*>(sums + kBalanceWarps * E);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -185,12 +206,20 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceArgs a)
 #pragma unroll
   for (int i = 0; i < V; ++i) mine[i] = 0.0f;
   int live_tokens = 0;
-  for (int64_t t = (int64_t)warp * gridDim.x + blockIdx.x; t < a.ntok; t += (int64_t)gridDim.x * kBalanceWarps) {
-    if (a.live != nullptr && a.live[t] == 0) continue;
+  const int64_t stride = (int64_t)gridDim.x * kBalanceWarps;
+  // the next token's logits are on their way while this one's are added
+  int64_t t = (int64_t)warp * gridDim.x + blockIdx.x;
+  float next[V];
+  const T* logits = static_cast<const T*>(a.logits);
+  if (t < a.ntok) load_logits<T, V>(logits + t * a.ldl, E, lane, next);
+  for (; t < a.ntok; t += stride) {
     float l[V], p[V];
-    load_logits<T, V>(static_cast<const T*>(a.logits) + t * a.ldl, E, lane, l);
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = next[i];
+    const bool live = a.live == nullptr || a.live[t] != 0;
     const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-    if (!row_shares<SIGMOID, V>(l, p)) continue;
+    if (t + stride < a.ntok) load_logits<T, V>(logits + (t + stride) * a.ldl, E, lane, next);
+    if (!live || !row_shares<SIGMOID, V>(l, p)) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) mine[i] += p[i];
     ++live_tokens;
@@ -202,56 +231,86 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceArgs a)
   }
   if (lane == 0 && live_tokens > 0) atomicAdd(&counts[E], live_tokens);
   __syncthreads();
-  float* part = a.part_sums + (int64_t)blockIdx.x * E;
-  int* part_counts = a.part_counts + (int64_t)blockIdx.x * (E + 1);
-  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) {
-    part_counts[e] = counts[e];
-    if (e == E) break;
+  const bool alone = gridDim.x == 1;
+  const int tokens = counts[E];
+  float part_loss = 0.0f;
+  for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBalanceWarps; ++w) v += sums[w * E + e];
-    part[e] = v;
+    if (alone) {
+      const float mean = tokens > 0 ? v / (float)tokens : 0.0f;
+      a.means[e] = mean;
+      a.counts[e] = counts[e];
+      if (tokens > 0) part_loss += (float)counts[e] / ((float)a.top_k * (float)tokens) * mean;
+    } else {
+      a.part_sums[(int64_t)blockIdx.x * E + e] = v;
+      a.part_counts[(int64_t)blockIdx.x * (E + 1) + e] = counts[e];
+    }
+  }
+  if (alone) {
+    const float loss = block_sum(part_loss, scratch);
+    if (threadIdx.x == 0) {
+      a.loss[0] = (float)E * loss;
+      a.counts[E] = tokens;
+    }
+  } else if (threadIdx.x == 0) {
+    a.part_counts[(int64_t)blockIdx.x * (E + 1) + E] = tokens;
   }
   pdl_launch_dependents();
 }
 
-__global__ void __launch_bounds__(1024) balance_finish_kernel(BalanceArgs a) {
-  __shared__ float warp_part[32];
-  __shared__ int tokens;
-  const int E = a.n_experts, e = threadIdx.x;
+__global__ void __launch_bounds__(kFinishCols * kFinishGroups) balance_finish_kernel(BalanceArgs a) {
+  __shared__ float group_sums[kFinishGroups][kFinishCols];
+  __shared__ int group_counts[kFinishGroups][kFinishCols];
+  __shared__ float scratch[32], loss_parts[8];
+  __shared__ int live_tokens;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int E = a.n_experts;
+  const int c = threadIdx.x % kFinishCols, group = threadIdx.x / kFinishCols;
+  const int e = (int)blockIdx.x * kFinishCols + c;
   pdl_wait();
   float sum = 0.0f;
   int n = 0;
   if (e < E) {
 #pragma unroll 8
-    for (int g = 0; g < a.parts; ++g) {
+    for (int g = group; g < a.parts; g += kFinishGroups) {
       sum += a.part_sums[(int64_t)g * E + e];
       n += a.part_counts[(int64_t)g * (E + 1) + e];
     }
   }
+  group_sums[group][c] = sum;
+  group_counts[group][c] = n;
   if (threadIdx.x < 32) {
     int live = 0;
     for (int g = threadIdx.x; g < a.parts; g += 32) live += a.part_counts[(int64_t)g * (E + 1) + E];
     live = __reduce_add_sync(0xffffffffu, live);
-    if (threadIdx.x == 0) tokens = live;
+    if (threadIdx.x == 0) live_tokens = live;
   }
   __syncthreads();
-  const int T = tokens;
-  const float mean = T > 0 ? sum / (float)T : 0.0f;
-  const float f = T > 0 ? (float)n / ((float)a.top_k * (float)T) : 0.0f;
-  const float part = warp_sum(e < E ? f * mean : 0.0f);
-  if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x / 32] = part;
-  if (e < E) {
+  const int T = live_tokens;
+  float part = 0.0f;
+  if (group == 0 && e < E) {
+    sum = 0.0f;
+    n = 0;
+#pragma unroll
+    for (int g = 0; g < kFinishGroups; ++g) {
+      sum += group_sums[g][c];
+      n += group_counts[g][c];
+    }
+    const float mean = T > 0 ? sum / (float)T : 0.0f;
     a.means[e] = mean;
     a.counts[e] = n;
+    part = T > 0 ? (float)n / ((float)a.top_k * (float)T) * mean : 0.0f;
   }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const float all = warp_sum(warp_part[threadIdx.x]);
-    if (threadIdx.x == 0) {
-      a.loss[0] = (float)E * all;
-      a.counts[E] = T;
-    }
+  part = block_sum(part, scratch);
+  if (threadIdx.x == 0) cluster.map_shared_rank(loss_parts, 0)[cluster.block_rank()] = part;
+  cluster.sync();
+  if (cluster.block_rank() == 0 && threadIdx.x == 0) {
+    float loss = 0.0f;
+    for (unsigned i = 0; i < cluster.num_blocks(); ++i) loss += loss_parts[i];
+    a.loss[0] = (float)E * loss;
+    a.counts[E] = T;
   }
   pdl_launch_dependents();
 }
@@ -269,27 +328,58 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(BalanceArgs a) {
 template <typename T, bool SIGMOID, int V>
 __global__ void __launch_bounds__(kRouterThreads) router_grad_kernel(RouterGradArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * kRouterWarps + threadIdx.x / 32;
   const int E = a.n_experts;
   pdl_wait();
-  if (t < a.ntok) {
+  // the loss's part: fractions of the slots, the same for every token
+  float f[V], c = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = 0.0f;
+  if (a.counts != nullptr) {
+    const int tokens = a.counts[E];
+    if (tokens > 0) {
+      const float per = 1.0f / ((float)a.top_k * (float)tokens);
+      c = a.dloss[0] * (float)E / (float)tokens;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        f[i] = e < E ? (float)a.counts[e] * per : 0.0f;
+      }
+    }
+  }
+  for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + threadIdx.x / 32; t < a.ntok; t += (int64_t)gridDim.x * kRouterWarps) {
     const bool live = a.live == nullptr || a.live[t] != 0;
     const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
     float l[V], p[V], d[V];
     load_logits<T, V>(row, E, lane, l);
+    int id = a.dweights != nullptr && lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
+    if (id >= E) id = -1;
+    const float dw = id >= 0 ? a.dweights[t * a.top_k + lane] : 0.0f;
+    float chosen = id >= 0 ? to_f32(row[id]) : neg_inf();
     const bool any = row_shares<SIGMOID, V>(l, p);
+    const float none = row_is_bad<SIGMOID, V>(l) ? __uint_as_float(0x7fc00000u) : 0.0f;
+    float inner = 0.0f;   // softmax: every expert's share times this goes off
+    if (a.counts != nullptr && any) {
+      float fp = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = 0.0f;
+      for (int i = 0; i < V; ++i) fp += f[i] * p[i];
+      fp = warp_sum(fp);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        d[i] = c * p[i] * (f[i] - fp);
+        if constexpr (SIGMOID) d[i] *= sigmoid(-l[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = 0.0f;
+    }
     if (a.dweights != nullptr) {
-      int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-      if (id >= E || !any) id = -1;
-      const bool has = id >= 0;
-      const float g = has ? a.scale * a.dweights[t * a.top_k + lane] : 0.0f;
-      const float chosen = has ? to_f32(row[id]) : neg_inf();
-      float add = 0.0f, inner = 0.0f;   // at the expert; softmax: times p everywhere
+      const bool has = id >= 0 && any;
+      const float g = has ? a.scale * dw : 0.0f;
+      if (!has) chosen = neg_inf();
+      float add = 0.0f;   // at the expert
       if (a.renorm) {
         const float top = warp_max(SIGMOID ? fminf(chosen, 0.0f) : chosen);
-        float q = !has ? 0.0f : (SIGMOID ? sigmoid_scaled(chosen, top) : (chosen == neg_inf() ? 0.0f : expf(chosen - top)));
+        float q = !has ? 0.0f : (SIGMOID ? sigmoid_scaled(chosen, top) : (chosen == neg_inf() ? 0.0f : exp_of(chosen - top)));
         const float sum = warp_sum(q);
         q = sum == 0.0f ? 0.0f : q / sum;
         add = q * (g - warp_sum(has ? g * q : 0.0f));
@@ -310,39 +400,16 @@ __global__ void __launch_bounds__(kRouterThreads) router_grad_kernel(RouterGradA
       for (int j = 0; j < a.top_k; ++j) {
         const int e = __shfl_sync(0xffffffffu, id, j);
         const float v = __shfl_sync(0xffffffffu, add, j);
+        const int at = (e & 31) == lane ? e >> 5 : -1;   // -1 of a slot without an expert matches no i
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] += lane + 32 * i == e ? v : 0.0f;
-      }
-      if (!SIGMOID && !a.renorm) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] -= p[i] * inner;
+        for (int i = 0; i < V; ++i) d[i] += at == i ? v : 0.0f;
       }
     }
-    if (a.counts != nullptr && any) {
-      const int tokens = a.counts[E];
-      const float per = tokens > 0 ? 1.0f / ((float)a.top_k * (float)tokens) : 0.0f;
-      float f[V], fp = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        f[i] = e < E ? (float)a.counts[e] * per : 0.0f;
-        fp += f[i] * p[i];
-      }
-      fp = warp_sum(fp);
-      const float c = tokens > 0 ? a.dloss[0] * (float)E / (float)tokens : 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float v = c * p[i] * (f[i] - fp);
-        if constexpr (SIGMOID) v *= sigmoid(-l[i]);
-        d[i] += v;
-      }
-    }
-    const float none = row_is_bad<SIGMOID, V>(l) ? __uint_as_float(0x7fc00000u) : 0.0f;
     T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = lane + 32 * i;
-      if (e < E) out[e] = from_f32<T>(live ? d[i] + none : 0.0f);
+      if (e < E) out[e] = from_f32<T>(live ? d[i] - p[i] * inner + none : 0.0f);
     }
   }
   pdl_launch_dependents();
@@ -381,6 +448,11 @@ cudaError_t router_dispatch(int type, int score, int n_experts, F&& f) {
   });
 }
 dim3 token_grid(int64_t ntok) { return dim3((unsigned)((ntok + kRouterWarps - 1) / kRouterWarps)); }
+// CTAs that take tokens in turn: several an SM, so that what they set up first is set up seldom.
+dim3 turn_grid(int64_t ntok) {
+  const int64_t most = 6 * (int64_t)device_sm_count(), n = (ntok + kRouterWarps - 1) / kRouterWarps;
+  return dim3((unsigned)(n < most ? n : most));
+}
 
 }  // namespace
 
@@ -394,14 +466,14 @@ cudaError_t launch_router(const RouterArgs& a) {
 cudaError_t launch_router_grad(const RouterGradArgs& a) {
   return router_dispatch(a.type, a.score, a.n_experts, [&](auto t, auto s, auto v) {
     return launch_pdl(router_grad_kernel<typename decltype(t)::type, decltype(s)::value, decltype(v)::value>,
-                      token_grid(a.ntok), dim3(kRouterThreads), 0, a.stream, a);
+                      turn_grid(a.ntok), dim3(kRouterThreads), 0, a.stream, a);
   });
 }
 
-// CTAs of the first launch: few, so that the second, of one CTA, has few rows to add.
 int balance_parts(int64_t ntok) {
-  const int64_t n = (ntok + 2 * kBalanceWarps - 1) / (2 * kBalanceWarps);
-  return (int)(n < 1 ? 1 : (n > 64 ? 64 : n));
+  if (ntok <= kBalanceAlone) return 1;
+  const int64_t n = (ntok + kBalanceWarps - 1) / kBalanceWarps;
+  return (int)(n < kBalanceParts ? n : kBalanceParts);
 }
 
 cudaError_t launch_balance(const BalanceArgs& a) {
@@ -417,8 +489,22 @@ cudaError_t launch_balance(const BalanceArgs& a) {
     }
     return launch_pdl(kernel, dim3((unsigned)a.parts), dim3(kBalanceThreads), smem, a.stream, a);
   });
-  if (e != cudaSuccess) return e;
-  return launch_pdl(balance_finish_kernel, dim3(1), dim3(1024), 0, a.stream, a);
+  if (e != cudaSuccess || a.parts == 1) return e;
+  const unsigned ctas = (unsigned)((a.n_experts + kFinishCols - 1) / kFinishCols);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kFinishCols * kFinishGroups);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.stream != nullptr ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, balance_finish_kernel, a);
 }
 
 }  // namespace qmv
