@@ -177,10 +177,11 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(RouterArgs a) {
 // takes needs no second launch. Slots and tokens are counted in integers, so
 // that every sum is the same every run.
 // ---------------------------------------------------------------------------
-constexpr int kBalanceThreads = 512;
-constexpr int kBalanceWarps = kBalanceThreads / 32;
+// Warps of a CTA: as many as have the registers for V sums, shares and logits a lane.
+template <int V>
+constexpr int kBalanceWarps = V <= 8 ? 32 : 16;
 constexpr int kBalanceAlone = 64;      // tokens that one CTA takes alone
-constexpr int kBalanceParts = 304;     // CTAs of the first launch at most: two an SM
+constexpr int kBalanceParts = 152;     // CTAs of the first launch at most: one an SM
 constexpr int kFinishCols = 128, kFinishGroups = 8;
 
 // Sum over the CTA's threads, in all of them; scratch: one number a warp.
@@ -193,20 +194,21 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
 }
 
 template <typename T, bool SIGMOID, int V>
-__global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(kBalanceWarps<V> * 32) balance_kernel(BalanceArgs a) {
+  constexpr int kWarps = kBalanceWarps<V>, kThreads = kWarps * 32;
   extern __shared__ float sums[];   // [warps][E], then counts [E + 1]
-  __shared__ float scratch[kBalanceWarps];
+  __shared__ float scratch[kWarps];
   const int E = a.n_experts;
-  int* counts = reinterpret_cast<int*>(sums + kBalanceWarps * E);
+  int* counts = reinterpret_cast<int*>(sums + kWarps * E);
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  for (int i = threadIdx.x; i <= E; i += kBalanceThreads) counts[i] = 0;
+  for (int i = threadIdx.x; i <= E; i += kThreads) counts[i] = 0;
   __syncthreads();
   pdl_wait();
   float mine[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) mine[i] = 0.0f;
   int live_tokens = 0;
-  const int64_t stride = (int64_t)gridDim.x * kBalanceWarps;
+  const int64_t stride = (int64_t)gridDim.x * kWarps;
   // the next token's logits are on their way while this one's are added
   int64_t t = (int64_t)warp * gridDim.x + blockIdx.x;
   float next[V];
@@ -234,10 +236,10 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_kernel(BalanceArgs a)
   const bool alone = gridDim.x == 1;
   const int tokens = counts[E];
   float part_loss = 0.0f;
-  for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
+  for (int e = threadIdx.x; e < E; e += kThreads) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kBalanceWarps; ++w) v += sums[w * E + e];
+    for (int w = 0; w < kWarps; ++w) v += sums[w * E + e];
     if (alone) {
       const float mean = tokens > 0 ? v / (float)tokens : 0.0f;
       a.means[e] = mean;
@@ -402,7 +404,9 @@ __global__ void __launch_bounds__(kRouterThreads) router_grad_kernel(RouterGradA
         const float v = __shfl_sync(0xffffffffu, add, j);
         const int at = (e & 31) == lane ? e >> 5 : -1;   // -1 of a slot without an expert matches no i
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] += at == i ? v : 0.0f;
+        for (int i = 0; i < V; ++i) {
+          if (at == i) d[i] += v;
+        }
       }
     }
     T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
@@ -472,22 +476,23 @@ cudaError_t launch_router_grad(const RouterGradArgs& a) {
 
 int balance_parts(int64_t ntok) {
   if (ntok <= kBalanceAlone) return 1;
-  const int64_t n = (ntok + kBalanceWarps - 1) / kBalanceWarps;
+  const int64_t n = (ntok + 15) / 16;
   return (int)(n < kBalanceParts ? n : kBalanceParts);
 }
 
 cudaError_t launch_balance(const BalanceArgs& a) {
-  const size_t smem = (size_t)a.n_experts * kBalanceWarps * 4 + (a.n_experts + 1) * 4;
   cudaError_t e = router_dispatch(a.type, a.score, a.n_experts, [&](auto t, auto s, auto v) {
     auto* kernel = balance_kernel<typename decltype(t)::type, decltype(s)::value, decltype(v)::value>;
-    constexpr int most = (32 * decltype(v)::value) * kBalanceWarps * 4 + (32 * decltype(v)::value + 1) * 4;
+    constexpr int warps = kBalanceWarps<decltype(v)::value>;
+    constexpr int most = (32 * decltype(v)::value) * warps * 4 + (32 * decltype(v)::value + 1) * 4;
+    const size_t smem = (size_t)a.n_experts * warps * 4 + (a.n_experts + 1) * 4;
     if constexpr (most > 48 * 1024) {
       g_launch_stage = "cudaFuncSetAttribute";
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return e;
       g_launch_stage = "launch";
     }
-    return launch_pdl(kernel, dim3((unsigned)a.parts), dim3(kBalanceThreads), smem, a.stream, a);
+    return launch_pdl(kernel, dim3((unsigned)a.parts), dim3(warps * 32), smem, a.stream, a);
   });
   if (e != cudaSuccess || a.parts == 1) return e;
   const unsigned ctas = (unsigned)((a.n_experts + kFinishCols - 1) / kFinishCols);
