@@ -196,6 +196,8 @@ def _check(rc: int) -> None:
 
 def _ptr(t) -> Optional[int]:
     """Device/host address of a torch tensor, numpy array or int (None -> NULL)."""
+    if type(t) is torch.Tensor:   # the common case first: a call of ten pointers spends 2 us on the others' checks
+        return t.data_ptr()
     if t is None:
         return None
     if isinstance(t, int):
@@ -394,7 +396,8 @@ def qmv_swiglu_bf16(g, u, h, n: int, stream=None) -> None:
 # Row and gradient outputs that are too small for the call raise QMV_ESIZE.
 
 def _type(dtype) -> int:
-    return TYPES[dtype] if isinstance(dtype, (str, torch.dtype)) else int(dtype)
+    got = TYPES.get(dtype)
+    return got if got is not None else (TYPES[dtype] if isinstance(dtype, (str, torch.dtype)) else int(dtype))
 
 
 def _fmt(fmt) -> int:
@@ -524,7 +527,7 @@ def qmv_moe_prefill_layer(gate_up_desc: WDesc, w_gate_up, down_desc: WDesc, w_do
 # score: "softmax", "sigmoid" or QMV_SCORE_*; live: None or one byte (bool, uint8) a token.
 
 def _score(score) -> int:
-    return SCORES[score] if isinstance(score, str) else int(score)
+    return SCORES[score] if type(score) is str else int(score)
 
 
 def _need(name: str, what: str, t, need: int) -> None:

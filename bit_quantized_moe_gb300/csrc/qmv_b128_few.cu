@@ -13,10 +13,18 @@
 // A step's sum starts from zero and is added in fp32 registers, scaled by its
 // row's scale (one a column here) times its block's, as in qmv_b128_gemm.cu.
 //
+// The rows come as a quantized buffer, by TMA, or as they are (X: their type):
+// where every CTA has one tile and few steps, it quantizes its rows' part of the
+// depth itself while its first weights are on their way, with the arithmetic of
+// the separate launch and instead of it. (Quantized step by step by two warps: 1 x
+// 7168 x 7168 18.8 us with its quantization, in two launches 15.6.)
+//
 // Warps: 0 issues the TMA copies, 1 the MMAs, 4..7 are the epilogue, thread =
-// row of the weights.
+// row of the weights; 2..7 quantize (X) first.
+#include <type_traits>
+
+#include "qmv_b128.cuh"
 #include "qmv_internal.h"
-#include "qmv_rows.cuh"
 #include "qmv_tc.cuh"
 
 namespace qmv {
@@ -26,22 +34,35 @@ constexpr int kFewAccs = 4;
 constexpr int kFewSplits = 8;          // CTAs of a cluster, at most
 constexpr uint32_t kFewW = 128 * 128;  // bytes of weights of a step
 
-template <int BN>
+constexpr int kFewQuantSteps = 16;     // X: steps of a CTA, at most
+constexpr int kFewQuantWarps = 6;
+// X: blocks of 128 columns of a CTA, at most (of equally full experts). 4 a CTA 6.8 us with the product, in two launches
+// 8.4; 64: 8.6 and 8.4; 192: 22.9 and 16.7 (1 and 16 x 2880 x 2880, 16 x 7168 x 7168).
+constexpr int kFewQuantUnits = 48;
+
+// X: the rows' codes of all steps lie beside the ring, which holds weights only.
+template <int BN, bool QUANT>
 struct Few {
   static constexpr int ctas = 2;   // of an SM
-  static constexpr int stages = BN == 16 ? 5 : 4;
+  static constexpr int stages = BN == 16 && !QUANT ? 5 : 4;
   static constexpr uint32_t x_bytes = BN * 128;
-  static constexpr uint32_t stage_bytes = kFewW + x_bytes;
+  static constexpr uint32_t stage_bytes = kFewW + (QUANT ? 0 : x_bytes);
+  static constexpr uint32_t quant_bytes = QUANT ? kFewQuantSteps * (x_bytes + BN * 4) : 0;
   static constexpr uint32_t join_bytes = BN * 128 * 4;
   static constexpr uint32_t scale_bytes = 4 * BN * 4;   // a warp's scales of a step
   static constexpr uint32_t tmem_cols = kFewAccs * BN;
   static constexpr size_t smem(int n_experts) {
-    return 1024 + (size_t)stages * stage_bytes + join_bytes + scale_bytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
+    return 1024 + (size_t)stages * stage_bytes + quant_bytes + join_bytes + scale_bytes +
+           2 * ((size_t)n_experts + 1) * sizeof(int);
   }
   static_assert(ctas * (smem(256) + 1536) <= 228 * 1024 && smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
 };
 
 struct FewParams {
+  const void* x;              // X: the rows
+  int64_t ldx;
+  bool x_vec;                 // X: every row starts on a 16-byte boundary
+  int K;
   const float4* sx;           // scales of the rows [nrows][blocks of depth, rounded up to 4]
   const float* sw;            // scales of the weights [E][ceil(N / 128)][ceil(K / 128)]
   const int32_t* offsets;
@@ -112,20 +133,23 @@ __device__ __forceinline__ void few_store(const FewParams& p, int64_t at, float 
   else static_cast<float*>(p.y)[at] = v;
 }
 
-// DX: the weights' outputs are their columns, read transposed.
-template <int BN, bool DX>
-__global__ void __launch_bounds__(kFewThreads, Few<BN>::ctas)
+// DX: the weights' outputs are their columns, read transposed. X: element type of rows to quantize, or void.
+template <int BN, bool DX, typename X>
+__global__ void __launch_bounds__(kFewThreads, 2)
 b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ FewParams p) {
-  using F = Few<BN>;
+  constexpr bool kQuant = !std::is_void_v<X>;
+  using F = Few<BN, kQuant>;
   constexpr int kStages = F::stages;
   extern __shared__ uint8_t dyn[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
-  float* join = reinterpret_cast<float*>(stages + kStages * F::stage_bytes);   // [BN][128] this CTA's sums
+  uint8_t* quant = stages + kStages * F::stage_bytes;                         // X: [kFewQuantSteps][BN][128] codes
+  float* quant_scales = reinterpret_cast<float*>(quant + (kQuant ? kFewQuantSteps * F::x_bytes : 0));   // [kFewQuantSteps][BN]
+  float* join = reinterpret_cast<float*>(quant + F::quant_bytes);             // [BN][128] this CTA's sums
   float* scales = join + BN * 128;                                            // [4 warps][BN]
   int* first_tile = reinterpret_cast<int*>(scales + 4 * BN);
   int* first_row = first_tile + p.n_experts + 1;
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kFewAccs], acc_empty[kFewAccs], joined, joint_read, done;
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kFewAccs], acc_empty[kFewAccs], joined, joint_read, done, quantized;
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), splits = cluster_size();
@@ -135,6 +159,7 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       mbar_init(smem_addr(&full[i]), 1);
       mbar_init(smem_addr(&empty[i]), 1);
     }
+    mbar_init(smem_addr(&quantized), kFewQuantWarps);
     for (int i = 0; i < kFewAccs; ++i) {
       mbar_init(smem_addr(&acc_full[i]), 1);
       mbar_init(smem_addr(&acc_empty[i]), 4);
@@ -161,6 +186,65 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   const int s0 = min(rank * p.per_split, p.steps), s1 = min(s0 + p.per_split, p.steps);   // this rank's steps
   bool ok = true;
 
+  if constexpr (kQuant) {
+    // ---- the rows of all of this CTA's steps: a warp takes a row's 128 columns of a step, lane = four of them; eight
+    // such units' loads are under way together. Only the tile's own rows: the others' columns are not stored, whatever
+    // they hold.
+    if (warp >= 2 && t0 < tiles) {
+      static_assert(sizeof(X) == 2, "8 bytes a lane");
+      const FewTile tile = few_tile<BN>(t0, p, first_tile, first_row);
+      const int rows = min(tile.rows, BN), units = rows * (s1 - s0);
+      constexpr int kTogether = 8;
+      for (int u0 = warp - 2; u0 < units; u0 += kFewQuantWarps * kTogether) {
+        uint2 v[kTogether];
+        uint32_t top[kTogether];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          const int u = u0 + i * kFewQuantWarps, step = u / rows, row = u - step * rows;
+          const int c = (s0 + step) * 128 + lane * 4;
+          const X* x = static_cast<const X*>(p.x) + (int64_t)(tile.row0 + row) * p.ldx + c;
+          v[i] = make_uint2(0, 0);
+          if (u < units && c < p.K) {
+            if (p.x_vec) {   // K is a multiple of 16
+              v[i] = *reinterpret_cast<const uint2*>(x);
+            } else {
+              X e[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) e[k] = x[k];
+              v[i] = *reinterpret_cast<const uint2*>(e);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          const X* e = reinterpret_cast<const X*>(&v[i]);
+          uint32_t m = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = max(m, __float_as_uint(to_f32(e[k])) & 0x7fffffffu);
+          top[i] = __reduce_max_sync(0xffffffffu, m);
+        }
+        uint32_t mine = 0;   // lane i: the maximum of unit i, whose scale it works out
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) mine = lane == i ? top[i] : mine;
+        const BlockScale scale = block_scale(mine);
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          const int u = u0 + i * kFewQuantWarps, step = u / rows, row = u - step * rows;
+          const float inverse = __shfl_sync(0xffffffffu, scale.inverse, i), s = __shfl_sync(0xffffffffu, scale.scale, i);
+          if (u < units) {
+            const X* e = reinterpret_cast<const X*>(&v[i]);
+            // rows of 128 bytes as the TMA copies lay them: 16-byte pieces exchanged by the row's place among eight
+            *reinterpret_cast<uint32_t*>(quant + step * F::x_bytes + row * 128 + ((lane / 4) ^ (row & 7)) * 16 + (lane & 3) * 4) =
+                codes4(to_f32(e[0]), to_f32(e[1]), to_f32(e[2]), to_f32(e[3]), inverse);
+            if (lane == 0) quant_scales[step * BN + row] = s;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_one(smem_addr(&quantized));
+    }
+  }
   if (warp == 0) {
     // ---- copies
     int it = 0, st = 0;
@@ -179,7 +263,7 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
           mbar_arrive_expect_tx(bar, F::stage_bytes);
           if constexpr (DX) tma_load_3d(w, &map_w, tile.n, s * 128, tile.expert, bar);
           else tma_load_3d(w, &map_w, s * 128, tile.n, tile.expert, bar);
-          tma_load_2d<false>(w + kFewW, &map_x, s * 128, tile.row0, bar);
+          if constexpr (!kQuant) tma_load_2d<false>(w + kFewW, &map_x, s * 128, tile.row0, bar);
         }
         __syncwarp();
         if (++st == kStages) st = 0;
@@ -200,7 +284,8 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const int total = my_tiles * (s1 - s0);
     int st = 0;
     uint32_t st_phase = 0;
-    for (int it = 0; it < total; ++it) {
+    if (kQuant && total > 0 && !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&quantized), 0))) ok = false;
+    for (int it = 0; it < total && ok; ++it) {
       const int acc = it % kFewAccs;
       if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_empty[acc]), ((it / kFewAccs) & 1) ^ 1)) ||
           !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&full[st]), st_phase))) {
@@ -208,7 +293,8 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         break;
       }
       tc_after_sync();
-      const uint32_t w = smem_addr(stages) + (uint32_t)st * F::stage_bytes, x = w + kFewW;
+      const uint32_t w = smem_addr(stages) + (uint32_t)st * F::stage_bytes;
+      const uint32_t x = kQuant ? smem_addr(quant) + (uint32_t)it * F::x_bytes : w + kFewW;   // X: one tile
       const uint32_t d = tm + (uint32_t)(acc * BN);
       if (elect_one()) {
 #pragma unroll
@@ -248,7 +334,7 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       float w32 = 0.0f;
       const float4* sx[kEach];
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
+      for (int i = 0; i < (kQuant ? 0 : kEach); ++i) {
         sx[i] = p.sx + min((int64_t)tile.row0 + lane + 32 * i, p.nrows - 1) * p.x_quads;
         next4[i] = s0 < s1 ? sx[i][s0 / 4] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         x4[i] = next4[i];
@@ -258,7 +344,7 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       for (float& v : sum) v = 0.0f;
       for (int s = s0; s < s1; ++s, ++it) {
         const int acc = it % kFewAccs;
-        if (s == s0 || s % 4 == 0) {
+        if (!kQuant && (s == s0 || s % 4 == 0)) {
 #pragma unroll
           for (int i = 0; i < kEach; ++i) {
             x4[i] = next4[i];
@@ -267,10 +353,14 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         }
         if ((s - s0) % 32 == 0) w32 = sw[min(s + lane, s1 - 1) * sw_stride];
         const float w = __shfl_sync(0xffffffffu, w32, (s - s0) & 31);
+        if (kQuant && s == s0 && !__all_sync(0xffffffffu, wait_for<false>(smem_addr(&quantized), 0))) {
+          ok = false;
+          break;
+        }
         __syncwarp();   // the step before has been read
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          const float x = (s & 2) ? ((s & 1) ? x4[i].w : x4[i].z) : ((s & 1) ? x4[i].y : x4[i].x);
+          const float x = kQuant ? quant_scales[(s - s0) * BN + (lane & (BN - 1))] : (s & 2) ? ((s & 1) ? x4[i].w : x4[i].z) : ((s & 1) ? x4[i].y : x4[i].x);
           if (BN >= 32 || lane < BN) mine[lane + 32 * i] = x * w;
         }
         __syncwarp();
@@ -356,13 +446,21 @@ QMV_DEFINE_STATUS_ACCESSOR(status_b128_few)
 
 namespace {
 
-template <int BN, bool DX>
+template <int BN, bool DX, typename X>
 cudaError_t few_go(const B128GemmArgs& a) {
-  using F = Few<BN>;
-  auto* kernel = b128_few_kernel<BN, DX>;
+  constexpr bool kQuant = !std::is_void_v<X>;
+  using F = Few<BN, kQuant>;
+  auto* kernel = b128_few_kernel<BN, DX, X>;
   const int depth = DX ? a.N : a.K;
   FewParams p = {};
-  p.sx = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(a.xq) + b128_scale_offset(a.nrows, depth));
+  if constexpr (kQuant) {
+    p.x = a.x;
+    p.ldx = a.ldx;
+    p.x_vec = a.ldx % (16 / (int64_t)sizeof(X)) == 0;
+  } else {
+    p.sx = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(a.xq) + b128_scale_offset(a.nrows, depth));
+  }
+  p.K = a.K;
   p.sw = a.w_scales;
   p.offsets = a.offsets;
   p.y = a.y;
@@ -387,7 +485,9 @@ cudaError_t few_go(const B128GemmArgs& a) {
     const cuuint32_t box[3] = {128, 128, 1};
     if (!encode(&mw, 3, a.w, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  {
+  if constexpr (kQuant) {
+    mx = mw;
+  } else {
     const cuuint64_t row = b128_row_bytes(depth);
     const cuuint64_t dims[2] = {row, (cuuint64_t)a.nrows}, strides[1] = {row};
     const cuuint32_t box[2] = {128, BN};
@@ -429,6 +529,11 @@ cudaError_t few_go(const B128GemmArgs& a) {
   }
   if (most < 1) return cudaErrorInvalidConfiguration;
   p.per_split = (p.steps + splits - 1) / splits;
+  if (kQuant) {
+    const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
+    const bool fits = most >= tiles && p.per_split <= kFewQuantSteps;
+    if (!fits || (a.nrows + hit - 1) / hit * p.per_split > kFewQuantUnits) return cudaErrorNotSupported;   // nothing is launched
+  }
   g_launch_stage = "launch";
   cfg.gridDim = dim3((unsigned)(splits * (tiles < most ? tiles : most)));
   cfg.numAttrs = a.stream != nullptr ? 2 : 1;
@@ -438,10 +543,16 @@ cudaError_t few_go(const B128GemmArgs& a) {
 template <bool DX>
 cudaError_t few_by_rows(const B128GemmArgs& a) {
   const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
-  return a.nrows <= 16 * hit ? few_go<16, DX>(a) : few_go<32, DX>(a);
+  return a.nrows <= 16 * hit ? few_go<16, DX, void>(a) : few_go<32, DX, void>(a);
 }
 
 }  // namespace
+
+cudaError_t launch_b128_few_linear(const B128GemmArgs& a) {
+  const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
+  if (a.x_type == QMV_F32 || a.nrows > 16 * hit) return cudaErrorNotSupported;
+  return a.x_type == QMV_BF16 ? few_go<16, false, __nv_bfloat16>(a) : few_go<16, false, __half>(a);
+}
 
 cudaError_t launch_b128_few(const B128GemmArgs& a, bool dx) { return dx ? few_by_rows<true>(a) : few_by_rows<false>(a); }
 

@@ -693,6 +693,23 @@ bool few_rows(const B128GemmArgs& a, int depth, int out_n) {
 }  // namespace
 
 cudaError_t launch_b128_product(const B128GemmArgs& a) { return few_rows(a, a.K, a.N) ? launch_b128_few(a, false) : product_go<kModeY>(a); }
+cudaError_t launch_b128_linear(const B128GemmArgs& a) {
+  if (few_rows(a, a.K, a.N)) {
+    const cudaError_t e = launch_b128_few_linear(a);
+    if (e != cudaErrorNotSupported) return e;
+    g_launch_stage = "launch";
+  }
+  B128QuantArgs q;
+  q.type = a.x_type;
+  q.x = a.x;
+  q.ldx = a.ldx;
+  q.nrows = a.nrows;
+  q.K = a.K;
+  q.xq = const_cast<void*>(a.xq);
+  q.stream = a.stream;
+  const cudaError_t e = launch_quantize_b128(q);
+  return e != cudaSuccess ? e : launch_b128_product(a);
+}
 cudaError_t launch_b128_grad_x(const B128GemmArgs& a) { return few_rows(a, a.N, a.K) ? launch_b128_few(a, true) : product_go<kModeDx>(a); }
 
 cudaError_t launch_b128_grad_w(const B128GradWArgs& a) {

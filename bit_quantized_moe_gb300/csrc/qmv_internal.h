@@ -237,6 +237,9 @@ struct B128GemmArgs {
   const void* w = nullptr;            // codes [E][N][K]
   const float* w_scales = nullptr;    // [E][ceil(N / 128)][ceil(K / 128)]
   const void* xq = nullptr;           // activation buffer of K (y) or N (dx) columns
+  const void* x = nullptr;            // launch_b128_linear: the rows to quantize into xq, or in the product itself
+  int64_t ldx = 0;
+  int x_type = 0;
   int64_t nrows = 0;
   const int32_t* offsets = nullptr;   // [E + 1]; null: every row, expert 0
   int out_type = 0;
@@ -244,9 +247,12 @@ struct B128GemmArgs {
   cudaStream_t stream = nullptr;
 };
 cudaError_t launch_b128_product(const B128GemmArgs& a);
+cudaError_t launch_b128_linear(const B128GemmArgs& a);
 cudaError_t launch_b128_grad_x(const B128GemmArgs& a);
 // Few rows of an expert (qmv_b128_few.cu); dx: grad_x.
 cudaError_t launch_b128_few(const B128GemmArgs& a, bool dx);
+// With the quantization of 16-bit rows in the same launch; cudaErrorNotSupported, and no launch, where that does not fit.
+cudaError_t launch_b128_few_linear(const B128GemmArgs& a);
 
 struct B128GradWArgs {
   int type = 0;                       // of dy and x, 16 bits

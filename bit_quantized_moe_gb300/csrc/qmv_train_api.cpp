@@ -266,9 +266,11 @@ int qmv_b128_linear(const void* w, const float* w_scales, int32_t n_experts, int
   if (any_null(x)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (nrows == 0) return done();
-  QMV_TRY(qmv_quantize_act_b128(type, x, ldx, nrows, K, workspace, workspace_bytes, stream));
+  g.x = x;
+  g.ldx = ldx;
+  g.x_type = type;
   g_launch_stage = "launch";
-  return launched(launch_b128_product(g), name);
+  return launched(launch_b128_linear(g), name);
 }
 
 int qmv_b128_grad_x(const void* w, const float* w_scales, int32_t n_experts, int32_t N, int32_t K, const void* dyq,

@@ -692,8 +692,9 @@ int qmv_quantize_weights_b128(int32_t type, const void* w_dev, int32_t n_experts
  * Scales may be any fp32; where the product of two leaves fp32's range, so do y's terms.
  *
  * qmv_b128_linear quantizes rows x (`type`, ldx apart) and multiplies: y has the
- * type of x. workspace: qmv_b128_linear_workspace_bytes(...) bytes of device
- * scratch; calls that share one must be ordered on one stream.
+ * type of x. Few rows are quantized within the product's launch. workspace:
+ * qmv_b128_linear_workspace_bytes(...) bytes of device scratch, whose contents
+ * afterwards are not specified; calls that share one must be ordered on one stream.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
  */
 int qmv_b128_product(const void* w_dev, const float* w_scales_dev, int32_t n_experts, int32_t N, int32_t K,

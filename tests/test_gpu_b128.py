@@ -177,8 +177,9 @@ def test_linear_and_gradients_of_random_numbers(out, rows, N, K):
     y, ws = torch.empty(rows, N, dtype=TORCH[act], device=DEV), buf(qmv.qmv_b128_linear_workspace_bytes(rows, K))
     qmv.qmv_b128_linear(codes, scales, 1, N, K, act, x, K, rows, None, ws, y)
     assert_within(host(y), xv @ wv.T, bound(K, np.abs(xv) @ np.abs(wv).T), act, "y")
-    y2 = torch.empty(rows, N, dtype=TORCH[out], device=DEV)
-    qmv.qmv_b128_product(codes, scales, 1, N, K, ws, rows, None, out, y2)
+    y2, xq = torch.empty(rows, N, dtype=TORCH[out], device=DEV), buf(qmv.qmv_act_b128_bytes(rows, K))
+    qmv.qmv_quantize_act_b128(act, x, K, rows, K, xq)
+    qmv.qmv_b128_product(codes, scales, 1, N, K, xq, rows, None, out, y2)
     assert_within(host(y2), xv @ wv.T, bound(K, np.abs(xv) @ np.abs(wv).T), out, "y")
     dyq, dx = buf(qmv.qmv_act_b128_bytes(rows, N)), torch.empty(rows, K, dtype=TORCH[out], device=DEV)
     qmv.qmv_quantize_act_b128(act, dy[0], dy[1], rows, N, dyq)
@@ -190,6 +191,45 @@ def test_linear_and_gradients_of_random_numbers(out, rows, N, K):
     d = host(dy[0][:, :N])
     assert_within(host(dw), d.T @ host(x), bound(rows, np.abs(d).T @ np.abs(host(x))), out, "dw")
     assert status_clean()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,N,K,extra", [(1, 7, 16, 0), (1, 300, 2880, 3), (3, 129, 400, 1), (16, 2880, 288, 8), (15, 130, 7168, 0), (9, 64, 144, 5)])
+def test_linear_is_quantize_and_product(dtype, rows, N, K, extra):
+    """Rows quantized within the product's launch give the bits of the two calls; special blocks among them, any stride."""
+    g = qi.rng(rows + N)
+    wc, ws = exact_weights(g, 1, N, K)
+    v = randn(rows + K, rows, K)
+    v[0, :min(K, 128)] = 0
+    v[-1, 0] = 3e4
+    if rows > 3:
+        v[1, 3], v[2, K - 1], v[3, 5] = np.nan, np.inf, -np.inf
+    x, ld = strided(v, dtype, extra)
+    w, wsd = dev(wc), dev(ws, "f32")
+    y, y2 = torch.full((rows + 1, N), 7.0, dtype=TORCH[dtype], device=DEV), torch.empty(rows, N, dtype=TORCH[dtype], device=DEV)
+    space = buf(qmv.qmv_b128_linear_workspace_bytes(rows, K))
+    qmv.qmv_b128_linear(w, wsd, 1, N, K, dtype, x, ld, rows, None, space, y)
+    xq = buf(qmv.qmv_act_b128_bytes(rows, K))
+    qmv.qmv_quantize_act_b128(dtype, x, ld, rows, K, xq)
+    qmv.qmv_b128_product(w, wsd, 1, N, K, xq, rows, None, dtype, y2)
+    assert torch.equal(torch.nan_to_num(y[:rows], 123.0), torch.nan_to_num(y2, 123.0)) and torch.equal(y[:rows].isnan(), y2.isnan())
+    assert (y[rows] == 7.0).all() and status_clean()
+
+
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0], [16, 0, 17, 1], [0, 40, 2, 0, 0, 7], [0, 0], [1] * 40])
+def test_grouped_linear_is_quantize_and_product(counts):
+    E, N, K, tail = len(counts), 200, 1184, 2
+    rows = sum(counts) + tail
+    g = qi.rng(rows)
+    wc, ws = exact_weights(g, E, N, K)
+    x = dev(randn(rows, rows, K), "bf16")
+    offsets = dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    y, y2 = (torch.full((rows, N), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    qmv.qmv_b128_linear(dev(wc), dev(ws, "f32"), E, N, K, "bf16", x, K, rows, offsets, buf(qmv.qmv_b128_linear_workspace_bytes(rows, K)), y)
+    xq = buf(qmv.qmv_act_b128_bytes(rows, K))
+    qmv.qmv_quantize_act_b128("bf16", x, K, rows, K, xq)
+    qmv.qmv_b128_product(dev(wc), dev(ws, "f32"), E, N, K, xq, rows, offsets, "bf16", y2)
+    assert torch.equal(y, y2) and status_clean()
 
 
 def grouped(counts, N, K, tail, seed):
