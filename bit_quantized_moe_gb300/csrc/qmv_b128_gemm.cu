@@ -22,6 +22,16 @@
 //
 // Warps: 0 issues the TMA copies, 1 (of the pair's first CTA) the MMAs, 2 clears
 // the rows behind an expert's last one (dW), 4..11 are the epilogue.
+//
+// What bounds y and dx: the epilogue beside the tensor cores. 8192 x 7168 x 7168:
+// MMAs alone 185 us, with the copies 220, with the epilogue's barriers 224, with
+// its loads of tensor memory 244, its additions 291, its scales 320, its stores
+// 345; with two loads out at once, and the sum released when half of it has been
+// added, 327 (2.6 PFLOP/s, 0.58 of the nominal rate). Tried and slower: four half
+// sums of 128 columns (413), 16 epilogue warps of 64 columns (353), the scales
+// through shared memory (384 to 433), loads of 16 columns one by one (357).
+// dW is bound by the copies and, over experts of few rows, by its output (32 x 2880
+// x 2880 from 16,384 rows: 377 us, 1.06 GB written; filling that takes 142).
 #include <cmath>
 #include <type_traits>
 
@@ -34,7 +44,8 @@ namespace qmv {
 enum : int { kModeY = 0, kModeDx = 1, kModeDw = 2 };
 
 // Steps whose MMAs add to one sum in tensor memory. y and dx: one, whose scales follow. dW has none: 512 rows, so that the
-// tensor cores' truncating additions stay few (8 steps: within 1e-6 of the sum of magnitudes) and the epilogue seldom.
+// tensor cores' truncating additions stay few (measured: within 3e-7 of the sum of magnitudes, 5e-7 of the matrix's norm)
+// and the epilogue seldom (8192 x 7168 x 7168 582 -> 472 us).
 template <int MODE>
 constexpr int kGroup = MODE == kModeDw ? 8 : 1;
 
@@ -54,12 +65,10 @@ constexpr size_t pair_smem(int n_experts) {
   return 1024 + (size_t)kPairStages * kStageBytes + kParkBytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
 }
 static_assert(pair_smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
-// Registers of an epilogue thread and of the others: 256 * 216 + 128 * 72 = 384 * 168, what the launch gives.
-template <int MODE>
-struct PairRegs {
-  static constexpr int epilogue = 232, other = 40;
-  static_assert(256 * epilogue + 128 * other <= kPairThreads * 168, "what the launch gives");
-};
+// Registers of an epilogue thread and of the others, within the 168 a thread that the launch gives. (Any spilled register
+// is in the steps' way: with 216 and 72 a kernel that spilled 80 bytes took 414 us instead of 345.)
+constexpr int kEpiRegs = 232, kOtherRegs = 40;
+static_assert(256 * kEpiRegs + 128 * kOtherRegs <= kPairThreads * 168, "what the launch gives");
 
 struct PairParams {
   const float4* sx;           // scales of the rows [nrows][blocks of depth, rounded up to 4]
@@ -337,7 +346,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   bool ok = true;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PairRegs<MODE>::other));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
     const auto tile_of = [&](int t) {   // the same in all lanes, and known to be
       PairTile r = pair_tile<MODE>(t, p, first_tile, first_row, rank);
@@ -475,7 +484,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
   } else {
     // ---- epilogue: thread = row 32 (warp % 4) + lane, columns 128 * half on
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PairRegs<MODE>::epilogue));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int quad = warp % 4, half = (warp - 4) / 4;
     const int r = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;

@@ -3,12 +3,13 @@
     python examples/moe_block.py [--tokens 512] [--hidden 2880] [--inner 2880] [--experts 32] [--top-k 4] [--fmt mxfp4]
 
 1. Prompt: the residual's addition and the RMS norm, the router, and the expert layer on all tokens
-   (qmv_rms_norm, qmv_moe_prefill_layer).
+   (qmv_rms_norm, qmv_moe_router, qmv_moe_prefill_layer).
 2. Decode: the next token through the same weights (qmv_moe_layer_combine). The two agree to the prompt
    path's quantization of the activations.
 3. A training step's routing: a trainable map in the experts' place between the dispatch and the weighted
    return, its gradient, the router weights' and the input's (qmv_moe_sort, qmv_moe_dispatch,
-   qmv_moe_return and their gradients; the experts' own input gradients are not among the calls).
+   qmv_moe_return and their gradients; the MX experts' own input gradients are not among the calls),
+   the balance loss, and the logits' gradient from both (qmv_moe_balance, qmv_moe_router_grad).
 """
 import argparse
 import os
@@ -55,8 +56,23 @@ class Block:
         self.router = (torch.randn(a.experts, a.hidden, generator=g, device=DEV) / a.hidden ** 0.5).bfloat16()
 
     def route(self, normed):
-        value, ids = torch.topk(normed @ self.router.T, self.top_k, dim=1)
-        return ids.to(torch.int32), torch.softmax(value.float(), 1)
+        """(expert ids, their weights, logits) of each token."""
+        logits = normed @ self.router.T
+        tokens = logits.shape[0]
+        ids, weights = empty(tokens, self.top_k, dtype=torch.int32), empty(tokens, self.top_k, dtype=torch.float32)
+        qmv.qmv_moe_router("bf16", logits, self.experts, None, tokens, self.experts, self.top_k, "softmax", True, 1.0, ids, weights)
+        return ids, weights, logits
+
+    def router_gradient(self, logits, ids, dweights, share):
+        """(balance loss, gradient of the logits from the weights' and from share times that loss)."""
+        tokens, experts, top_k = logits.shape[0], self.experts, self.top_k
+        counts, means, loss = empty(experts + 1, dtype=torch.int32), empty(experts, dtype=torch.float32), empty(1, dtype=torch.float32)
+        ws = empty(qmv.qmv_moe_balance_workspace_bytes(tokens, experts), dtype=torch.uint8)
+        qmv.qmv_moe_balance("bf16", logits, experts, None, ids, tokens, experts, top_k, "softmax", counts, means, loss, ws)
+        dlogits = torch.empty_like(logits)
+        qmv.qmv_moe_router_grad("bf16", logits, experts, None, ids, dweights, counts, torch.full_like(loss, share), tokens, experts,
+                                top_k, "softmax", True, 1.0, dlogits, experts)
+        return loss, dlogits
 
     def norm(self, x, residual):
         """(normed, x + residual) of rows x."""
@@ -67,7 +83,7 @@ class Block:
 
     def prompt(self, x, residual):
         normed, total = self.norm(x, residual)
-        ids, weights = self.route(normed)
+        ids, weights, _ = self.route(normed)
         tokens = x.shape[0]
         ws = empty(qmv.qmv_moe_prefill_layer_workspace_bytes(self.gate_up, self.down, tokens, self.top_k), dtype=torch.uint8)
         y = empty(tokens, self.hidden)
@@ -78,7 +94,7 @@ class Block:
     def decode(self, x, residual):
         """Up to 16 tokens with bf16 activations."""
         normed, total = self.norm(x, residual)
-        ids, weights = self.route(normed)
+        ids, weights, _ = self.route(normed)
         tokens = x.shape[0]
         ws = empty(qmv.qmv_moe_layer_combine_workspace_bytes(self.gate_up, self.down, tokens, self.top_k), dtype=torch.uint8)
         y = empty(tokens, self.hidden)
@@ -130,9 +146,10 @@ class Returned(torch.autograd.Function):
 
 
 def training_step(block, x, target):
-    """Loss and gradients of a scale per column on the experts' rows, of the router's weights and of x."""
+    """Loss and gradients of a scale per column on the experts' rows, of the router's weights, of x and of the logits (with a
+    hundredth of the balance loss), and that loss."""
     tokens, experts, top_k = x.shape[0], block.experts, block.top_k
-    ids, weights = block.route(x)
+    ids, weights, logits = block.route(x)
     i32 = torch.int32
     offsets, row_of_slot, slot_of_row = empty(experts + 1, dtype=i32), empty(tokens * top_k, dtype=i32), empty(tokens * top_k, dtype=i32)
     qmv.qmv_moe_sort(ids, tokens, top_k, experts, offsets, row_of_slot, slot_of_row)
@@ -141,7 +158,8 @@ def training_step(block, x, target):
     y = Returned.apply(Routed.apply(x, row_of_slot, top_k) * scale, weights, row_of_slot)
     loss = (y.float() - target.float()).square().mean()
     loss.backward()
-    return loss.detach(), scale.grad, weights.grad, x.grad
+    balance, dlogits = block.router_gradient(logits, ids, weights.grad, 0.01)
+    return loss.detach(), scale.grad, weights.grad, x.grad, dlogits, balance
 
 
 def main(argv=None):
@@ -158,13 +176,14 @@ def main(argv=None):
     y1, _ = block.decode(x[:few].contiguous(), residual[:few].contiguous())
     apart = ((y[:few].float() - y1.float()).norm() / y1.float().norm()).item()
     print(f"prompt: {a.tokens} tokens; the first {few} through the decode layer differ by {apart:.3f} (activations in {a.fmt})")
-    loss, dscale, dweights, dx = training_step(block, total, y)
+    loss, dscale, dweights, dx, dlogits, balance = training_step(block, total, y)
     print(f"training step: loss {loss.item():.4f}, |d scale| {dscale.float().norm().item():.4f}, "
-          f"|d weights| {dweights.norm().item():.4f}, |dx| {dx.float().norm().item():.4f}")
+          f"|d weights| {dweights.norm().item():.4f}, |dx| {dx.float().norm().item():.4f}, "
+          f"balance loss {balance.item():.4f}, |d logits| {dlogits.float().norm().item():.4f}")
     status = qmv.qmv_device_status(clear=True)
     if status:
         raise SystemExit(f"device status {status}")
-    return apart, loss.item(), (dscale, dweights, dx)
+    return apart, loss.item(), (dscale, dweights, dx, dlogits)
 
 
 if __name__ == "__main__":
