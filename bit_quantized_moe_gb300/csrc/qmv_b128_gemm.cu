@@ -27,7 +27,10 @@
 // MMAs alone 185 us, with the copies 220, with the epilogue's barriers 224, with
 // its loads of tensor memory 244, its additions 291, its scales 320, its stores
 // 345; with two loads out at once, and the sum released when half of it has been
-// added, 327 (2.6 PFLOP/s, 0.58 of the nominal rate). Tried and slower: four half
+// added, 330; with the loads of scales behind that release, and a tile's first
+// before the stores of the one before, 294 (2.86 PFLOP/s, 0.64 of the nominal
+// rate). Tried and slower: the next step's first loads of tensor memory before the
+// last additions (337), the next step's scale there (304), four half
 // sums of 128 columns (413), 16 epilogue warps of 64 columns (353), the scales
 // through shared memory (384 to 433), loads of 16 columns one by one (357).
 // dW is bound by the copies and, over experts of few rows, by its output (32 x 2880
@@ -118,22 +121,7 @@ __device__ __forceinline__ void mbar_expect_pair(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// 16 accumulator columns of this thread's row; not used before tmem_ld_wait16.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :: "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // As mbar_wait_bounded, without a hint to sleep.
@@ -490,25 +478,33 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     uint8_t* warp_park = park + (uint32_t)(warp - 4) * 32 * kParkPitch;
     int it = 0;
-    for (int t = t0; t < tiles && ok; t += dt) {
-      // The scales: the row's four steps at a time, a load ahead; the weights' blocks' 32 steps at a time, a lane each.
-      // (A thread's loads under way are waited for with its next load of tensor memory: two loads a step, 8192 x 7168 x
-      // 7168 334 us.)
-      int steps;
-      const float4* sx = nullptr;
-      const float* sw = nullptr;
-      float4 x4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f), next4 = x4;
-      float w32 = 1.0f;
-      {
-        const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
-        steps = (tile.steps + kGroup<MODE> - 1) / kGroup<MODE>;
-        if constexpr (MODE != kModeDw) {
-          sx = p.sx + min((int64_t)tile.row0 + r, p.nrows - 1) * p.x_quads;
-          const int block = min((tile.n + half * kHalf) / kB128, (MODE == kModeY ? p.n_blocks : p.k_blocks) - 1);
-          sw = p.sw + (int64_t)tile.expert * p.n_blocks * p.k_blocks + (MODE == kModeY ? (int64_t)block * p.k_blocks : block);
-          next4 = *sx;
-        }
+    // The scales: the row's four steps at a time, a load ahead; the weights' blocks' 32 steps at a time, a lane each, a load
+    // ahead; a tile's first before the stores of the one before. (A thread's loads under way are waited for with its next
+    // load of tensor memory, so they follow a step's last: before its first, 8192 x 7168 x 7168 took 330 us.)
+    int steps = 0;
+    const float4* sx = nullptr;
+    const float* sw = nullptr;
+    float4 next4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    float next32 = 1.0f;
+    const auto block_scales = [&](int from) {
+      const int at = min(from + lane, steps - 1);
+      return sw[MODE == kModeY ? (int64_t)at : (int64_t)at * p.k_blocks];
+    };
+    const auto begin = [&](int t) {
+      const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
+      steps = (tile.steps + kGroup<MODE> - 1) / kGroup<MODE>;
+      if constexpr (MODE != kModeDw) {
+        sx = p.sx + min((int64_t)tile.row0 + r, p.nrows - 1) * p.x_quads;
+        const int block = min((tile.n + half * kHalf) / kB128, (MODE == kModeY ? p.n_blocks : p.k_blocks) - 1);
+        sw = p.sw + (int64_t)tile.expert * p.n_blocks * p.k_blocks + (MODE == kModeY ? (int64_t)block * p.k_blocks : block);
+        next4 = *sx;
+        next32 = block_scales(0);
       }
+    };
+    if (t0 < tiles) begin(t0);
+    for (int t = t0; t < tiles && ok; t += dt) {
+      float4 x4 = next4;
+      float w32 = next32;
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
@@ -518,11 +514,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         if constexpr (MODE != kModeDw) {
           if (s % 4 == 0) {
             x4 = next4;
-            if (s + 4 < steps) next4 = sx[s / 4 + 1];
-            if (s % 32 == 0) {
-              const int at = min(s + lane, steps - 1);
-              w32 = sw[MODE == kModeY ? (int64_t)at : (int64_t)at * p.k_blocks];
-            }
+            if (s % 32 == 0) w32 = next32;
           }
           const float x = (s & 2) ? ((s & 1) ? x4.w : x4.z) : ((s & 1) ? x4.y : x4.x);
           scale = x * __shfl_sync(0xffffffffu, w32, s & 31);
@@ -558,11 +550,16 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         tc_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(leader_addr(smem_addr(&acc_empty[acc])));   // read
+        if constexpr (MODE != kModeDw) {
+          if (s % 4 == 0 && s + 4 < steps) next4 = sx[s / 4 + 1];
+          if (s % 32 == 31 && s + 1 < steps) next32 = block_scales(s + 1);
+        }
         add(2);
         add(3);
       }
       if (!ok) break;
       asm volatile("" : "+r"(t));   // the tile's place is worked out again, not kept in registers over the steps
+      if (t + dt < tiles) begin(t + dt);
       const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
       const int n0 = tile.n + half * kHalf;   // first column of this thread
       const int64_t row0 = MODE == kModeDw ? (int64_t)tile.expert * p.N + tile.m : (int64_t)tile.row0;   // of the CTA
