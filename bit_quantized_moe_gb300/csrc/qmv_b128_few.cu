@@ -4,11 +4,15 @@
 //
 // Bound by reading the weights once. The weights take the tensor cores' 128
 // rows, the activations' rows their columns (BN of them), so that a step moves
-// 16 KB of weights and 2 or 4 KB of rows. Two CTAs an SM keep a ring of 5 or 4
-// steps under way each. (64 columns, one CTA an SM: slower from 32 rows to 128, by
-// up to a third over experts.) Where there are fewer tiles than
-// SMs, a cluster of CTAs shares a tile's depth and adds its parts in shared
-// memory in the order of the ranks: no workspace, the same bits every run.
+// 16 KB of weights and 2 to 8 KB of rows. Two CTAs an SM keep a ring of 4 or 5
+// steps under way each. Where there are fewer tiles than SMs, a cluster of CTAs
+// shares a tile's depth and adds its parts in shared memory in the order of the
+// ranks: no workspace, the same bits every run.
+//
+// Measured (16, 32, 64 columns for as many rows of an expert): 16 x 7168 x 7168 14.3
+// us, 32 rows 15.6, 64 rows 17.1 (with 32 columns 20.8), 2048 rows of 32 experts of
+// 2880 x 2880 69 (80). 128 columns, one CTA an SM, four groups of epilogue warps: 128 x
+// 7168 x 7168 24.9 (with 64 27.3), but 2048 rows of 32 experts 88.
 //
 // A step's sum starts from zero and is added in fp32 registers, scaled by its
 // row's scale (one a column here) times its block's, as in qmv_b128_gemm.cu.
@@ -19,8 +23,9 @@
 // the separate launch and instead of it. (Quantized step by step by two warps: 1 x
 // 7168 x 7168 18.8 us with its quantization, in two launches 15.6.)
 //
-// Warps: 0 issues the TMA copies, 1 the MMAs, 4..7 are the epilogue, thread =
-// row of the weights; 2..7 quantize (X) first.
+// Warps: 0 issues the TMA copies, 1 the MMAs, 4 and on are the epilogue, thread =
+// row of the weights and 16 or 32 columns; 2..7 quantize (X) first.
+#include <cmath>
 #include <type_traits>
 
 #include "qmv_b128.cuh"
@@ -29,10 +34,15 @@
 
 namespace qmv {
 
-constexpr int kFewThreads = 256;
+constexpr int kFewCtas = 2;            // of an SM
 constexpr int kFewAccs = 4;
-constexpr int kFewSplits = 8;          // CTAs of a cluster, at most
+constexpr int kFewSplits = 6;          // CTAs of a cluster, at most
+constexpr int kFewJoinSteps = 5;       // steps that take as long as the cluster's start and join
 constexpr uint32_t kFewW = 128 * 128;  // bytes of weights of a step
+
+// 64 columns: registers of an epilogue thread and of the others, within the 80 a thread that the launch gives.
+constexpr int kFewEpiRegs = 104, kFewOtherRegs = 32;
+static_assert(256 * kFewEpiRegs + 128 * kFewOtherRegs <= 384 * 80, "what the launch gives");
 
 constexpr int kFewQuantSteps = 16;     // X: steps of a CTA, at most
 constexpr int kFewQuantWarps = 6;
@@ -43,19 +53,20 @@ constexpr int kFewQuantUnits = 48;
 // X: the rows' codes of all steps lie beside the ring, which holds weights only.
 template <int BN, bool QUANT>
 struct Few {
-  static constexpr int ctas = 2;   // of an SM
-  static constexpr int stages = BN == 16 && !QUANT ? 5 : 4;
+  static constexpr int stages = QUANT || BN == 64 ? 4 : 5;
+  static constexpr int groups = BN == 64 ? 2 : 1;   // of four epilogue warps
+  static constexpr int cols = BN / groups;          // columns of a group
+  static constexpr int threads = 128 + 128 * groups;
   static constexpr uint32_t x_bytes = BN * 128;
   static constexpr uint32_t stage_bytes = kFewW + (QUANT ? 0 : x_bytes);
   static constexpr uint32_t quant_bytes = QUANT ? kFewQuantSteps * (x_bytes + BN * 4) : 0;
-  static constexpr uint32_t join_bytes = BN * 128 * 4;
   static constexpr uint32_t scale_bytes = 4 * BN * 4;   // a warp's scales of a step
   static constexpr uint32_t tmem_cols = kFewAccs * BN;
   static constexpr size_t smem(int n_experts) {
-    return 1024 + (size_t)stages * stage_bytes + quant_bytes + join_bytes + scale_bytes +
-           2 * ((size_t)n_experts + 1) * sizeof(int);
+    return 1024 + (size_t)stages * stage_bytes + quant_bytes + scale_bytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
   }
-  static_assert(ctas * (smem(256) + 1536) <= 228 * 1024 && smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
+  static_assert(BN * 128 * 4 <= stages * stage_bytes, "the sums to join");
+  static_assert(kFewCtas * (smem(256) + 1536) <= 228 * 1024 && smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
 };
 
 struct FewParams {
@@ -135,7 +146,7 @@ __device__ __forceinline__ void few_store(const FewParams& p, int64_t at, float 
 
 // DX: the weights' outputs are their columns, read transposed. X: element type of rows to quantize, or void.
 template <int BN, bool DX, typename X>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__((Few<BN, false>::threads), kFewCtas)
 b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ FewParams p) {
   constexpr bool kQuant = !std::is_void_v<X>;
@@ -145,11 +156,11 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
   uint8_t* quant = stages + kStages * F::stage_bytes;                         // X: [kFewQuantSteps][BN][128] codes
   float* quant_scales = reinterpret_cast<float*>(quant + (kQuant ? kFewQuantSteps * F::x_bytes : 0));   // [kFewQuantSteps][BN]
-  float* join = reinterpret_cast<float*>(quant + F::quant_bytes);             // [BN][128] this CTA's sums
-  float* scales = join + BN * 128;                                            // [4 warps][BN]
+  float* scales = reinterpret_cast<float*>(quant + F::quant_bytes);           // [4 warps][BN]
+  float* join = reinterpret_cast<float*>(stages);   // [BN][128] this CTA's sums, where its steps were
   int* first_tile = reinterpret_cast<int*>(scales + 4 * BN);
   int* first_row = first_tile + p.n_experts + 1;
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kFewAccs], acc_empty[kFewAccs], joined, joint_read, done, quantized;
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kFewAccs], acc_empty[kFewAccs], joined, done, quantized;
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), splits = cluster_size();
@@ -162,10 +173,9 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     mbar_init(smem_addr(&quantized), kFewQuantWarps);
     for (int i = 0; i < kFewAccs; ++i) {
       mbar_init(smem_addr(&acc_full[i]), 1);
-      mbar_init(smem_addr(&acc_empty[i]), 4);
+      mbar_init(smem_addr(&acc_empty[i]), 4 * F::groups);
     }
-    mbar_init(smem_addr(&joined), 4 * splits);
-    mbar_init(smem_addr(&joint_read), 4 * splits);
+    mbar_init(smem_addr(&joined), 4 * F::groups * splits);
     mbar_init(smem_addr(&done), 1);
     fence_mbar_init();
   }
@@ -245,6 +255,9 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       if (lane == 0) mbar_arrive_one(smem_addr(&quantized));
     }
   }
+  if constexpr (BN == 64) {
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewOtherRegs));
+  }
   if (warp == 0) {
     // ---- copies
     int it = 0, st = 0;
@@ -317,12 +330,12 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
   } else if (warp >= 4) {
     // ---- epilogue: thread = row of the weights 32 (warp % 4) + lane; the tile's rows are its columns
-    constexpr int kEach = (BN + 31) / 32;   // rows whose scales a lane loads
-    const int quad = warp % 4;
-    float* mine = scales + quad * BN;
+    if constexpr (BN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFewEpiRegs));
+    constexpr int kCols = F::cols;
+    const int quad = warp % 4, group = F::groups == 1 ? 0 : warp / 4 - 1, c0 = group * kCols;   // its first column
+    float* mine = scales + (warp - 4) * kCols;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     int it = 0;
-    uint32_t phase = 0;   // of the joins
     for (int t = t0; t < tiles && ok; t += dt) {
       const FewTile tile = few_tile<BN>(t, p, first_tile, first_row);
       const int block = tile.n / kB128;
@@ -330,26 +343,22 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       const int64_t sw_stride = DX ? p.k_blocks : 1;
       // the rows' scales four steps at a time, a load ahead; the block's 32 steps at a time, a lane each (a thread's loads
       // under way are waited for with its next load of tensor memory)
-      float4 x4[kEach], next4[kEach];
+      float4 x4, next4;
       float w32 = 0.0f;
-      const float4* sx[kEach];
-#pragma unroll
-      for (int i = 0; i < (kQuant ? 0 : kEach); ++i) {
-        sx[i] = p.sx + min((int64_t)tile.row0 + lane + 32 * i, p.nrows - 1) * p.x_quads;
-        next4[i] = s0 < s1 ? sx[i][s0 / 4] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        x4[i] = next4[i];
+      const float4* sx = nullptr;
+      if constexpr (!kQuant) {
+        sx = p.sx + min((int64_t)tile.row0 + c0 + lane, p.nrows - 1) * p.x_quads;
+        next4 = s0 < s1 ? sx[s0 / 4] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        x4 = next4;
       }
-      float sum[BN];
+      float sum[kCols];
 #pragma unroll
       for (float& v : sum) v = 0.0f;
       for (int s = s0; s < s1; ++s, ++it) {
         const int acc = it % kFewAccs;
         if (!kQuant && (s == s0 || s % 4 == 0)) {
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            x4[i] = next4[i];
-            if (s / 4 * 4 + 4 < s1) next4[i] = sx[i][s / 4 + 1];
-          }
+          x4 = next4;
+          if (s / 4 * 4 + 4 < s1) next4 = sx[s / 4 + 1];
         }
         if ((s - s0) % 32 == 0) w32 = sw[min(s + lane, s1 - 1) * sw_stride];
         const float w = __shfl_sync(0xffffffffu, w32, (s - s0) & 31);
@@ -358,11 +367,8 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
           break;
         }
         __syncwarp();   // the step before has been read
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const float x = kQuant ? quant_scales[(s - s0) * BN + (lane & (BN - 1))] : (s & 2) ? ((s & 1) ? x4[i].w : x4[i].z) : ((s & 1) ? x4[i].y : x4[i].x);
-          if (BN >= 32 || lane < BN) mine[lane + 32 * i] = x * w;
-        }
+        const float x = kQuant ? quant_scales[(s - s0) * BN + (lane & (BN - 1))] : (s & 2) ? ((s & 1) ? x4.w : x4.z) : ((s & 1) ? x4.y : x4.x);
+        if (lane < kCols) mine[lane] = x * w;
         __syncwarp();
         if (!__all_sync(0xffffffffu, wait_for<false>(smem_addr(&acc_full[acc]), (it / kFewAccs) & 1))) {
           ok = false;
@@ -370,10 +376,10 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         }
         tc_after_sync();
 #pragma unroll
-        for (int c = 0; c < BN; c += 16) {
+        for (int c = 0; c < kCols; c += 16) {
           uint32_t v[16];
-          tmem_ld16_now(tmem + (uint32_t)(acc * BN + c) + lanes, v);
-          if (c + 16 >= BN) {   // read
+          tmem_ld16_now(tmem + (uint32_t)(acc * BN + c0 + c) + lanes, v);
+          if (c + 16 >= kCols) {   // read
             tc_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_one(smem_addr(&acc_empty[acc]));
@@ -392,41 +398,42 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       const int n = tile.n + quad * 32 + lane;
       if (splits == 1) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c) {
-          if (c < tile.rows && n < p.out_n) few_store(p, ((int64_t)tile.row0 + c) * p.out_n + n, sum[c]);
+        for (int c = 0; c < kCols; ++c) {
+          if (c0 + c < tile.rows && n < p.out_n) few_store(p, ((int64_t)tile.row0 + c0 + c) * p.out_n + n, sum[c]);
         }
       } else {
-        // every rank's sums lie in its own shared memory; each adds up the rows that are its share
+        // every rank's sums lie in its own shared memory; each adds up the rows that are its share. A cluster has one tile
+        // only: its last sum is complete, so that no copy or product uses the ring any more.
         const int rows = min(tile.rows, BN);
 #pragma unroll
-        for (int c = 0; c < BN; ++c) {
-          if (c < rows) join[c * 128 + quad * 32 + lane] = sum[c];
+        for (int c = 0; c < kCols; ++c) {
+          if (c0 + c < rows) join[(c0 + c) * 128 + quad * 32 + lane] = sum[c];
         }
         __syncwarp();
         if (lane < splits) mbar_arrive_cluster(peer_addr(smem_addr(&joined), lane));
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_addr(&joined), phase, kWaitLimitNs))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_addr(&joined), 0, kWaitLimitNs))) {
           ok = false;
           break;
         }
-        for (int c = rank; c < rows; c += splits) {
-          const uint32_t at = smem_addr(join + c * 128 + quad * 32 + lane);
-          float part[kFewSplits];
+        // several rows' parts are on their way together (X: seldom more than one row; 1 x 2880 x 2880 6.8 us, by four 7.1)
+        constexpr int kRows = kQuant ? 1 : 4;
+        const int step = splits * F::groups;
+        for (int c = rank + splits * group; c < rows; c += kRows * step) {
+          float part[kRows][kFewSplits];
 #pragma unroll
-          for (int i = 0; i < kFewSplits; ++i) part[i] = i < splits ? ld_cluster(peer_addr(at, i)) : 0.0f;
-          float v = part[0];
+          for (int k = 0; k < kRows; ++k) {
+            const uint32_t at = smem_addr(join + (c + k * step) * 128 + quad * 32 + lane);
 #pragma unroll
-          for (int i = 1; i < kFewSplits; ++i) v += part[i];
-          if (n < p.out_n) few_store(p, ((int64_t)tile.row0 + c) * p.out_n + n, v);
-        }
-        if (t + dt < tiles) {   // the next tile's sums take the same place
-          __syncwarp();
-          if (lane < splits) mbar_arrive_cluster(peer_addr(smem_addr(&joint_read), lane));
-          if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_addr(&joint_read), phase, kWaitLimitNs))) {
-            ok = false;
-            break;
+            for (int i = 0; i < kFewSplits; ++i) part[k][i] = i < splits && c + k * step < rows ? ld_cluster(peer_addr(at, i)) : 0.0f;
+          }
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) {
+            float v = part[k][0];
+#pragma unroll
+            for (int i = 1; i < kFewSplits; ++i) v += part[k][i];
+            if (c + k * step < rows && n < p.out_n) few_store(p, ((int64_t)tile.row0 + c + k * step) * p.out_n + n, v);
           }
         }
-        phase ^= 1;
       }
     }
   }
@@ -445,6 +452,23 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 QMV_DEFINE_STATUS_ACCESSOR(status_b128_few)
 
 namespace {
+
+// Ranks that share a tile's depth: as many as there is room for on the SMs, each with two steps at least, while every tile
+// has a cluster of its own and it saves more than joining them costs. Measured, us: 1 x 7168 x 7168 (56 tiles) one rank
+// 20.8, two 14.3, three 13.3, five 12.6, clusters that take a second tile 16.7 and more; 64 x 2880 x 2880 five 8.7, six
+// 8.4, seven 10.3, eight 9.6; 333 x 2880 of depth 1001 (8 steps) one 7.2, two 11.0; 64 x 2880 x 512 one 5.2, two 6.8.
+int few_splits(int64_t tiles, int steps) {
+  int splits = 1;
+  while (splits < kFewSplits && (splits + 1) * tiles <= kFewCtas * device_sm_count() && (splits + 1) * 2 <= steps) ++splits;
+  return (steps + splits - 1) / splits + kFewJoinSteps < steps ? splits : 1;
+}
+
+int64_t hit_experts(const B128GemmArgs& a) { return a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts; }
+// Columns of a tile, by the rows of an expert, taken as equally full.
+int few_columns(const B128GemmArgs& a) {
+  const int64_t hit = hit_experts(a);
+  return a.nrows <= 16 * hit ? 16 : a.nrows <= 32 * hit ? 32 : 64;
+}
 
 template <int BN, bool DX, typename X>
 cudaError_t few_go(const B128GemmArgs& a) {
@@ -494,11 +518,11 @@ cudaError_t few_go(const B128GemmArgs& a) {
     if (!encode(&mx, 2, a.xq, dims, strides, box)) return cudaErrorInvalidValue;
   }
   // tiles that there can be: every expert has at most one partial row tile
-  const int64_t row_tiles = a.nrows / BN + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);
-  const int64_t tiles = (a.n_experts == 1 ? (a.nrows + BN - 1) / BN : row_tiles) * p.n_tiles;
+  const int64_t row_tiles = a.n_experts == 1 ? (a.nrows + BN - 1) / BN : a.nrows / BN + hit_experts(a);
+  const int64_t tiles = row_tiles * p.n_tiles;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kFewThreads);
+  cfg.blockDim = dim3(F::threads);
   cfg.dynamicSmemBytes = F::smem(a.n_experts);
   cfg.stream = a.stream;
   cudaLaunchAttribute attr[2];
@@ -510,12 +534,9 @@ cudaError_t few_go(const B128GemmArgs& a) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Ranks of a tile: as many as there is room for on the SMs, each with two steps at least, while every tile has a
-  // cluster of its own (1 x 7168 x 7168, 56 tiles: one rank 20.8 us, two 14.3, three 13.3, five 12.6; clusters that take
-  // a second tile 16.7 and more). The occupancy query counts one CTA an SM; two run (the fives above are 280 CTAs).
+  // The occupancy query counts one CTA an SM; two run (the fives of 56 tiles are 280 CTAs).
   static PerDevice clusters[kFewSplits + 1];   // of each size that run at once
-  int splits = 1, most = 0;
-  while (splits < kFewSplits && (splits + 1) * tiles <= F::ctas * device_sm_count() && (splits + 1) * 2 <= p.steps) ++splits;
+  int splits = few_splits(tiles, p.steps), most = 0;
   for (;; --splits) {
     attr[0].val.clusterDim.x = (unsigned)splits;
     g_launch_stage = "cudaOccupancyMaxActiveClusters";
@@ -524,13 +545,13 @@ cudaError_t few_go(const B128GemmArgs& a) {
       return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
     });
     if (e != cudaSuccess) return e;
-    most *= F::ctas;
+    most *= kFewCtas;
     if (splits == 1 || most >= tiles) break;
   }
   if (most < 1) return cudaErrorInvalidConfiguration;
   p.per_split = (p.steps + splits - 1) / splits;
   if (kQuant) {
-    const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
+    const int64_t hit = hit_experts(a);
     const bool fits = most >= tiles && p.per_split <= kFewQuantSteps;
     if (!fits || (a.nrows + hit - 1) / hit * p.per_split > kFewQuantUnits) return cudaErrorNotSupported;   // nothing is launched
   }
@@ -542,16 +563,26 @@ cudaError_t few_go(const B128GemmArgs& a) {
 
 template <bool DX>
 cudaError_t few_by_rows(const B128GemmArgs& a) {
-  const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
-  return a.nrows <= 16 * hit ? few_go<16, DX, void>(a) : few_go<32, DX, void>(a);
+  const int columns = few_columns(a);
+  return columns == 16 ? few_go<16, DX, void>(a) : columns == 32 ? few_go<32, DX, void>(a) : few_go<64, DX, void>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_b128_few_linear(const B128GemmArgs& a) {
-  const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
-  if (a.x_type == QMV_F32 || a.nrows > 16 * hit) return cudaErrorNotSupported;
+  if (a.x_type == QMV_F32 || few_columns(a) > 16) return cudaErrorNotSupported;
   return a.x_type == QMV_BF16 ? few_go<16, false, __nv_bfloat16>(a) : few_go<16, false, __half>(a);
+}
+
+double b128_few_us(const B128GemmArgs& a, int depth, int out_n) {
+  const int columns = few_columns(a), steps = b128_blocks(depth);
+  const double hit = (double)hit_experts(a), each = a.nrows / hit / columns;
+  const double row_tiles = a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
+  const double tiles = row_tiles * b128_blocks(out_n);
+  const int splits = few_splits((int64_t)ceil(tiles), steps);
+  const double chain = ceil(tiles * splits / (kFewCtas * device_sm_count())) * ((steps + splits - 1) / splits) * 0.5;
+  const double all = tiles * steps * (columns == 64 ? 2.5e-3 : 2e-3), read = hit * a.N * a.K / 5.2e6;
+  return 4.0 + fmax(fmax(all, read), chain + (splits > 1 ? 2.5 : 0.0));
 }
 
 cudaError_t launch_b128_few(const B128GemmArgs& a, bool dx) { return dx ? few_by_rows<true>(a) : few_by_rows<false>(a); }

@@ -678,22 +678,17 @@ cudaError_t product_go(const B128GemmArgs& a) {
                               (uint64_t)a.K, (uint64_t)a.K, a.stream);
 }
 
-// Whether a product takes the kernel for few rows (32 a tile). Its time goes by the tiles' steps, 2 ns each over the whole
-// device, or by reading the weights, at about 4.5 TB/s; a pair's by the tiles that each pair has to take, 0.41 us a
-// step; both as fitted to GB300. Experts are taken as equally full, with half a tile more each. Measured (few / pairs, us):
-//   1 x 2880 x 2880 6.1 / 13.8, 16 x 7168 x 7168 14.3 / 28.7, 128 x 7168 x 7168 28.3 / 30.2, 256 x 7168 x 7168 54 / 30.0
-//   over 32 experts of 2880 x 2880: 1024 rows 53 / 79, 2048 rows 80 / 80, 4096 rows 160 / 82
+// Whether a product takes the kernel for few rows: both times are estimated. The pairs' goes by the tiles that each pair
+// has to take, 0.38 us a step, or by reading the weights, at 4 TB/s, as fitted to GB300; experts are taken as equally
+// full, with half a tile more each. Measured (few / pairs, us):
+//   1 x 2880 x 2880 6.1 / 13.0, 16 x 7168 x 7168 13.6 / 26.3, 64 x 7168 x 7168 17.1 / 26.6, 128 x 7168 x 7168 25.9 / 27.6,
+//   256 x 7168 x 7168 39 / 27.6, 333 x 1001 x 2880 10.0 / 18.7, 400 x 2880 x 2880 18.2 / 13.9; over 32 experts of 2880 x
+//   2880: 1024 rows 54 / 73, 2048 rows 69 / 74, 4096 rows 106 / 75
 bool few_rows(const B128GemmArgs& a, int depth, int out_n) {
-  const double hit = a.nrows < a.n_experts ? (double)a.nrows : (double)a.n_experts;
-  const auto row_tiles = [&](int rows) {
-    const double each = a.nrows / hit / rows;
-    return a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
-  };
-  const double steps = b128_blocks(depth);
-  const double tile_us = row_tiles(32) * b128_blocks(out_n) * steps * 2e-3, read_us = hit * a.N * a.K / 4.5e6;
-  const double pair_tiles = row_tiles(kPairTile) * ((out_n + kPairTile - 1) / kPairTile);
-  const double pair_us = ceil(pair_tiles / (device_sm_count() / 2)) * steps * 0.41;
-  return 4.0 + (tile_us > read_us ? tile_us : read_us) < 7.0 + (pair_us > read_us ? pair_us : read_us);
+  const double hit = a.nrows < a.n_experts ? (double)a.nrows : (double)a.n_experts, each = a.nrows / hit / kPairTile;
+  const double row_tiles = a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
+  const double rounds = ceil(row_tiles * ((out_n + kPairTile - 1) / kPairTile) / (device_sm_count() / 2));
+  return b128_few_us(a, depth, out_n) < 5.5 + fmax(rounds * b128_blocks(depth) * 0.38, hit * a.N * a.K / 4e6);
 }
 
 }  // namespace

@@ -287,6 +287,19 @@ def test_products_of_many_experts():
     check_grouped(E, N, K, *grouped([int(c) for c in counts], N, K, 3, 5))
 
 
+@pytest.mark.parametrize("rows,N,K", [(33, 1000, 1040), (63, 130, 2064), (64, 2049, 144), (65, 264, 7168), (97, 1290, 272), (128, 1160, 1168)])
+def test_products_of_tens_of_rows(rows, N, K):
+    """Tiles of 64 rows, their depth shared by clusters of two to eight and of one."""
+    check_grouped(1, N, K, *grouped([rows], N, K, 0, rows))
+
+
+@pytest.mark.parametrize("counts,N,K", [([4000], 1304, 1168), ([3841], 1001, 2064), ([5120], 1408, 656), ([1500, 0, 1, 2049, 255, 513], 1160, 1040),
+                                        ([300] * 13, 1290, 784), ([257, 3000, 0, 1000], 776, 1936)])
+def test_products_of_thousands_of_rows(counts, N, K):
+    """Every pair of CTAs has its share of 256 x 256 tiles, some of them ragged in each direction, of several experts."""
+    check_grouped(len(counts), N, K, *grouped(counts, N, K, 3 if len(counts) > 1 else 0, N))
+
+
 def test_nan_stays_in_its_rows():
     """Rows with NaN scales or codes, and an expert whose weights are NaN, leave the others alone."""
     counts, N, K = [70, 3, 200, 33], 136, 272
