@@ -115,6 +115,13 @@ __device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t (&r)[16])
       : "memory");
 }
 
+// The epilogue's warps say that they have read their last sums; the MMAs' warp waits for it.
+template <int THREADS, bool WAIT>
+__device__ __forceinline__ void sums_read() {
+  if constexpr (WAIT) asm volatile("bar.sync 1, %0;" :: "n"(THREADS) : "memory");
+  else asm volatile("bar.arrive 1, %0;" :: "n"(THREADS) : "memory");
+}
+
 struct FewTile {
   int expert, row0, rows, n;   // first row of the tile, and rows from there on; first output
 };
@@ -160,7 +167,7 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   float* join = reinterpret_cast<float*>(stages);   // [BN][128] this CTA's sums, where its steps were
   int* first_tile = reinterpret_cast<int*>(scales + 4 * BN);
   int* first_row = first_tile + p.n_experts + 1;
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kFewAccs], acc_empty[kFewAccs], joined, done, quantized;
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kFewAccs], acc_empty[kFewAccs], done, quantized;
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), splits = cluster_size();
@@ -175,7 +182,6 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       mbar_init(smem_addr(&acc_full[i]), 1);
       mbar_init(smem_addr(&acc_empty[i]), 4 * F::groups);
     }
-    mbar_init(smem_addr(&joined), 4 * F::groups * splits);
     mbar_init(smem_addr(&done), 1);
     fence_mbar_init();
   }
@@ -188,7 +194,6 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
   if (warp == 0) expert_tiles(p.offsets, (int)p.nrows, p.n_experts, BN, p.n_tiles, lane, first_row, first_tile);
   tc_before_sync();
   __syncthreads();
-  if (splits > 1) cluster_sync_all();   // every CTA's barriers exist
   tc_after_sync();
   const uint32_t tmem = tmem_base;
   const int tiles = first_tile[p.n_experts];
@@ -328,6 +333,12 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     if (elect_one()) mma_commit_to<false>(smem_addr(&done));
     __syncwarp();
     if (!wait_for<false>(smem_addr(&done), 0)) ok = false;
+    __syncwarp();
+    // Tensor memory is given back before the ranks wait for one another: held until then, it could keep a cluster of another
+    // stream's kernel from starting that holds some where this one's peers are to start.
+    sums_read<F::threads - 96, true>();
+    tc_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(F::tmem_cols));
   } else if (warp >= 4) {
     // ---- epilogue: thread = row of the weights 32 (warp % 4) + lane; the tile's rows are its columns
     if constexpr (BN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFewEpiRegs));
@@ -395,26 +406,28 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         }
       }
       if (!ok) break;
-      const int n = tile.n + quad * 32 + lane;
       if (splits == 1) {
+        const int n = tile.n + quad * 32 + lane;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           if (c0 + c < tile.rows && n < p.out_n) few_store(p, ((int64_t)tile.row0 + c0 + c) * p.out_n + n, sum[c]);
         }
       } else {
-        // every rank's sums lie in its own shared memory; each adds up the rows that are its share. A cluster has one tile
-        // only: its last sum is complete, so that no copy or product uses the ring any more.
-        const int rows = min(tile.rows, BN);
+        // A cluster has one tile only: its last sum is complete, so that no copy or product uses the ring any more.
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
-          if (c0 + c < rows) join[(c0 + c) * 128 + quad * 32 + lane] = sum[c];
+          if (c0 + c < tile.rows) join[(c0 + c) * 128 + quad * 32 + lane] = sum[c];
         }
-        __syncwarp();
-        if (lane < splits) mbar_arrive_cluster(peer_addr(smem_addr(&joined), lane));
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_addr(&joined), 0, kWaitLimitNs))) {
-          ok = false;
-          break;
-        }
+      }
+    }
+    tc_before_sync();
+    __syncwarp();
+    sums_read<F::threads - 96, false>();
+    if (splits > 1) {
+      cluster_sync_all();   // every rank's sums lie in its own shared memory; each adds up the rows that are its share
+      if (t0 < tiles && ok) {
+        const FewTile tile = few_tile<BN>(t0, p, first_tile, first_row);
+        const int n = tile.n + quad * 32 + lane, rows = min(tile.rows, BN);
         // several rows' parts are on their way together (X: seldom more than one row; 1 x 2880 x 2880 6.8 us, by four 7.1)
         constexpr int kRows = kQuant ? 1 : 4;
         const int step = splits * F::groups;
@@ -437,16 +450,11 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       }
     }
   }
+  if (splits > 1 && warp < 4) cluster_sync_all();
   if (!ok && lane == 0) set_status(kStatusWaitTile);
   __syncwarp();
   pdl_launch_dependents();
-  tc_before_sync();
-  __syncthreads();
   if (splits > 1) cluster_sync_all();   // no CTA's sums are being read any more
-  if (warp == 1) {
-    tc_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(F::tmem_cols));
-  }
 }
 
 QMV_DEFINE_STATUS_ACCESSOR(status_b128_few)
