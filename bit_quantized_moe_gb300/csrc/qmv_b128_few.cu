@@ -9,8 +9,8 @@
 // shares a tile's depth and adds its parts in shared memory in the order of the
 // ranks: no workspace, the same bits every run.
 //
-// Measured (16, 32, 64 columns for as many rows of an expert): 16 x 7168 x 7168 14.3
-// us, 32 rows 15.6, 64 rows 17.1 (with 32 columns 20.8), 2048 rows of 32 experts of
+// Measured (16, 32, 64 columns for as many rows of an expert): 16 x 7168 x 7168 13.0
+// us, 32 rows 14.0, 64 rows 16.7 (with 32 columns 20.8), 2048 rows of 32 experts of
 // 2880 x 2880 69 (80). 128 columns, one CTA an SM, four groups of epilogue warps: 128 x
 // 7168 x 7168 24.9 (with 64 27.3), but 2048 rows of 32 experts 88.
 //
@@ -21,7 +21,7 @@
 // where every CTA has one tile and few steps, it quantizes its rows' part of the
 // depth itself while its first weights are on their way, with the arithmetic of
 // the separate launch and instead of it. (Quantized step by step by two warps: 1 x
-// 7168 x 7168 18.8 us with its quantization, in two launches 15.6.)
+// 7168 x 7168 18.8 us with its quantization where two launches took 15.6.)
 //
 // Warps: 0 issues the TMA copies, 1 the MMAs, 4 and on are the epilogue, thread =
 // row of the weights and 16 or 32 columns; 2..7 quantize (X) first.
@@ -46,8 +46,8 @@ static_assert(256 * kFewEpiRegs + 128 * kFewOtherRegs <= 384 * 80, "what the lau
 
 constexpr int kFewQuantSteps = 16;     // X: steps of a CTA, at most
 constexpr int kFewQuantWarps = 6;
-// X: blocks of 128 columns of a CTA, at most (of equally full experts). 4 a CTA 6.8 us with the product, in two launches
-// 8.4; 64: 8.6 and 8.4; 192: 22.9 and 16.7 (1 and 16 x 2880 x 2880, 16 x 7168 x 7168).
+// X: blocks of 128 columns of a CTA, at most (of equally full experts). Four a CTA 6.2 us with the product, in two launches
+// 7.3; 48: 7.5 and 8.1; 64: 9.5 and 8.1; 192: 22.2 and 15.0 (1, 12 and 16 x 2880 x 2880, 16 x 7168 x 7168).
 constexpr int kFewQuantUnits = 48;
 
 // X: the rows' codes of all steps lie beside the ring, which holds weights only.
@@ -428,7 +428,7 @@ b128_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
       if (t0 < tiles && ok) {
         const FewTile tile = few_tile<BN>(t0, p, first_tile, first_row);
         const int n = tile.n + quad * 32 + lane, rows = min(tile.rows, BN);
-        // several rows' parts are on their way together (X: seldom more than one row; 1 x 2880 x 2880 6.8 us, by four 7.1)
+        // several rows' parts are on their way together (X: seldom more than one row; by four, 1 x 2880 x 2880 takes 0.3 us more)
         constexpr int kRows = kQuant ? 1 : 4;
         const int step = splits * F::groups;
         for (int c = rank + splits * group; c < rows; c += kRows * step) {
@@ -463,8 +463,8 @@ namespace {
 
 // Ranks that share a tile's depth: as many as there is room for on the SMs, each with two steps at least, while every tile
 // has a cluster of its own and it saves more than joining them costs. Measured, us: 1 x 7168 x 7168 (56 tiles) one rank
-// 20.8, two 14.3, three 13.3, five 12.6, clusters that take a second tile 16.7 and more; 64 x 2880 x 2880 five 8.7, six
-// 8.4, seven 10.3, eight 9.6; 333 x 2880 of depth 1001 (8 steps) one 7.2, two 11.0; 64 x 2880 x 512 one 5.2, two 6.8.
+// 20.8, two 14.3, three 13.3, five 12.6, clusters that take a second tile 16.7 and more; 64 x 2880 x 2880 five 8.2, six
+// 7.9, eight 9.2; 333 x 2880 of depth 1001 (8 steps) one 7.2, two 10.5; 64 x 2880 x 512 one 5.2, two 6.8.
 int few_splits(int64_t tiles, int steps) {
   int splits = 1;
   while (splits < kFewSplits && (splits + 1) * tiles <= kFewCtas * device_sm_count() && (splits + 1) * 2 <= steps) ++splits;

@@ -33,8 +33,11 @@
 // last additions (337), the next step's scale there (304), four half
 // sums of 128 columns (413), 16 epilogue warps of 64 columns (353), the scales
 // through shared memory (384 to 433), loads of 16 columns one by one (357).
-// dW is bound by the copies and, over experts of few rows, by its output (32 x 2880
-// x 2880 from 16,384 rows: 377 us, 1.06 GB written; filling that takes 142).
+// dW is bound by the MMAs (8192 x 7168 x 7168: 470 us, 1.8 PFLOP/s) and, over experts
+// of few rows, by its output and the steps that rows behind an expert's last are
+// cleared in (32 x 2880 x 2880 from 16,384 rows: 300 us, 1.06 GB written; filling that
+// takes 142. Rows in whole sixteens, which need no clearing: 274. With all of the
+// step's 64 rows cleared and multiplied 379).
 #include <cmath>
 #include <type_traits>
 
@@ -365,13 +368,13 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             if constexpr (MODE == kModeDw) {
               // two panels of 64 outputs x 64 rows each
               const int row = tile.row0 + 64 * s, x0 = (tile.m) * 2, y0 = (tile.n + rank * kHalf) * 2;
-              if (tile.rows - 64 * s >= 64) {
+              if (tile.rows - 64 * s >= 64 || (tile.rows & 15) == 0) {
                 mbar_expect_pair(lead, kStageBytes);
                 tma_load_2d<true>(a, &map_a, x0, row, lead);
                 tma_load_2d<true>(a + kOperandBytes / 2, &map_a, x0 + 128, row, lead);
                 tma_load_2d<true>(b, &map_b, y0, row, lead);
                 tma_load_2d<true>(b + kOperandBytes / 2, &map_b, y0 + 128, row, lead);
-              } else {   // rows of the next expert come too: warp 2 clears them, then arrives
+              } else {   // the last 16 rows that are multiplied hold the next expert's too: warp 2 clears those, then arrives
                 const uint32_t mine = smem_addr(&tail[st]);
                 mbar_arrive_expect_tx(mine, kStageBytes);
                 tma_load_2d<false>(a, &map_a, x0, row, mine);
@@ -402,7 +405,8 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       int st = 0, sums = 0;
       uint32_t st_phase = 0;
       for (int i = 0; i < my_tiles && ok; ++i) {
-        const int steps = tile_of(t0 + i * dt).steps;
+        const PairTile tile = tile_of(t0 + i * dt);
+        const int steps = tile.steps;
         for (int s = 0; s < steps; ++s) {
           const int acc = sums & 1;
           if ((s % kGroup<MODE> == 0 && !__all_sync(0xffffffffu, wait_brisk(smem_addr(&acc_empty[acc]), ((sums >> 1) & 1) ^ 1))) ||
@@ -410,8 +414,9 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             ok = false;
             break;
           }
-          // what warp 2 of both CTAs cleared
-          if (MODE == kModeDw && s == steps - 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          // What warp 2 of both CTAs cleared: the phase is complete, and is acquired at the cluster's scope. (As a fence of the
+          // cluster 32 experts' dW below took 318 us.)
+          if (MODE == kModeDw && s == steps - 1 && (tile.rows & 15) != 0) mbar_wait_cluster(smem_addr(&full[st]), st_phase, 0);
           tc_after_sync();
           const uint32_t a = data0 + (uint32_t)st * kStageBytes, b = a + kOperandBytes;
           const uint32_t d = tm + (uint32_t)(acc * kPairTile);
@@ -419,6 +424,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {   // 32 bytes of depth each; transposed: 32 or 16 depths
+              if (MODE == kModeDw && 64 * s + 16 * j >= tile.rows) break;
               uint64_t da, db;
               if constexpr (MODE == kModeDw) {
                 da = transposed_desc(a + j * 16 * 128, kOperandBytes / 2);
@@ -444,27 +450,23 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       __syncwarp();
       if (!wait_brisk(smem_addr(&done), 0)) ok = false;
     } else if (warp == 2 && MODE == kModeDw) {
-      // ---- the rows behind an expert's last one, cleared in both operands (0 times a NaN is one)
+      // ---- the rows behind an expert's last one, up to a multiple of 16, cleared in both operands (0 times a NaN is one)
       int it = 0;
       uint32_t phases = 0;   // bit st: of tail[st]
       for (int i = 0; i < my_tiles && ok; ++i) {
         const PairTile tile = tile_of(t0 + i * dt);
         it += tile.steps;
-        const int valid = tile.rows - 64 * (tile.steps - 1);
-        if (tile.steps == 0 || valid == 64) continue;
+        if ((tile.rows & 15) == 0) continue;
         const int st = (it - 1) % kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&tail[st]), (phases >> st) & 1, kWaitLimitNs))) {
+        if (!__all_sync(0xffffffffu, wait_brisk(smem_addr(&tail[st]), (phases >> st) & 1))) {
           ok = false;
           break;
         }
         phases ^= 1u << st;
-        uint8_t* at = stages + (uint32_t)st * kStageBytes;
-        // four panels of 64 rows of 128 bytes
-        for (int j = lane; j < 4 * (64 - valid) * 8; j += 32) {
-          const int piece = j & 7, r = j / 8;
-          const int panel = r / (64 - valid), row = valid + r - panel * (64 - valid);
-          reinterpret_cast<uint4*>(at + panel * (kOperandBytes / 2) + row * 128)[piece] = make_uint4(0, 0, 0, 0);
-        }
+        // a row of four panels at a time, 16 bytes a lane
+        uint8_t* at = stages + (uint32_t)st * kStageBytes + (lane / 8) * (kOperandBytes / 2) + (lane & 7) * 16;
+        const int valid = tile.rows - 64 * (tile.steps - 1), end = (valid + 15) / 16 * 16;
+        for (int row = valid; row < end; ++row) *reinterpret_cast<uint4*>(at + row * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(leader_addr(smem_addr(&full[st])));

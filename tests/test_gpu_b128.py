@@ -360,6 +360,29 @@ def test_grad_w_without_rows_is_zero():
     assert not dw.any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_grad_w_beside_rows_of_nan(dtype):
+    """Every other expert's rows are NaN, those behind the last one too: none reaches the experts between, whatever their rows
+    past the last whole 16 or 64."""
+    counts = [n for m in (1, 2, 15, 16, 17, 31, 32, 33, 48, 49, 63, 64, 65, 80, 127, 129, 528, 577) for n in (m, 3 + m % 5)]
+    E, N, K, rows = len(counts), 300, 272, sum(counts) + 40
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    g = qi.rng(9)
+    dy, x = (g.integers(-15, 16, size=(rows, n)).astype(np.float64) for n in (N, K))
+    for bad in (0, 1):
+        d, v = dy.copy(), x.copy()
+        for e in range(bad, E, 2):
+            d[offsets[e]:offsets[e + 1]] = v[offsets[e]:offsets[e + 1]] = np.nan
+        d[offsets[-1]:] = v[offsets[-1]:] = np.nan
+        dyd, ld = strided(d, dtype, -N % 8)
+        dw = torch.full((E, N, K), 7.0, device=DEV)
+        qmv.qmv_b128_grad_w(dtype, dyd, ld, dev(v, dtype), K, E, N, K, rows, dev(offsets), "f32", dw)
+        for e in range(E):
+            a, b = offsets[e], offsets[e + 1]
+            assert np.array_equal(host(dw[e]), d[a:b].T @ v[a:b], equal_nan=True), (bad, e)
+    assert status_clean()
+
+
 def test_grad_w_matches_differences():
     """L = <y, dy> of unquantized rows is linear in W: its difference along a direction is the gradient's product with it."""
     rows, N, K = 90, 136, 144
