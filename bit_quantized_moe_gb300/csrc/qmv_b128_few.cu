@@ -90,11 +90,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -582,13 +577,16 @@ cudaError_t launch_b128_few_linear(const B128GemmArgs& a) {
   return a.x_type == QMV_BF16 ? few_go<16, false, __nv_bfloat16>(a) : few_go<16, false, __half>(a);
 }
 
+// By the CTAs' steps, alone or side by side, 2 or 2.5 ns a tile's step over the whole device, or reading the weights at 5.2
+// TB/s, as fitted to GB300; experts are taken as equally full, with half a tile more each.
 double b128_few_us(const B128GemmArgs& a, int depth, int out_n) {
   const int columns = few_columns(a), steps = b128_blocks(depth);
   const double hit = (double)hit_experts(a), each = a.nrows / hit / columns;
   const double row_tiles = a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
   const double tiles = row_tiles * b128_blocks(out_n);
   const int splits = few_splits((int64_t)ceil(tiles), steps);
-  const double chain = ceil(tiles * splits / (kFewCtas * device_sm_count())) * ((steps + splits - 1) / splits) * 0.5;
+  const double ctas = tiles * splits, step = columns < 64 ? 0.5 : ctas > device_sm_count() ? 0.68 : 0.4;   // us, of a CTA
+  const double chain = ceil(ctas / (kFewCtas * device_sm_count())) * ((steps + splits - 1) / splits) * step;
   const double all = tiles * steps * (columns == 64 ? 2.5e-3 : 2e-3), read = hit * a.N * a.K / 5.2e6;
   return 4.0 + fmax(fmax(all, read), chain + (splits > 1 ? 2.5 : 0.0));
 }

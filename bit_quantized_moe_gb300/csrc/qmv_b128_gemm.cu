@@ -67,6 +67,9 @@ constexpr int kEpiWarps = 8;           // a CTA's
 // them, and the pitch of a row there (an odd number of 16 bytes: no bank conflicts).
 constexpr int kParkRow = 128, kParkPitch = kParkRow + 16;
 constexpr uint32_t kParkBytes = kEpiWarps * 32 * kParkPitch;
+constexpr int kPairJoinSteps = 9;      // steps that take as long as joining two pairs' sums
+constexpr int kJoinBytes = 32 * kHalf / 2 * 4;   // of half of a warp's sums
+static_assert(kEpiWarps * kJoinBytes <= kPairStages * kStageBytes, "the sums to join");
 constexpr size_t pair_smem(int n_experts) {
   return 1024 + (size_t)kPairStages * kStageBytes + kParkBytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
 }
@@ -86,7 +89,7 @@ struct PairParams {
   int out_n;                  // columns of the output
   int out_type;
   bool whole16;               // the output's rows are of whole 16 bytes
-  int steps;                  // y, dx: of depth
+  int steps, per_split;       // y, dx: of depth, and of the first of two pairs
   int x_quads;                // fours of a row's scales
   int k_blocks, n_blocks;     // of the weights' scales
   int n_tiles, m_tiles;       // column tiles; dW: row tiles of a matrix
@@ -125,6 +128,23 @@ __device__ __forceinline__ void mbar_expect_pair(uint32_t bar, uint32_t bytes) {
 }
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The address of `addr` in the first CTA of this one's pair.
+template <bool SPLIT>
+__device__ __forceinline__ uint32_t pair_leader(uint32_t addr) {
+  if constexpr (!SPLIT) return leader_addr(addr);
+  return peer_addr(addr, (int)(cluster_rank() & ~1u));
+}
+// The MMAs so far, complete, arrive at a barrier of both CTAs of the pair.
+template <bool SPLIT>
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  if constexpr (!SPLIT) return mma_commit_to<true>(bar);
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(bar), "h"((uint16_t)(3u << (cluster_rank() & ~1u))) : "memory");
+}
+__device__ __forceinline__ void ld_cluster4(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared::cluster.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
 
 // As mbar_wait_bounded, without a hint to sleep.
@@ -172,16 +192,16 @@ __device__ __forceinline__ uint32_t two16(float a, float b) {
   }
 }
 
-// The 128 columns from n0 on of a warp's 32 rows, as T: parked 128 bytes a row
+// The columns from n0 on of a warp's 32 rows, as T: parked 128 bytes a row
 // at a time and stored four rows by 128 bytes an instruction. (As 32-byte stores of
 // 32 rows at once: 8192 x 7168 x 7168 396 us; as bulk copies of 128 bytes: 347 us,
 // but dW of 32 experts of 2880 627.) Rows are of whole 16 bytes.
-template <typename T>
+template <typename T, int TWOS>
 __device__ __forceinline__ void store_rows(const PairParams& p, uint8_t* park, int64_t row0, int rows, int n0, int lane,
-                                           const uint64_t (&sum)[64]) {
+                                           const uint64_t (&sum)[TWOS]) {
   constexpr int cols = kParkRow / (int)sizeof(T);
 #pragma unroll
-  for (int c = 0; c < kHalf; c += cols) {
+  for (int c = 0; c < 2 * TWOS; c += cols) {
     const int vecs = min(cols, p.out_n - n0 - c) * (int)sizeof(T) / 16;
     if (vecs <= 0) break;
     uint8_t* mine = park + lane * kParkPitch;
@@ -241,6 +261,22 @@ __device__ __forceinline__ void store_turned(const PairParams& p, float* park, i
   __syncwarp();
 }
 
+template <int TWOS>
+__device__ __forceinline__ void store_tile(const PairParams& p, uint8_t* park, int64_t row0, int rows, int n0, int lane,
+                                           const uint64_t (&sum)[TWOS]) {
+  if (p.whole16) {
+    if (p.out_type == QMV_BF16) store_rows<__nv_bfloat16>(p, park, row0, rows, n0, lane, sum);
+    else if (p.out_type == QMV_F16) store_rows<__half>(p, park, row0, rows, n0, lane, sum);
+    else store_rows<float>(p, park, row0, rows, n0, lane, sum);
+  } else {
+#pragma unroll
+    for (int c = 0; c < TWOS / 8; ++c) {
+      if (n0 + 16 * c >= p.out_n) break;
+      store_turned(p, reinterpret_cast<float*>(park), row0, rows, n0 + 16 * c, lane, sum + 8 * c);
+    }
+  }
+}
+
 // What a CTA does of one output tile.
 struct PairTile {
   int expert;
@@ -289,7 +325,9 @@ __device__ __forceinline__ PairTile pair_tile(int t, const PairParams& p, const 
   return r;
 }
 
-template <int MODE, bool F16>
+// SPLIT: the two pairs of a cluster share a tile's depth. Each thread keeps half of its columns and takes the other pair's
+// sums of them from its shared memory; the first pair's come first. A cluster has one tile.
+template <int MODE, bool F16, bool SPLIT>
 __global__ void __launch_bounds__(kPairThreads, 1)
 b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ PairParams p) {
@@ -305,7 +343,10 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], tail[kStages], done;
   __shared__ uint32_t tmem_base;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank();
+  static_assert(!SPLIT || MODE != kModeDw, "depth of y and dx");
+  const int rank = SPLIT ? (int)cluster_rank() & 1 : (int)cluster_rank();
+  constexpr int splits = SPLIT ? 2 : 1;
+  const int part = SPLIT ? (int)cluster_rank() / 2 : 0, first_step = SPLIT ? part * p.per_split : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -333,7 +374,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   tc_after_sync();
   const uint32_t tmem = tmem_base;
   const int tiles = MODE == kModeDw ? p.n_experts * p.m_tiles * p.n_tiles : first_tile[p.n_experts];
-  const int t0 = (int)blockIdx.x / 2, dt = (int)gridDim.x / 2;
+  const int t0 = (int)blockIdx.x / (2 * splits), dt = (int)gridDim.x / (2 * splits);
   bool ok = true;
 
   if (warp < 4) {
@@ -341,6 +382,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     const int my_tiles = __shfl_sync(0xffffffffu, t0 < tiles ? (tiles - t0 + dt - 1) / dt : 0, 0);
     const auto tile_of = [&](int t) {   // the same in all lanes, and known to be
       PairTile r = pair_tile<MODE>(t, p, first_tile, first_row, rank);
+      if constexpr (SPLIT) r.steps = part == 0 ? p.per_split : r.steps - first_step;
       r.expert = __shfl_sync(0xffffffffu, r.expert, 0);
       r.row0 = __shfl_sync(0xffffffffu, r.row0, 0);
       r.rows = __shfl_sync(0xffffffffu, r.rows, 0);
@@ -363,7 +405,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             break;
           }
           const uint32_t a = data0 + (uint32_t)st * kStageBytes, b = a + kOperandBytes;
-          const uint32_t lead = leader_addr(smem_addr(&full[st]));
+          const uint32_t lead = pair_leader<SPLIT>(smem_addr(&full[st]));
           if (elect_one()) {
             if constexpr (MODE == kModeDw) {
               // two panels of 64 outputs x 64 rows each
@@ -383,10 +425,11 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 tma_load_2d<false>(b + kOperandBytes / 2, &map_b, y0 + 128, row, mine);
               }
             } else {
+              const int at = (first_step + s) * 128;
               mbar_expect_pair(lead, (uint32_t)copies * 64 * 128 + kOperandBytes);
-              for (int c = 0; c < copies; ++c) tma_load_2d<true>(a + c * 64 * 128, &map_a, s * 128, tile.row0 + 64 * c, lead);
-              if constexpr (MODE == kModeY) tma_load_3d_pair(b, &map_b, s * 128, tile.n + rank * kHalf, tile.expert, lead);
-              else tma_load_3d_pair(b, &map_b, tile.n + rank * kHalf, s * 128, tile.expert, lead);
+              for (int c = 0; c < copies; ++c) tma_load_2d<true>(a + c * 64 * 128, &map_a, at, tile.row0 + 64 * c, lead);
+              if constexpr (MODE == kModeY) tma_load_3d_pair(b, &map_b, at, tile.n + rank * kHalf, tile.expert, lead);
+              else tma_load_3d_pair(b, &map_b, tile.n + rank * kHalf, at, tile.expert, lead);
             }
           }
           __syncwarp();
@@ -435,8 +478,8 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
               }
               pair_mma<MODE>(d, da, db, idesc, s % kGroup<MODE> > 0 || j > 0 ? 1u : 0u);
             }
-            mma_commit_to<true>(smem_addr(&empty[st]));
-            if (last) mma_commit_to<true>(smem_addr(&acc_full[acc]));
+            pair_commit<SPLIT>(smem_addr(&empty[st]));
+            if (last) pair_commit<SPLIT>(smem_addr(&acc_full[acc]));
           }
           __syncwarp();
           sums += last;
@@ -446,7 +489,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           }
         }
       }
-      if (elect_one()) mma_commit_to<true>(smem_addr(&done));
+      if (elect_one()) pair_commit<SPLIT>(smem_addr(&done));
       __syncwarp();
       if (!wait_brisk(smem_addr(&done), 0)) ok = false;
     } else if (warp == 2 && MODE == kModeDw) {
@@ -469,7 +512,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         for (int row = valid; row < end; ++row) *reinterpret_cast<uint4*>(at + row * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_addr(smem_addr(&full[st])));
+        if (lane == 0) mbar_arrive_cluster(pair_leader<SPLIT>(smem_addr(&full[st])));
       }
     }
   } else {
@@ -495,19 +538,24 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     const auto begin = [&](int t) {
       const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
       steps = (tile.steps + kGroup<MODE> - 1) / kGroup<MODE>;
+      if constexpr (SPLIT) steps = part == 0 ? p.per_split : steps - first_step;
       if constexpr (MODE != kModeDw) {
         sx = p.sx + min((int64_t)tile.row0 + r, p.nrows - 1) * p.x_quads;
         const int block = min((tile.n + half * kHalf) / kB128, (MODE == kModeY ? p.n_blocks : p.k_blocks) - 1);
         sw = p.sw + (int64_t)tile.expert * p.n_blocks * p.k_blocks + (MODE == kModeY ? (int64_t)block * p.k_blocks : block);
+        if constexpr (SPLIT) {   // a whole number of fours
+          sx += first_step / 4;
+          sw += MODE == kModeY ? (int64_t)first_step : (int64_t)first_step * p.k_blocks;
+        }
         next4 = *sx;
         next32 = block_scales(0);
       }
     };
+    uint64_t sum[64];
     if (t0 < tiles) begin(t0);
     for (int t = t0; t < tiles && ok; t += dt) {
       float4 x4 = next4;
       float w32 = next32;
-      uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
       for (int s = 0; s < steps; ++s, ++it) {
@@ -551,7 +599,7 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         tmem_ld_wait(v[1]);
         tc_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(leader_addr(smem_addr(&acc_empty[acc])));   // read
+        if (lane == 0) mbar_arrive_pair(pair_leader<SPLIT>(smem_addr(&acc_empty[acc])));   // read
         if constexpr (MODE != kModeDw) {
           if (s % 4 == 0 && s + 4 < steps) next4 = sx[s / 4 + 1];
           if (s % 32 == 31 && s + 1 < steps) next32 = block_scales(s + 1);
@@ -560,27 +608,44 @@ b128_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         add(3);
       }
       if (!ok) break;
+      if constexpr (SPLIT) break;
       asm volatile("" : "+r"(t));   // the tile's place is worked out again, not kept in registers over the steps
       if (t + dt < tiles) begin(t + dt);
       const PairTile tile = pair_tile<MODE>(t, p, first_tile, first_row, rank);
       const int n0 = tile.n + half * kHalf;   // first column of this thread
       const int64_t row0 = MODE == kModeDw ? (int64_t)tile.expert * p.N + tile.m : (int64_t)tile.row0;   // of the CTA
       const int rows = MODE == kModeDw ? p.N - tile.m : tile.rows;
-      if (p.whole16) {
-        if (p.out_type == QMV_BF16) store_rows<__nv_bfloat16>(p, warp_park, row0 + quad * 32, rows - quad * 32, n0, lane, sum);
-        else if (p.out_type == QMV_F16) store_rows<__half>(p, warp_park, row0 + quad * 32, rows - quad * 32, n0, lane, sum);
-        else store_rows<float>(p, warp_park, row0 + quad * 32, rows - quad * 32, n0, lane, sum);
-      } else {
+      store_tile<64>(p, warp_park, row0 + quad * 32, rows - quad * 32, n0, lane, sum);
+    }
+    if constexpr (SPLIT) {
+      // Where the CTA's steps were: the tile's last sum is complete. 16 bytes a lane follow one another, as they cross best.
+      uint4* mine = reinterpret_cast<uint4*>(stages + (warp - 4) * kJoinBytes) + lane;
+      uint64_t keep[32];
+      if (t0 < tiles) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (n0 + 16 * c >= p.out_n) break;
-          store_turned(p, reinterpret_cast<float*>(warp_park), row0 + quad * 32, rows - quad * 32, n0 + 16 * c, lane, sum + 8 * c);
+        for (int i = 0; i < 32; i += 2) {
+          const uint64_t a = part == 0 ? sum[32 + i] : sum[i], b = part == 0 ? sum[33 + i] : sum[i + 1];
+          keep[i] = part == 0 ? sum[i] : sum[32 + i];
+          keep[i + 1] = part == 0 ? sum[i + 1] : sum[33 + i];
+          mine[i * 16] = make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
         }
+      }
+      cluster_sync_all();
+      if (t0 < tiles && ok) {
+        uint64_t other[32];
+        const uint32_t from = peer_addr(smem_addr(mine), (int)cluster_rank() ^ 2);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) ld_cluster4(from + 256 * i, other[i], other[i + 1]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) add2(keep[i], other[i]);   // the same in either order
+        const PairTile tile = pair_tile<MODE>(t0, p, first_tile, first_row, rank);
+        store_tile<32>(p, warp_park, (int64_t)tile.row0 + quad * 32, tile.rows - quad * 32, tile.n + half * kHalf + part * (kHalf / 2), lane, keep);
       }
     }
     // the first CTA's last arrivals have reached this one before it may exit
     if (ok && !wait_brisk(smem_addr(&done), 0)) ok = false;
   }
+  if (SPLIT && warp < 4) cluster_sync_all();
   if (!ok && lane == 0) set_status(kStatusWaitTile);
   __syncwarp();
   pdl_launch_dependents();
@@ -597,10 +662,11 @@ QMV_DEFINE_STATUS_ACCESSOR(status_b128_gemm)
 
 namespace {
 
-template <int MODE, bool F16>
+template <int MODE, bool F16, bool SPLIT>
 cudaError_t pair_go(PairParams& p, int64_t tiles, const void* a, uint64_t a_bytes, uint64_t a_stride, const void* b,
                     uint64_t b_bytes, uint64_t b_stride, cudaStream_t stream) {
-  auto* kernel = b128_pair_kernel<MODE, F16>;
+  constexpr int kCluster = SPLIT ? 4 : 2;
+  auto* kernel = b128_pair_kernel<MODE, F16, SPLIT>;
   // The most that any call asks for (the attribute is the function's), and before the tensor maps: it makes the device's
   // context current on a host thread whose first CUDA call this is.
   g_launch_stage = "cudaFuncSetAttribute";
@@ -634,27 +700,44 @@ cudaError_t pair_go(PairParams& p, int64_t tiles, const void* a, uint64_t a_byte
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // no more pairs than run at once
-  static PerDevice pairs;
+  // no more clusters than run at once
+  static PerDevice clusters;
   int most = 0;
   g_launch_stage = "cudaOccupancyMaxActiveClusters";
-  e = pairs.get(&most, [&](int* n) {
-    cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2));
+  e = clusters.get(&most, [&](int* n) {
+    cfg.gridDim = dim3((unsigned)(device_sm_count() / kCluster * kCluster));
     return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
   });
   if (e != cudaSuccess) return e;
   if (most < 1) return cudaErrorInvalidConfiguration;
   g_launch_stage = "launch";
-  cfg.gridDim = dim3((unsigned)(2 * (tiles < most ? tiles : most)));
+  cfg.gridDim = dim3((unsigned)(kCluster * (SPLIT || tiles < most ? tiles : most)));
   cfg.numAttrs = stream != nullptr ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+}
+
+// Tiles that there can be of `out_n` columns: every expert has at most one partial row tile.
+int64_t pair_tiles(const B128GemmArgs& a, int out_n) {
+  const int64_t hit = a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts;
+  const int64_t rows = a.n_experts == 1 ? (a.nrows + kPairTile - 1) / kPairTile : a.nrows / kPairTile + hit;
+  return rows * ((out_n + kPairTile - 1) / kPairTile);
+}
+
+// Steps of the first pair where two share a tile's: fours, as the rows' scales are loaded.
+int first_half(int steps) { return (steps / 2 + 3) / 4 * 4; }
+
+// Whether two pairs share a tile's depth: where all run at once and it saves more than joining costs. Measured (one pair /
+// two, us): 256 x 7168 x 7168 27.6 / 21.8, 160 x 7168 x 16384 57 / 38, 1000 x 1024 x 4096 17.4 / 14.0, 256 x 8192 x 2880
+// 14.6 / 14.3, 256 x 8192 x 2048 11.8 / 12.2, 512 x 2880 x 1024 8.4 / 9.3. (Three and four took as long as two, or more.)
+bool pairs_split(int64_t tiles, int steps) {
+  return 2 * tiles <= device_sm_count() / 2 && first_half(steps) + kPairJoinSteps < steps;
 }
 
 template <int MODE>
@@ -674,23 +757,26 @@ cudaError_t product_go(const B128GemmArgs& a) {
   p.out_type = a.out_type;
   p.steps = b128_blocks(depth);
   p.n_tiles = (p.out_n + kPairTile - 1) / kPairTile;
-  // no more pairs than tiles there can be: every expert has at most one partial row tile
-  const int64_t row_tiles = a.nrows / kPairTile + (a.nrows < a.n_experts ? a.nrows : (int64_t)a.n_experts);
-  return pair_go<MODE, false>(p, row_tiles * p.n_tiles, a.xq, b128_row_bytes(depth), b128_row_bytes(depth), a.w,
+  const int64_t tiles = pair_tiles(a, p.out_n);
+  p.per_split = first_half(p.steps);
+  auto* go = pairs_split(tiles, p.steps) ? pair_go<MODE, false, true> : pair_go<MODE, false, false>;
+  return go(p, tiles, a.xq, b128_row_bytes(depth), b128_row_bytes(depth), a.w,
                               (uint64_t)a.K, (uint64_t)a.K, a.stream);
 }
 
 // Whether a product takes the kernel for few rows: both times are estimated. The pairs' goes by the tiles that each pair
 // has to take, 0.38 us a step, or by reading the weights, at 4 TB/s, as fitted to GB300; experts are taken as equally
 // full, with half a tile more each. Measured (few / pairs, us):
-//   1 x 2880 x 2880 6.1 / 13.0, 16 x 7168 x 7168 13.6 / 26.3, 64 x 7168 x 7168 17.1 / 26.6, 128 x 7168 x 7168 25.9 / 27.6,
-//   256 x 7168 x 7168 39 / 27.6, 333 x 1001 x 2880 10.0 / 18.7, 400 x 2880 x 2880 18.2 / 13.9; over 32 experts of 2880 x
-//   2880: 1024 rows 54 / 73, 2048 rows 69 / 74, 4096 rows 106 / 75
+//   1 x 2880 x 2880 5.8 / 13, 16 x 7168 x 7168 13.0 / 22, 64 x 7168 x 7168 16.7 / 21.5, 128 x 7168 x 7168 25.6 / 21.5,
+//   256 x 7168 x 7168 39 / 21.8, 256 x 2880 x 2880 12.1 / 12.3, 333 x 1001 x 2880 9.9 / 14.5, 400 x 2880 x 2880 18.2 / 12.8,
+//   512 x 2880 x 1024 9.4 / 8.4; over 32 experts of 2880 x 2880: 1024 rows 53 / 73, 2048 rows 69 / 74, 4096 rows 106 / 75
 bool few_rows(const B128GemmArgs& a, int depth, int out_n) {
+  const int steps = b128_blocks(depth);
   const double hit = a.nrows < a.n_experts ? (double)a.nrows : (double)a.n_experts, each = a.nrows / hit / kPairTile;
   const double row_tiles = a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
   const double rounds = ceil(row_tiles * ((out_n + kPairTile - 1) / kPairTile) / (device_sm_count() / 2));
-  return b128_few_us(a, depth, out_n) < 5.5 + fmax(rounds * b128_blocks(depth) * 0.38, hit * a.N * a.K / 4e6);
+  const double chain = pairs_split(pair_tiles(a, out_n), steps) ? first_half(steps) * 0.38 + 5.0 : rounds * steps * 0.38;
+  return b128_few_us(a, depth, out_n) < 5.5 + fmax(chain, hit * a.N * a.K / 4e6);
 }
 
 }  // namespace
@@ -730,9 +816,9 @@ cudaError_t launch_b128_grad_w(const B128GradWArgs& a) {
   const int64_t tiles = (int64_t)a.n_experts * p.m_tiles * p.n_tiles;
   const uint64_t ld_dy = (uint64_t)a.ld_dy * 2, ldx = (uint64_t)a.ldx * 2;
   if (a.type == QMV_F16) {
-    return pair_go<kModeDw, true>(p, tiles, a.dy, (uint64_t)a.N * 2, ld_dy, a.x, (uint64_t)a.K * 2, ldx, a.stream);
+    return pair_go<kModeDw, true, false>(p, tiles, a.dy, (uint64_t)a.N * 2, ld_dy, a.x, (uint64_t)a.K * 2, ldx, a.stream);
   }
-  return pair_go<kModeDw, false>(p, tiles, a.dy, (uint64_t)a.N * 2, ld_dy, a.x, (uint64_t)a.K * 2, ldx, a.stream);
+  return pair_go<kModeDw, false, false>(p, tiles, a.dy, (uint64_t)a.N * 2, ld_dy, a.x, (uint64_t)a.K * 2, ldx, a.stream);
 }
 
 }  // namespace qmv

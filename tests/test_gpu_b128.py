@@ -293,6 +293,13 @@ def test_products_of_tens_of_rows(rows, N, K):
     check_grouped(1, N, K, *grouped([rows], N, K, 0, rows))
 
 
+@pytest.mark.parametrize("counts,N,K", [([200], 7168, 2816), ([129], 2817, 7168), ([300], 4101, 4112), ([256], 4000, 4368), ([511], 4360, 2896),
+                                        ([200, 100], 2600, 4112), ([0, 260], 3000, 5136), ([1000], 1032, 4112)])
+def test_products_of_hundreds_of_rows(counts, N, K):
+    """Two pairs of CTAs share a tile's depth, unequally where its blocks are odd in number or not of fours."""
+    check_grouped(len(counts), N, K, *grouped(counts, N, K, 3 if len(counts) > 1 else 0, N))
+
+
 @pytest.mark.parametrize("counts,N,K", [([4000], 1304, 1168), ([3841], 1001, 2064), ([5120], 1408, 656), ([1500, 0, 1, 2049, 255, 513], 1160, 1040),
                                         ([300] * 13, 1290, 784), ([257, 3000, 0, 1000], 776, 1936)])
 def test_products_of_thousands_of_rows(counts, N, K):
