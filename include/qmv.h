@@ -640,7 +640,7 @@ int qmv_moe_balance(int32_t type, const void* logits_dev, int64_t ldl, const uin
  * are constants; slots whose id is outside [0, n_experts) take no part, an expert
  * that is named twice takes both slots'. dweights_dev fp32 [ntok][top_k], or NULL for the loss
  * alone; counts_dev as qmv_moe_balance gave them and dloss_dev fp32 [1], or both
- * NULL for the weights alone. Padding's rows are zero; a row with a NaN (softmax:
+ * NULL for the weights alone. dlogits may be the logits themselves (ldd = ldl). Padding's rows are zero; a row with a NaN (softmax:
  * or +infinity) among its logits is NaN. live, score, renorm and scale as in
  * the calls above. fp32 until it is stored; one launch.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ECUDA.

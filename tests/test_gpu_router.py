@@ -235,6 +235,22 @@ def test_gradient_matches_autograd():
     assert np.abs(got - want.cpu().numpy()).max() <= 4 * rel(r.l, 24, 20) * float(want.abs().max())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("score,renorm", MODES)
+def test_gradient_in_the_logits_place(score, renorm, dtype):
+    """dlogits may be the logits themselves: the bits of a call with a place of its own."""
+    for tokens, experts, top_k in ((3000, 40, 4), (9, 300, 8), (1, 1, 1)):
+        r = Router(logits(tokens, tokens, experts), dtype, top_k, score, renorm, 1.5)
+        ids, w = r.route()
+        counts, means, loss = r.balance(ids)
+        dw, dl = dev(qi.rng(3).standard_normal((tokens, top_k)), "f32"), dev([0.5], "f32")
+        t = r.t.clone()
+        d = torch.empty_like(t)
+        for out in (d, t):
+            qmv.qmv_moe_router_grad(dtype, t, experts, None, ids, dw, counts, dl, tokens, experts, top_k, score, renorm, 1.5, out, experts)
+        assert torch.equal(d, t)
+
+
 def test_router_in_a_graph_and_on_two_streams():
     """Captured calls replay on new logits; two graphs with a workspace each run at once."""
     tokens, experts, top_k = 700, 64, 6

@@ -137,3 +137,27 @@ def test_router_past_32_bits():
                                 "softmax", True, 1.0)
     # stored in bf16: half a step of 2^-8 besides
     assert (np.abs(d[at, :experts].double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 150 * 2.0 ** -24 * size + 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("rows", [1, 70, 700])
+def test_most_columns(rows):
+    """The most outputs that a matrix may have, the gradient's depth."""
+    N, K = 1 << 20, 48
+    w, dc, xc = codes(4, 1, N, K), codes(5, rows, N), codes(6, rows, K)
+    ws = torch.ones(1, N // 128, 1, device=DEV)
+    xq, xs = act(xc, 7)
+    dyq, ds = act(dc, 8)
+    y, dx = torch.empty(rows, N, device=DEV), torch.empty(rows, K, device=DEV)
+    qmv.qmv_b128_product(w, ws, 1, N, K, xq, rows, None, "f32", y)
+    qmv.qmv_b128_grad_x(w, ws, 1, N, K, dyq, rows, None, "f32", dx)
+    at = torch.tensor([0, 1, 129, N // 2, N - 130, N - 1], device=DEV)
+    assert torch.equal(y[:, at].double(), spread(xc, xs) @ values(w[0, at]).T)
+    dv, wv, want = spread(dc, ds), values(w[0]), torch.zeros(rows, K, dtype=torch.float64, device=DEV)
+    for n in range(0, N, 1 << 16):
+        want += dv[:, n:n + (1 << 16)] @ wv[n:n + (1 << 16)]
+    # terms of at most 18, of both signs: the sum of 2^20 wanders some 2^13, far below the 2^24 up to which fp32 is exact
+    assert want.abs().max() < 2.0 ** 20 and torch.equal(dx.double(), want)
+    dw = torch.empty(1, N, K, device=DEV)
+    qmv.qmv_b128_grad_w("bf16", values(dc).bfloat16(), N, values(xc).bfloat16(), K, 1, N, K, rows, None, "f32", dw)
+    assert torch.equal(dw[0, at].double(), values(dc[:, at]).T @ values(xc))
+    assert status_clean()
