@@ -460,9 +460,9 @@ namespace {
 // has a cluster of its own and it saves more than joining them costs. Measured, us: 1 x 7168 x 7168 (56 tiles) one rank
 // 20.8, two 14.3, three 13.3, five 12.6, clusters that take a second tile 16.7 and more; 64 x 2880 x 2880 five 8.2, six
 // 7.9, eight 9.2; 333 x 2880 of depth 1001 (8 steps) one 7.2, two 10.5; 64 x 2880 x 512 one 5.2, two 6.8.
-int few_splits(int64_t tiles, int steps) {
+int few_splits(int64_t tiles, int steps, int sms) {
   int splits = 1;
-  while (splits < kFewSplits && (splits + 1) * tiles <= kFewCtas * device_sm_count() && (splits + 1) * 2 <= steps) ++splits;
+  while (splits < kFewSplits && (splits + 1) * tiles <= kFewCtas * sms && (splits + 1) * 2 <= steps) ++splits;
   return (steps + splits - 1) / splits + kFewJoinSteps < steps ? splits : 1;
 }
 
@@ -500,6 +500,16 @@ cudaError_t few_go(const B128GemmArgs& a) {
   p.n_blocks = b128_blocks(a.N);
   p.steps = b128_blocks(depth);
   p.n_tiles = b128_blocks(p.out_n);
+  // tiles that there can be: every expert has at most one partial row tile
+  const int64_t row_tiles = a.n_experts == 1 ? (a.nrows + BN - 1) / BN : a.nrows / BN + hit_experts(a);
+  const int64_t tiles = row_tiles * p.n_tiles;
+  int splits = few_splits(tiles, p.steps, device_sm_count()), most = 0;
+  const auto quantizes = [&] {   // X: whether a CTA's rows are few enough
+    p.per_split = (p.steps + splits - 1) / splits;
+    const int64_t hit = hit_experts(a);
+    return p.per_split <= kFewQuantSteps && (a.nrows + hit - 1) / hit * p.per_split <= kFewQuantUnits;
+  };
+  if (kQuant && !quantizes()) return cudaErrorNotSupported;   // nothing is launched
   g_launch_stage = "cudaFuncSetAttribute";
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::smem(QMV_MAX_SORT_EXPERTS));
   if (e != cudaSuccess) return e;
@@ -520,10 +530,6 @@ cudaError_t few_go(const B128GemmArgs& a) {
     const cuuint32_t box[2] = {128, BN};
     if (!encode(&mx, 2, a.xq, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  // tiles that there can be: every expert has at most one partial row tile
-  const int64_t row_tiles = a.n_experts == 1 ? (a.nrows + BN - 1) / BN : a.nrows / BN + hit_experts(a);
-  const int64_t tiles = row_tiles * p.n_tiles;
-
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(F::threads);
   cfg.dynamicSmemBytes = F::smem(a.n_experts);
@@ -539,7 +545,6 @@ cudaError_t few_go(const B128GemmArgs& a) {
   cfg.numAttrs = 1;
   // The occupancy query counts one CTA an SM; two run (the fives of 56 tiles are 280 CTAs).
   static PerDevice clusters[kFewSplits + 1];   // of each size that run at once
-  int splits = few_splits(tiles, p.steps), most = 0;
   for (;; --splits) {
     attr[0].val.clusterDim.x = (unsigned)splits;
     g_launch_stage = "cudaOccupancyMaxActiveClusters";
@@ -552,12 +557,8 @@ cudaError_t few_go(const B128GemmArgs& a) {
     if (splits == 1 || most >= tiles) break;
   }
   if (most < 1) return cudaErrorInvalidConfiguration;
+  if (kQuant && (most < tiles || !quantizes())) return cudaErrorNotSupported;
   p.per_split = (p.steps + splits - 1) / splits;
-  if (kQuant) {
-    const int64_t hit = hit_experts(a);
-    const bool fits = most >= tiles && p.per_split <= kFewQuantSteps;
-    if (!fits || (a.nrows + hit - 1) / hit * p.per_split > kFewQuantUnits) return cudaErrorNotSupported;   // nothing is launched
-  }
   g_launch_stage = "launch";
   cfg.gridDim = dim3((unsigned)(splits * (tiles < most ? tiles : most)));
   cfg.numAttrs = a.stream != nullptr ? 2 : 1;
@@ -579,14 +580,14 @@ cudaError_t launch_b128_few_linear(const B128GemmArgs& a) {
 
 // By the CTAs' steps, alone or side by side, 2 or 2.5 ns a tile's step over the whole device, or reading the weights at 5.2
 // TB/s, as fitted to GB300; experts are taken as equally full, with half a tile more each.
-double b128_few_us(const B128GemmArgs& a, int depth, int out_n) {
+double b128_few_us(const B128GemmArgs& a, int depth, int out_n, int sms) {
   const int columns = few_columns(a), steps = b128_blocks(depth);
   const double hit = (double)hit_experts(a), each = a.nrows / hit / columns;
   const double row_tiles = a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
   const double tiles = row_tiles * b128_blocks(out_n);
-  const int splits = few_splits((int64_t)ceil(tiles), steps);
-  const double ctas = tiles * splits, step = columns < 64 ? 0.5 : ctas > device_sm_count() ? 0.68 : 0.4;   // us, of a CTA
-  const double chain = ceil(ctas / (kFewCtas * device_sm_count())) * ((steps + splits - 1) / splits) * step;
+  const int splits = few_splits((int64_t)ceil(tiles), steps, sms);
+  const double ctas = tiles * splits, step = columns < 64 ? 0.5 : ctas > sms ? 0.68 : 0.4;   // us, of a CTA
+  const double chain = ceil(ctas / (kFewCtas * sms)) * ((steps + splits - 1) / splits) * step;
   const double all = tiles * steps * (columns == 64 ? 2.5e-3 : 2e-3), read = hit * a.N * a.K / 5.2e6;
   return 4.0 + fmax(fmax(all, read), chain + (splits > 1 ? 2.5 : 0.0));
 }

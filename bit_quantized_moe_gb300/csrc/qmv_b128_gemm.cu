@@ -736,8 +736,8 @@ int first_half(int steps) { return (steps / 2 + 3) / 4 * 4; }
 // Whether two pairs share a tile's depth: where all run at once and it saves more than joining costs. Measured (one pair /
 // two, us): 256 x 7168 x 7168 27.6 / 21.8, 160 x 7168 x 16384 57 / 38, 1000 x 1024 x 4096 17.4 / 14.0, 256 x 8192 x 2880
 // 14.6 / 14.3, 256 x 8192 x 2048 11.8 / 12.2, 512 x 2880 x 1024 8.4 / 9.3. (Three and four took as long as two, or more.)
-bool pairs_split(int64_t tiles, int steps) {
-  return 2 * tiles <= device_sm_count() / 2 && first_half(steps) + kPairJoinSteps < steps;
+bool pairs_split(int64_t tiles, int steps, int sms) {
+  return 2 * tiles <= sms / 2 && first_half(steps) + kPairJoinSteps < steps;
 }
 
 template <int MODE>
@@ -759,7 +759,7 @@ cudaError_t product_go(const B128GemmArgs& a) {
   p.n_tiles = (p.out_n + kPairTile - 1) / kPairTile;
   const int64_t tiles = pair_tiles(a, p.out_n);
   p.per_split = first_half(p.steps);
-  auto* go = pairs_split(tiles, p.steps) ? pair_go<MODE, false, true> : pair_go<MODE, false, false>;
+  auto* go = pairs_split(tiles, p.steps, device_sm_count()) ? pair_go<MODE, false, true> : pair_go<MODE, false, false>;
   return go(p, tiles, a.xq, b128_row_bytes(depth), b128_row_bytes(depth), a.w,
                               (uint64_t)a.K, (uint64_t)a.K, a.stream);
 }
@@ -771,19 +771,20 @@ cudaError_t product_go(const B128GemmArgs& a) {
 //   256 x 7168 x 7168 39 / 21.8, 256 x 2880 x 2880 12.1 / 12.3, 333 x 1001 x 2880 9.9 / 14.5, 400 x 2880 x 2880 18.2 / 12.8,
 //   512 x 2880 x 1024 9.4 / 8.4; over 32 experts of 2880 x 2880: 1024 rows 53 / 73, 2048 rows 69 / 74, 4096 rows 106 / 75
 bool few_rows(const B128GemmArgs& a, int depth, int out_n) {
-  const int steps = b128_blocks(depth);
+  const int steps = b128_blocks(depth), sms = device_sm_count();
   const double hit = a.nrows < a.n_experts ? (double)a.nrows : (double)a.n_experts, each = a.nrows / hit / kPairTile;
   const double row_tiles = a.n_experts == 1 ? ceil(each) : hit * (each > 0.5 ? each + 0.5 : 1.0);
-  const double rounds = ceil(row_tiles * ((out_n + kPairTile - 1) / kPairTile) / (device_sm_count() / 2));
-  const double chain = pairs_split(pair_tiles(a, out_n), steps) ? first_half(steps) * 0.38 + 5.0 : rounds * steps * 0.38;
-  return b128_few_us(a, depth, out_n) < 5.5 + fmax(chain, hit * a.N * a.K / 4e6);
+  const double rounds = ceil(row_tiles * ((out_n + kPairTile - 1) / kPairTile) / (sms / 2));
+  const double chain = pairs_split(pair_tiles(a, out_n), steps, sms) ? first_half(steps) * 0.38 + 5.0 : rounds * steps * 0.38;
+  return b128_few_us(a, depth, out_n, sms) < 5.5 + fmax(chain, hit * a.N * a.K / 4e6);
 }
 
 }  // namespace
 
 cudaError_t launch_b128_product(const B128GemmArgs& a) { return few_rows(a, a.K, a.N) ? launch_b128_few(a, false) : product_go<kModeY>(a); }
 cudaError_t launch_b128_linear(const B128GemmArgs& a) {
-  if (few_rows(a, a.K, a.N)) {
+  const bool few = few_rows(a, a.K, a.N);
+  if (few) {
     const cudaError_t e = launch_b128_few_linear(a);
     if (e != cudaErrorNotSupported) return e;
     g_launch_stage = "launch";
@@ -797,7 +798,7 @@ cudaError_t launch_b128_linear(const B128GemmArgs& a) {
   q.xq = const_cast<void*>(a.xq);
   q.stream = a.stream;
   const cudaError_t e = launch_quantize_b128(q);
-  return e != cudaSuccess ? e : launch_b128_product(a);
+  return e != cudaSuccess ? e : few ? launch_b128_few(a, false) : product_go<kModeY>(a);
 }
 cudaError_t launch_b128_grad_x(const B128GemmArgs& a) { return few_rows(a, a.N, a.K) ? launch_b128_few(a, true) : product_go<kModeDx>(a); }
 

@@ -251,8 +251,8 @@ cudaError_t launch_b128_linear(const B128GemmArgs& a);
 cudaError_t launch_b128_grad_x(const B128GemmArgs& a);
 // Few rows of an expert (qmv_b128_few.cu); dx: grad_x.
 cudaError_t launch_b128_few(const B128GemmArgs& a, bool dx);
-// An estimate of its time, us.
-double b128_few_us(const B128GemmArgs& a, int depth, int out_n);
+// An estimate of its time on a device with so many SMs, us.
+double b128_few_us(const B128GemmArgs& a, int depth, int out_n, int sms);
 // With the quantization of 16-bit rows in the same launch; cudaErrorNotSupported, and no launch, where that does not fit.
 cudaError_t launch_b128_few_linear(const B128GemmArgs& a);
 
