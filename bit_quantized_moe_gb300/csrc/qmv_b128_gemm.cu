@@ -70,8 +70,12 @@ constexpr uint32_t kParkBytes = kEpiWarps * 32 * kParkPitch;
 constexpr int kPairJoinSteps = 9;      // steps that take as long as joining two pairs' sums
 constexpr int kJoinBytes = 32 * kHalf / 2 * 4;   // of half of a warp's sums
 static_assert(kEpiWarps * kJoinBytes <= kPairStages * kStageBytes, "the sums to join");
+// At least so much that no other kernel with tensor memory fits beside it on an SM (the smallest takes 10 KB): of a pair and
+// a cluster of another stream's kernel, each could wait on one SM for what the other holds on the next.
+constexpr size_t kPairSmemLeast = 219 * 1024;
 constexpr size_t pair_smem(int n_experts) {
-  return 1024 + (size_t)kPairStages * kStageBytes + kParkBytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
+  const size_t used = 1024 + (size_t)kPairStages * kStageBytes + kParkBytes + 2 * ((size_t)n_experts + 1) * sizeof(int);
+  return used < kPairSmemLeast ? kPairSmemLeast : used;
 }
 static_assert(pair_smem(QMV_MAX_SORT_EXPERTS) + 512 <= 227 * 1024, "shared memory");
 // Registers of an epilogue thread and of the others, within the 168 a thread that the launch gives. (Any spilled register
