@@ -2,6 +2,7 @@
 // and their weights, the balance loss with the slots of each expert, and the
 // gradient of both.
 #include <type_traits>
+#include <utility>
 
 #include <cooperative_groups.h>
 
@@ -268,6 +269,9 @@ __global__ void __launch_bounds__(kFinishCols * kFinishGroups) balance_finish_ke
   __shared__ float scratch[32], loss_parts[8];
   __shared__ int live_tokens;
   cg::cluster_group cluster = cg::this_cluster();
+  // A CTA may write to another's shared memory only once that one runs: each says so here and waits for the others behind
+  // its sums, so that the barrier is out of the loads' way.
+  auto running = cluster.barrier_arrive();
   const int E = a.n_experts;
   const int c = threadIdx.x % kFinishCols, group = threadIdx.x / kFinishCols;
   const int e = (int)blockIdx.x * kFinishCols + c;
@@ -306,6 +310,7 @@ __global__ void __launch_bounds__(kFinishCols * kFinishGroups) balance_finish_ke
     part = T > 0 ? (float)n / ((float)a.top_k * (float)T) * mean : 0.0f;
   }
   part = block_sum(part, scratch);
+  cluster.barrier_wait(std::move(running));
   if (threadIdx.x == 0) cluster.map_shared_rank(loss_parts, 0)[cluster.block_rank()] = part;
   cluster.sync();
   if (cluster.block_rank() == 0 && threadIdx.x == 0) {
