@@ -1,7 +1,8 @@
 // qmv_train_api.cpp -- the C ABI (include/qmv.h) of the router with its balance
 // loss, and of the products with a scale for each block of 128, with their
 // gradients: argument checks and dispatch to the launchers. Nothing here reads
-// device memory or synchronizes.
+// device memory or synchronizes. Without rows (an empty tensor's address is
+// NULL) only what does not depend on them has to be there.
 #include <cmath>
 #include <cstring>
 
@@ -60,7 +61,7 @@ int product_args(const void* w, const float* w_scales, int n_experts, int N, int
   QMV_TRY(check_matrix(n_experts, N, K, offsets, name));
   QMV_TRY(check_type(out_type, name));
   QMV_TRY(check_rows(nrows, name));
-  if (any_null(w, w_scales, xq, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (any_null(w, w_scales) || (nrows > 0 && any_null(xq, y))) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(w, w_scales, xq, y, offsets))
     return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const size_t need = b128_act_bytes(nrows, D);
@@ -94,7 +95,7 @@ int qmv_moe_router(int32_t type, const void* logits, int64_t ldl, const uint8_t*
   const char* name = "qmv_moe_router";
   QMV_TRY(check_router(type, ldl, ntok, n_experts, top_k, score, name));
   QMV_TRY(check_scale(scale, name));
-  if (any_null(logits, ids, weights)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (ntok > 0 && any_null(logits, ids, weights)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(logits, live, ids, weights))
     return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (ntok == 0) return done();
@@ -126,7 +127,8 @@ int qmv_moe_balance(int32_t type, const void* logits, int64_t ldl, const uint8_t
                     void* workspace, size_t workspace_bytes, void* stream) {
   const char* name = "qmv_moe_balance";
   QMV_TRY(check_router(type, ldl, ntok, n_experts, top_k, score, name));
-  if (any_null(logits, ids, counts, means, loss, workspace)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (any_null(counts, means, loss, workspace) || (ntok > 0 && any_null(logits, ids)))
+    return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(logits, live, ids, counts, means, loss, workspace))
     return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const BalanceSpace s = balance_space(ntok, n_experts);
@@ -159,7 +161,7 @@ int qmv_moe_router_grad(int32_t type, const void* logits, int64_t ldl, const uin
   QMV_TRY(check_router(type, ldl, ntok, n_experts, top_k, score, name));
   QMV_TRY(check_ld(ldd, n_experts, name));
   QMV_TRY(check_scale(scale, name));
-  if (any_null(logits, dlogits) || (dweights != nullptr && ids == nullptr) || (counts == nullptr) != (dloss == nullptr))
+  if ((ntok > 0 && (any_null(logits, dlogits) || (dweights != nullptr && ids == nullptr))) || (counts == nullptr) != (dloss == nullptr))
     return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(logits, live, ids, dweights, counts, dloss, dlogits))
     return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
@@ -194,8 +196,8 @@ size_t qmv_act_b128_scale_offset(int32_t nrows, int32_t K) {
 
 int qmv_act_b128_unpack(const void* xq, int32_t nrows, int32_t K, uint8_t* codes, float* scales) {
   const char* name = "qmv_act_b128_unpack";
-  if (any_null(xq, codes, scales)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (!act_shape(nrows, K)) return record_error(QMV_ESHAPE, "%s: %d rows, K=%d", name, nrows, K);
+  if (nrows > 0 && any_null(xq, codes, scales)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   const uint8_t* src = static_cast<const uint8_t*>(xq);
   const uint8_t* words = src + b128_scale_offset(nrows, K);
   const size_t blocks = (size_t)b128_blocks(K);
@@ -213,7 +215,7 @@ int qmv_quantize_act_b128(int32_t type, const void* x, int64_t ldx, int32_t nrow
   QMV_TRY(check_rows(nrows, name));
   QMV_TRY(check_width(K, false, name, QMV_MAX_N));
   QMV_TRY(check_ld(ldx, K, name));
-  if (any_null(x, xq)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (nrows > 0 && any_null(x, xq)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x, xq)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const size_t need = b128_act_bytes(nrows, K);
   if (xq_bytes < need) return record_error(QMV_ESIZE, "%s: output %zu bytes < %zu", name, xq_bytes, need);
@@ -263,7 +265,7 @@ int qmv_b128_linear(const void* w, const float* w_scales, int32_t n_experts, int
   B128GemmArgs g;
   QMV_TRY(product_args(w, w_scales, n_experts, N, K, workspace, workspace_bytes, K, nrows, offsets, type, y, stream, name, g));
   QMV_TRY(check_ld(ldx, K, name));
-  if (any_null(x)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (nrows > 0 && any_null(x)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (nrows == 0) return done();
   g.x = x;
@@ -293,7 +295,7 @@ int qmv_b128_grad_w(int32_t type, const void* dy, int64_t ld_dy, const void* x, 
   QMV_TRY(check_ld(ld_dy, N, name));
   QMV_TRY(check_ld(ldx, K, name));
   if (ld_dy % 8 || ldx % 8) return record_error(QMV_ESHAPE, "%s: row strides must be multiples of 8", name);
-  if (any_null(dy, x, dw)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (any_null(dw) || (nrows > 0 && any_null(dy, x))) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(dy, x, offsets, dw)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (nrows == 0) {   // the sum over no rows
     g_launch_stage = "cudaMemsetAsync";

@@ -422,7 +422,8 @@ int qmv_moe_layer_noalloc(const qmv_wdesc* gate_up_desc, const void* w_gate_up_d
  * packed weights. (The MX products' input gradients are not among them; those of
  * the products with a scale for each block of 128 are.) Rows and slots up to QMV_MAX_ROWS; a call with no
  * rows (or no tokens) is valid and writes nothing (qmv_moe_sort: offsets of
- * zero). Rows of a strided operand are `ld` elements apart (ld >= the row's
+ * zero; qmv_moe_balance and qmv_b128_grad_w: zeros), and its pointers to rows, slots
+ * and buffers of rows may be NULL. Rows of a strided operand are `ld` elements apart (ld >= the row's
  * width); the others are contiguous.
  * ---------------------------------------------------------------------------
  */
