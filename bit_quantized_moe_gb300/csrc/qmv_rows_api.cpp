@@ -1,6 +1,7 @@
 // qmv_rows_api.cpp -- the many-row part of the C ABI (include/qmv.h): argument
 // checks and dispatch to the launchers. Nothing here reads device memory or
-// synchronizes.
+// synchronizes. Without rows (an empty tensor's address is NULL) only what does
+// not depend on them has to be there.
 #include <cmath>
 #include <cstring>
 
@@ -27,7 +28,7 @@ int product_args(const qmv_wdesc* desc, const void* w, const void* xq, size_t xq
     return record_error(QMV_EINVAL, "%s: a dense product needs n_experts == 1 (got %d)", name, desc->n_experts);
   if (desc->n_experts > QMV_MAX_SORT_EXPERTS)
     return record_error(QMV_EINVAL, "%s: %d experts > %d", name, desc->n_experts, QMV_MAX_SORT_EXPERTS);
-  if (any_null(w, xq, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (any_null(w) || (nrows > 0 && any_null(xq, y))) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(w, xq, y, offsets)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const size_t need = mx_act_bytes(desc->fmt, nrows, desc->K);
   if (xq_bytes < need) return record_error(QMV_ESIZE, "%s: activations %zu bytes < %zu", name, xq_bytes, need);
@@ -63,7 +64,7 @@ int route_args(int type, int ntok, int top_k, int K, int most, const int32_t* ro
   QMV_TRY(check_type(type, name));
   QMV_TRY(check_slots(ntok, top_k, name));
   QMV_TRY(check_width(K, false, name, most));
-  if (row_of_slot == nullptr) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (ntok > 0 && row_of_slot == nullptr) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (misaligned(row_of_slot)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   r = RouteArgs();
   r.type = type;
@@ -80,7 +81,7 @@ int return_rows(int type, const void* ys, bool ys_f32, const float* wide, const 
   RouteArgs r;
   QMV_TRY(route_args(type, ntok, top_k, N, QMV_MAX_N, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ldy, N, name));
-  if (any_null(ys, weights, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (ntok > 0 && any_null(ys, weights, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(ys, weights, y)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (ntok == 0) return done();
   r.rows = ys;
@@ -159,8 +160,9 @@ size_t qmv_act_mx_scale_offset(int32_t fmt, int32_t nrows, int32_t K) {
 
 int qmv_act_mx_unpack(int32_t fmt, const void* xq, int32_t nrows, int32_t K, uint8_t* codes, uint8_t* scales) {
   const char* name = "qmv_act_mx_unpack";
-  if (any_null(xq, codes, scales)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (!mx_shape(fmt, nrows, K)) return record_error(QMV_ESHAPE, "%s: format %d, %d rows, K=%d", name, fmt, nrows, K);
+  if (nrows == 0) return done();
+  if (any_null(xq, codes, scales)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   const uint8_t* src = static_cast<const uint8_t*>(xq);
   std::memcpy(codes, src, (size_t)nrows * mx_row_bytes(fmt, K));
   const uint8_t* words = src + mx_scale_offset(fmt, nrows, K);
@@ -179,7 +181,7 @@ int qmv_quantize_act_mx(int32_t fmt, int32_t type, const void* x, int64_t ldx, i
   QMV_TRY(check_rows(nrows, name));
   QMV_TRY(check_width(K, true, name));
   QMV_TRY(check_ld(ldx, K, name));
-  if (any_null(x, xq)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (nrows > 0 && any_null(x, xq)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x, xq)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const size_t need = mx_act_bytes(fmt, nrows, K);
   if (xq_bytes < need) return record_error(QMV_ESIZE, "%s: output %zu bytes < %zu", name, xq_bytes, need);
@@ -209,7 +211,7 @@ int qmv_rms_norm(int32_t type, const void* x, int64_t ldx, const void* res, int6
   QMV_TRY(check_ld(ldx, K, name));
   if (res != nullptr || sum != nullptr) QMV_TRY(check_ld(ldr, K, name));
   if (!(eps >= 0.0f) || std::isinf(eps)) return record_error(QMV_EINVAL, "%s: eps=%g", name, (double)eps);
-  if (any_null(x, gain, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (any_null(gain) || (nrows > 0 && any_null(x, y))) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x, res, gain, sum, y)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   size_t need = (size_t)nrows * K * (type == QMV_F32 ? 4 : 2);
   if (out == QMV_NORM_MXFP8 || out == QMV_NORM_MXFP4) {
@@ -269,7 +271,7 @@ int qmv_moe_sort(const int32_t* ids, int32_t ntok, int32_t top_k, int32_t n_expe
   QMV_TRY(check_slots(ntok, top_k, name));
   if (n_experts < 1 || n_experts > QMV_MAX_SORT_EXPERTS)
     return record_error(QMV_EINVAL, "%s: n_experts=%d outside [1, %d]", name, n_experts, QMV_MAX_SORT_EXPERTS);
-  if (any_null(ids, offsets, row_of_slot, slot_of_row)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (any_null(offsets) || (ntok > 0 && any_null(ids, row_of_slot, slot_of_row))) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(ids, offsets, row_of_slot, slot_of_row, workspace))
     return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const size_t need = qmv_moe_sort_workspace_bytes(ntok, top_k, n_experts);
@@ -292,7 +294,7 @@ int qmv_moe_dispatch(int32_t type, const void* x, int64_t ldx, int32_t ntok, int
   RouteArgs r;
   QMV_TRY(route_args(type, ntok, top_k, K, QMV_MAX_K, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ldx, K, name));
-  if (any_null(x, xs)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (ntok > 0 && any_null(x, xs)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x, xs)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (ntok == 0) return done();
   r.tok = x;
@@ -310,7 +312,7 @@ int qmv_moe_dispatch_mx(int32_t fmt, int32_t type, const void* x, int64_t ldx, i
   QMV_TRY(route_args(type, ntok, top_k, K, QMV_MAX_K, row_of_slot, stream, name, r));
   QMV_TRY(check_width(K, true, name));
   QMV_TRY(check_ld(ldx, K, name));
-  if (any_null(x, xq)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (ntok > 0 && any_null(x, xq)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(x, xq)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const int64_t slots = (int64_t)ntok * top_k;
   const size_t need = mx_act_bytes(fmt, slots, K);
@@ -339,7 +341,7 @@ int qmv_moe_dispatch_grad(int32_t type, const void* dxs, int32_t ntok, int32_t t
   RouteArgs r;
   QMV_TRY(route_args(type, ntok, top_k, K, QMV_MAX_K, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ldx, K, name));
-  if (any_null(dxs, dx)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (ntok > 0 && any_null(dxs, dx)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(dxs, dx)) return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (ntok == 0) return done();
   r.rows = dxs;
@@ -361,7 +363,7 @@ int qmv_moe_return_grad(int32_t type, const void* dy, int64_t ld_dy, const void*
   RouteArgs r;
   QMV_TRY(route_args(type, ntok, top_k, N, QMV_MAX_N, row_of_slot, stream, name, r));
   QMV_TRY(check_ld(ld_dy, N, name));
-  if (any_null(dy, ys, weights, dys, dweights)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (ntok > 0 && any_null(dy, ys, weights, dys, dweights)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(dy, ys, weights, dys, dweights))
     return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   if (ntok == 0) return done();
@@ -387,7 +389,7 @@ int qmv_moe_prefill_layer(const qmv_wdesc* gu, const void* w_gu, const qmv_wdesc
   QMV_TRY(check_layer(gu, down, ntok, top_k, name));
   if (type != QMV_BF16 && type != QMV_F16) return record_error(QMV_EINVAL, "%s: bf16 or fp16 only (type %d)", name, type);
   QMV_TRY(check_ld(ldx, gu->K, name));
-  if (any_null(w_gu, w_down, x, ids, weights, ws, y)) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
+  if (any_null(w_gu, w_down, ws) || (ntok > 0 && any_null(x, ids, weights, y))) return record_error(QMV_EINVAL, "%s: NULL pointer", name);
   if (any_misaligned(w_gu, w_down, x, ids, weights, ws, y))
     return record_error(QMV_EALIGN, "%s: pointers must be 16-byte aligned", name);
   const int64_t slots = (int64_t)ntok * top_k;

@@ -78,6 +78,76 @@ def test_what_does_not_depend_on_the_rows_is_still_needed():
     assert lib.qmv_moe_router(0, None, E - 1, None, 0, E, TOP_K, 0, 0, 1.0, None, None, 0) == -2
 
 
+def rows_calls(device, stream=None):
+    """(name, call) of the other calls of many rows that enqueue nothing."""
+    one, four = (qmv.wdesc("mxfp4", N, K, n) for n in (1, E))
+    gate, down = qmv.wdesc("mxfp4", N, K, E), qmv.wdesc("mxfp8", K, N, E)
+    w = torch.zeros(16, dtype=torch.uint8, device=device)   # stands for packed weights: not read
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=device)
+
+    def new(*shape, dtype=torch.bfloat16):
+        return rows(*shape, dtype=dtype, device=device)
+
+    def act(fmt, columns):
+        return space(qmv.qmv_act_mx_bytes(fmt, 0, columns), device)
+
+    def row():
+        return new(0, TOP_K, dtype=torch.int32)
+
+    def weights():
+        return new(0, TOP_K, dtype=torch.float32)
+
+    return [
+        ("quantize", lambda: qmv.qmv_quantize_act_mx("mxfp8", "bf16", new(0, K), K, 0, K, act("mxfp8", K), stream)),
+        ("norm", lambda: qmv.qmv_rms_norm("bf16", new(0, K), K, new(0, K), K, torch.zeros(K, dtype=torch.bfloat16, device=device), 0, K,
+                                          1e-5, new(0, K), "plain", new(0, K), stream)),
+        ("norm to q8", lambda: qmv.qmv_rms_norm("bf16", new(0, K), K, None, K, torch.zeros(K, dtype=torch.bfloat16, device=device), 0, K,
+                                                1e-5, None, "q8", space(0, device), stream)),
+        ("product", lambda: qmv.qmv_mx_product(four, w, act("mxfp4", K), 0, offsets, "bf16", new(0, N), stream)),
+        ("dense product", lambda: qmv.qmv_mx_product(one, w, act("mxfp4", K), 0, None, "f32", new(0, N, dtype=torch.float32), stream)),
+        ("gate and up", lambda: qmv.qmv_mx_gate_up_swiglu(gate, w, act("mxfp4", K), 0, offsets, "mxfp8", act("mxfp8", N), stream)),
+        ("dispatch", lambda: qmv.qmv_moe_dispatch("bf16", new(0, K), K, 0, TOP_K, K, row(), new(0, K), stream)),
+        ("dispatch_mx", lambda: qmv.qmv_moe_dispatch_mx("mxfp4", "bf16", new(0, K), K, 0, TOP_K, K, row(), act("mxfp4", K), stream)),
+        ("dispatch_grad", lambda: qmv.qmv_moe_dispatch_grad("bf16", new(0, K), 0, TOP_K, K, row(), new(0, K), K, stream)),
+        ("return", lambda: qmv.qmv_moe_return("bf16", new(0, N), weights(), 0, TOP_K, N, row(), new(0, N), N, stream)),
+        ("return_grad", lambda: qmv.qmv_moe_return_grad("bf16", new(0, N), N, new(0, N), weights(), 0, TOP_K, N, row(), new(0, N),
+                                                        weights(), stream)),
+        ("layer", lambda: qmv.qmv_moe_prefill_layer(gate, w, down, w, "bf16", new(0, K), K, row(), weights(), 0, TOP_K,
+                                                    space(qmv.qmv_moe_prefill_layer_workspace_bytes(gate, down, 0, TOP_K), device),
+                                                    new(0, K), stream)),
+    ]
+
+
+@pytest.mark.parametrize("name", [name for name, _ in rows_calls("cpu")])
+def test_calls_of_many_rows(name):
+    dict(rows_calls("cpu", 0))[name]()
+
+
+def test_mx_unpack():
+    assert qmv.lib.qmv_act_mx_unpack(0, None, 0, 64, None, None) == 0
+    assert qmv.lib.qmv_act_mx_unpack(0, None, 1, 64, None, None) == qmv.QMV_EINVAL
+
+
+def test_calls_of_many_rows_still_need_the_rest():
+    lib, P, by = qmv.lib, 1 << 40, qmv.ctypes.byref
+    four = qmv.wdesc("mxfp4", N, K, E)
+    assert lib.qmv_mx_product(by(four), None, None, 0, 0, P, 0, None, 0) == -1
+    assert lib.qmv_mx_product(by(four), P, None, 0, 0, None, 0, None, 0) == -1   # rows of four experts need offsets
+    assert lib.qmv_rms_norm(0, None, K, None, K, None, 0, K, 1e-5, None, 0, None, 0, 0) == -1   # the gain
+    assert lib.qmv_moe_sort(None, 0, TOP_K, E, None, None, None, None, 0, 0) == -1   # written all the same
+    assert lib.qmv_moe_prefill_layer(by(four), P, by(qmv.wdesc("mxfp4", K, N, E)), P, 0, None, K, None, None, 0, TOP_K, None, 0, None, 0) == -1
+
+
+@pytest.mark.gpu
+def test_calls_of_many_rows_on_a_gpu():
+    for name, call in rows_calls("cuda"):
+        call()
+    offsets = torch.full((E + 1,), 7, dtype=torch.int32, device="cuda")
+    ids, row, slot = (rows(0, TOP_K, dtype=torch.int32, device="cuda") for _ in range(3))
+    qmv.qmv_moe_sort(ids, 0, TOP_K, E, offsets, row, slot)
+    assert not offsets.any() and qmv.qmv_device_status() == 0
+
+
 @pytest.mark.gpu
 def test_router_and_block_products_on_a_gpu():
     """The same on the device, and what is written without rows: the loss's zeros, the weights' gradient of zeros."""
