@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_grad_kernel(RouterGradA
         }
       }
     }
+    __syncwarp();   // out may be the logits: every lane has read its slot's, which another lane writes
     T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {

@@ -72,3 +72,25 @@ def test_loss_of_parts_of_several_ctas(experts, tokens, score):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for got in again for a, b in zip(first, got))
     assert status_clean()
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_in_the_place_of_padded_strided_logits(score, renorm, dtype):
+    """The logits' own place, rows further apart than they are wide, padding, and experts named twice, so that a lane's logit is
+    read by many and overwritten by one: the bits of a call with a place of its own, and nothing between the rows."""
+    tokens, top_k = 4000, 8
+    g = qi.rng(21)
+    for experts, ld in ((33, 40), (256, 257), (1000, 1024)):
+        rows = dev(g.standard_normal((tokens, ld)).astype(np.float32)).to(dtype)
+        ids = dev(g.integers(0, experts, size=(tokens, 1)) + g.integers(0, 3, size=(tokens, top_k))).to(torch.int32)   # some past the experts
+        live = dev(g.random(tokens) < 0.9)
+        dw, dl, counts = dev(g.standard_normal((tokens, top_k)).astype(np.float32)), torch.full((1,), 0.5, device=DEV), torch.zeros(experts + 1, dtype=torch.int32, device=DEV)
+        counts[:-1], counts[-1] = torch.bincount(ids[ids < experts], minlength=experts), tokens
+        own, place = torch.full_like(rows, 7.0), rows.clone()
+        for out in (own, place):
+            qmv.qmv_moe_router_grad(dtype, place, ld, live, ids, dw, counts, dl, tokens, experts, top_k, score, renorm, 1.5, out, ld)
+        assert torch.equal(own[:, :experts], place[:, :experts])
+        assert torch.equal(place[:, experts:], rows[:, experts:]) and (own[:, experts:] == 7.0).all()
+        assert not place[~live, :experts].any()
+    assert status_clean()
