@@ -6,7 +6,10 @@ a = (4 + 3.4 R) * 2^-24. A sigmoid adds another exponential, at most half of its
 A score's share divides two such numbers, of which the lower is a sum (E / 32 additions in a lane and five levels), by a
 reciprocal and a product: 3 a + (E / 32 + 12) * 2^-24. A mean of T shares adds its longest chain of additions, at most
 T / 16 + 80 of them; the loss the fraction's and the product's four roundings and the additions of at most 18 numbers in a row.
-Numbers below 2^-126 may be lost whole: 2^-120 is added."""
+A gradient's terms are products of at most three such numbers b, one of them behind a sum over the experts, with the fraction
+and the loss's factor of three roundings each and the additions of the two parts: 3 b + (E / 32 + 24) * 2^-24 of the sum of their
+magnitudes. Numbers below 2^-126 may be lost whole: 2^-120 is added. An output of 16 bits is the fp32 result rounded to
+nearest (assert_within)."""
 import numpy as np
 import pytest
 import torch
@@ -17,6 +20,8 @@ import train_reference as tr  # noqa: E402
 from qmv_testutil import DEV, assert_within, status_clean  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+
+MODES = [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)]
 
 
 def dev(a):
@@ -74,7 +79,7 @@ def test_loss_of_parts_of_several_ctas(experts, tokens, score):
     assert status_clean()
 
 
-@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("score,renorm", MODES)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_gradient_in_the_place_of_padded_strided_logits(score, renorm, dtype):
     """The logits' own place, rows further apart than they are wide, padding, and experts named twice, so that a lane's logit is
@@ -93,4 +98,33 @@ def test_gradient_in_the_place_of_padded_strided_logits(score, renorm, dtype):
         assert torch.equal(own[:, :experts], place[:, :experts])
         assert torch.equal(place[:, experts:], rows[:, experts:]) and (own[:, experts:] == 7.0).all()
         assert not place[~live, :experts].any()
+    assert status_clean()
+
+
+@pytest.mark.parametrize("score,renorm", MODES)
+@pytest.mark.parametrize("spread", [1.0, 8.0, 30.0, 70.0])
+def test_scores_of_logits_far_apart(score, renorm, spread):
+    """Weights, means, loss and gradient where exponentials have arguments of hundreds."""
+    tokens, experts, top_k = 300, 48, 6
+    l = logits(int(spread), tokens, experts, spread)
+    l[0] = -200 + np.arange(experts) % 3
+    l[1] = 200 - np.arange(experts) % 7
+    l[2] = np.where(np.arange(experts) % 2, -100, 100)
+    ld, l64, live = dev(l), l.astype(np.float64), np.ones(tokens, bool)
+    ids, w = torch.empty(tokens, top_k, dtype=torch.int32, device=DEV), torch.empty(tokens, top_k, device=DEV)
+    qmv.qmv_moe_router("f32", ld, experts, None, tokens, experts, top_k, score, renorm, 2.5, ids, w)
+    want_ids, want = tr.route(l64, live, top_k, score, renorm, 2.5)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    b = share_error(l64, experts)
+    assert_within(host(w), want, b * want + 2.0 ** -120, "f32", "weights")
+    counts, means, loss = balance(ld, ids, top_k, score)
+    wc, wm, wl = tr.balance(l64, live, want_ids, top_k, score)
+    assert np.array_equal(counts.cpu().numpy(), wc)
+    c = share_error(l64, experts, tokens / 16 + 80)
+    assert_within(host(means), wm, c * wm + 2.0 ** -120, "f32", "means")
+    assert_within(host(loss)[0], wl, (c + 22 * 2.0 ** -24) * wl, "f32", "loss")
+    dw, dl, d = dev(qi.rng(5).standard_normal((tokens, top_k)).astype(np.float32)), torch.full((1,), 0.37, device=DEV), torch.empty_like(ld)
+    qmv.qmv_moe_router_grad("f32", ld, experts, None, ids, dw, counts, dl, tokens, experts, top_k, score, renorm, 2.5, d, experts)
+    wd, size = tr.router_grad(l64, live, want_ids, host(dw), wc, host(dl)[0], top_k, score, renorm, 2.5)
+    assert_within(host(d), wd, (3 * b + (experts / 32 + 24) * 2.0 ** -24) * size + 2.0 ** -120, "f32", "dlogits")
     assert status_clean()
