@@ -625,7 +625,7 @@ int qmv_moe_router(int32_t type, const void* logits_dev, int64_t ldl, const uint
  *   loss [1]                 fp32
  * Sums are fp32 in a fixed order. A call without tokens writes zeros.
  * workspace: qmv_moe_balance_workspace_bytes(...) bytes of device scratch; calls that
- * share one must be ordered on one stream. Two launches.
+ * share one must be ordered on one stream. One launch for up to 64 tokens, two for more.
  * Errors: QMV_EINVAL, QMV_ESHAPE, QMV_EALIGN, QMV_ESIZE, QMV_ECUDA.
  */
 size_t qmv_moe_balance_workspace_bytes(int32_t ntok, int32_t n_experts);
